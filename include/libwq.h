@@ -509,6 +509,95 @@ int wq_kv_quantize(const void* X, int x_dtype, int64_t T, int64_t hd, const int3
 int wq_kv_dequant(const uint8_t* codes, const uint16_t* s_f16, const uint8_t* zpacked, int64_t T, int64_t hd,
                   const int32_t* slot, int64_t S, int out_dtype, void* out, void* stream);
 
+/* ---- Attention next to the INT4 KV cache --------------------------------------
+ * The operators on either side of the cache: the norm and rotation that make
+ * the queries and keys, the attention over a prompt whose keys and values are
+ * then quantized (wq_kv_quantize), and the attention that reads the cache.
+ * dtype is WQ_BF16 or WQ_F16 for every 16-bit tensor of a call.  Heads: Hq
+ * query heads and Hkv key / value heads of D values (D = 64, 128 or 256), Hq a
+ * multiple of Hkv; query head h reads KV head h / (Hq / Hkv).  Query, key and
+ * value tensors are [T][heads][D] with the heads and values of a token
+ * contiguous and a stride (in values, at least heads * D, a multiple of 8)
+ * from token to token, so slices of one fused projection can be passed; they are 16-byte
+ * aligned.  T == 0 (or B == 0) enqueues nothing.  Errors: WQ_EINVAL for a NULL
+ * pointer, a bad size, dtype, scale or eps; WQ_EUNSUPPORTED for a head size, head
+ * count, rotation or page size outside the above and below; WQ_EALIGN for
+ * misaligned pointers or strides.  All three are deterministic and can be
+ * captured into graphs. */
+
+/* Norm of every query and key head and the rotation of its position, in one
+ * pass: for a head row x of token t,
+ *   n = x / sqrt(mean(x^2) + eps) * w   (w: q_weight or k_weight [D], or NULL for ones)
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for the rot / 2 pairs of its first
+ *   rot values (pair i: values i and i + rot/2, or 2i and 2i + 1 when
+ *   interleaved is 1), cos and sin being row positions[t] of the fp32 tables
+ *   [P][rot / 2]; values rot.. are left at n.
+ * fp32 arithmetic, one rounding to dtype at the end.  A token whose position
+ * lies outside [0, P) is padding: its output rows are left as they were.  rot: a
+ * positive multiple of 16, at most D.  eps finite and not negative.
+ *   positions  device int32 [T], 4-byte aligned; cos, sin 16-byte aligned,
+ *              weights 8-byte aligned
+ *   q_out, k_out  [T][heads][D] with their own token strides; an output may be
+ *              its input (same pointer and stride), other overlaps are not allowed */
+int wq_qk_norm_rope(const void* q, const void* k, int dtype, int64_t T, int Hq, int Hkv, int D, int64_t q_stride,
+                    int64_t k_stride, const void* q_weight, const void* k_weight, float eps, const int32_t* positions,
+                    const float* cos, const float* sin, int64_t P, int rot, int interleaved, void* q_out, void* k_out,
+                    int64_t q_out_stride, int64_t k_out_stride, void* stream);
+
+/* Causal attention over B prompts packed one after another: sequence b holds
+ * tokens seq_starts[b] .. seq_starts[b + 1] - 1 (device int32 [B + 1], 4-byte
+ * aligned, increasing; the lengths are read on the device and may be 0), and
+ *   out[i] = sum_{t <= i} softmax_t(scale * q_i . k_t) v_t
+ * over the tokens t of i's own sequence.  Scores and sums in fp32; the softmax
+ * weights are rounded to dtype for the product with v; one rounding at the end.
+ * out [T][Hq][D] contiguous (16-byte aligned); lse, if not NULL, fp32 [T][Hq]:
+ * log sum_t exp(scale * q.k_t).  Tokens outside every sequence keep what out
+ * and lse held there.  scale finite and positive. */
+int wq_prompt_attention(const void* q, const void* k, const void* v, int dtype, int64_t T, int Hq, int Hkv, int D,
+                        int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t B, const int32_t* seq_starts,
+                        float scale, void* out, float* lse, void* stream);
+
+/* Attention over the INT4 KV cache.  The K and the V cache have S rows of
+ * hd = Hkv * D values each (a multiple of 128; arrays as wq_kv_quantize writes
+ * them, codes 16-byte aligned), shared by B sequences in pages of page_size rows
+ * (a power of two up to S): token t of sequence b lies in row
+ *   block_table[b][t / page_size] * page_size + t % page_size
+ * (device int32 [B][table_width]; a page number outside [0, S / page_size) marks
+ * tokens that are not attended).  context_lens[b] (device int32 [B]) counts the
+ * sequence's cached tokens, those of this call's queries included; at most
+ * max_context (<= table_width * page_size) are attended.
+ *   Queries: one per sequence (q_starts NULL, T == B, max_queries 1), or those
+ * of sequence b at q_starts[b] .. q_starts[b + 1] - 1 (device int32 [B + 1],
+ * increasing; at most max_queries of each are computed).  The n queries of a
+ * sequence are its last n tokens: query i sees tokens t <= context_len - n + i.
+ *   out[i] = sum_t softmax_t(scale * q_i . k_t) v_t with k and v decoded
+ * exactly as s * (q - z); scores and sums in fp32; a softmax weight times its
+ * token's V scale is rounded to fp16 for the product with the integers q - z;
+ * one rounding at the end.  A query that sees no token gets zeros (lse: -inf).
+ * out [T][Hq][D] contiguous, 16-byte aligned; lse as above (or NULL); rows of T
+ * outside every sequence keep what they held.  scale finite and positive.
+ *   workspace  wq_kv_attention_workspace_bytes bytes, 256-byte aligned, for
+ * the partial results of contexts split across workgroups; its content needs
+ * no initialisation and is not used after the call's work, so calls ordered on
+ * one stream may share it, concurrent ones (graphs included) may not.
+ * WQ_EWORKSPACE when missing or too small.  Preconditions: finite scales and
+ * block contents in attended rows. */
+int wq_kv_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D, int64_t q_stride,
+                    const uint8_t* k_codes, const uint16_t* k_s_f16, const uint8_t* k_zpacked, const uint8_t* v_codes,
+                    const uint16_t* v_s_f16, const uint8_t* v_zpacked, int64_t S, int64_t B,
+                    const int32_t* block_table, int64_t table_width, int page_size, const int32_t* context_lens,
+                    int64_t max_context, const int32_t* q_starts, int64_t max_queries, float scale, void* out,
+                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of that call (0: none needed, or sizes it would refuse).
+ * Host-only. */
+size_t wq_kv_attention_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size,
+                                       int64_t max_context, int64_t max_queries);
+
+/* Names the kernel instance and launch shape of that call (as wq_gemm_plan). */
+int wq_kv_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size, int64_t max_context,
+                         int64_t max_queries, char* buf, size_t buf_len);
+
 /* ---- Streaming-read probe (a measurement aid, not a step of the method) -----
  * A decode product's time is the reading of its weights ("Hardware, formats
  * and the roofline": decode is bound by memory bandwidth), so the rate at which

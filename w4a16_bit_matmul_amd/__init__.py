@@ -60,6 +60,8 @@ EXPORTED = (
     "wq_layout_bytes_w8", "wq_quantize_w8", "wq_pack_int8", "wq_dequant_w8", "wq_gemm_w8a16_workspace_bytes",
     "wq_gemm_w8a16", "wq_gemm_w8a16_ex", "wq_gemm_w8a16_plan",
     "wq_kv_layout_bytes", "wq_kv_quantize", "wq_kv_dequant",
+    "wq_qk_norm_rope", "wq_prompt_attention", "wq_kv_attention", "wq_kv_attention_workspace_bytes",
+    "wq_kv_attention_plan",
     "wq_quantize_groups_scaled", "wq_scale_activations", "wq_channel_absmean",
     "wq_layout_bytes_mxfp4", "wq_quantize_mxfp4", "wq_pack_mxfp4", "wq_dequant_mxfp4",
     "wq_gemm_mxfp4_workspace_bytes", "wq_gemm_mxfp4", "wq_gemm_mxfp4_ex", "wq_gemm_mxfp4_plan",
@@ -86,7 +88,7 @@ def lib() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is missing: build it first (python __graft_entry__.py or "
                           f"python w4a16_bit_matmul_amd/_build.py)")
     L = ctypes.CDLL(LIB_PATH)
-    P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+    P, I, I64, SZ, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     sig = {
         "wq_version": (I, []),
         "wq_strerror": (ctypes.c_char_p, [I]),
@@ -113,6 +115,12 @@ def lib() -> ctypes.CDLL:
         "wq_kv_layout_bytes": (I, [I64, I64, ctypes.POINTER(SZ), ctypes.POINTER(SZ), ctypes.POINTER(SZ)]),
         "wq_kv_quantize": (I, [P, I, I64, I64, P, I64, P, P, P, P]),
         "wq_kv_dequant": (I, [P, P, P, I64, I64, P, I64, I, P, P]),
+        "wq_qk_norm_rope": (I, [P, P, I, I64, I, I, I, I64, I64, P, P, F, P, P, P, I64, I, I, P, P, I64, I64, P]),
+        "wq_prompt_attention": (I, [P, P, P, I, I64, I, I, I, I64, I64, I64, I64, P, F, P, P, P]),
+        "wq_kv_attention": (I, [P, I, I64, I, I, I, I64, P, P, P, P, P, P, I64, I64, P, I64, I, P, I64, P, I64, F, P,
+                                P, P, SZ, P]),
+        "wq_kv_attention_workspace_bytes": (SZ, [I64, I, I, I, I64, I, I64, I64]),
+        "wq_kv_attention_plan": (I, [I64, I, I, I, I64, I, I64, I64, ctypes.c_char_p, SZ]),
         "wq_quantize_groups_scaled": (I, [P, I, I64, I64, I, I, P, P, P, P, P, P, P]),
         "wq_scale_activations": (I, [P, I64, I64, P, P, P]),
         "wq_channel_absmean": (I, [P, I64, I64, P, P]),
@@ -487,6 +495,196 @@ def wq_kv_dequant(cache: KVCache, T: int, slot: torch.Tensor | None = None, out_
     _check(lib().wq_kv_dequant(_ptr(cache.codes), _ptr(cache.s), _ptr(cache.zpacked), T, cache.hd, _ptr(slot),
                                cache.S, _DT.get(out_dtype, -1), _ptr(out), _stream(stream)), "wq_kv_dequant")
     return out
+
+
+# ---- attention next to the INT4 KV cache ----------------------------------------
+# These calls run on their tensors' device whichever is current, and allocate
+# outputs and workspaces on the stream they run on.
+
+class _on:
+    """The device of a tensor and the stream of a call, current inside the with block."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        if t.device.type != "cuda":
+            raise ValueError(f"tensors must be on the GPU (got {t.device})")
+        self.device = t.device
+        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
+        if self.stream.device != t.device:
+            raise ValueError(f"the stream belongs to {self.stream.device}, the tensors are on {t.device}")
+
+    def __enter__(self):
+        self.guard = torch.cuda.stream(self.stream)  # sets the stream's device too
+        self.guard.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *e):
+        return self.guard.__exit__(*e)
+
+
+def _heads(name: str, x: torch.Tensor, like: torch.Tensor | None = None, T: int | None = None) -> int:
+    """x is [T][heads][D], heads and values contiguous; its stride between tokens."""
+    if x.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{name} must be a bfloat16 or float16 tensor [tokens][heads][D] "
+                         f"(got {x.dtype}, shape {tuple(x.shape)})")
+    n, h, d = x.shape
+    if (d > 1 and x.stride(2) != 1) or (h > 1 and x.stride(1) != d):
+        raise ValueError(f"{name}: the heads and values of a token must be contiguous (strides {x.stride()})")
+    if like is not None and (x.dtype != like.dtype or x.device != like.device or d != like.shape[2]):
+        raise ValueError(f"{name} is {x.dtype} on {x.device} with D={d}, expected {like.dtype} on {like.device} with "
+                         f"D={like.shape[2]}")
+    if T is not None and n != T:
+        raise ValueError(f"{name} has {n} tokens, expected {T}")
+    return x.stride(0) if n > 1 else h * d
+
+
+def _dev_array(name: str, t: torch.Tensor, dtype, shape, like: torch.Tensor) -> torch.Tensor:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device} "
+                         f"(got {t.dtype}, shape {tuple(t.shape)}, on {t.device})")
+    return t
+
+
+def wq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor, *,
+                    q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                    interleaved: bool = False, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                    stream=None):
+    """Norm of every head of q [T][Hq][D] and k [T][Hkv][D] (bf16 or fp16; slices
+    of a fused projection are fine) and the rotation of its position, in one
+    pass.  cos, sin: fp32 [P][rot/2] tables; positions: int32 [T] (a token whose
+    position lies outside [0, P) leaves its output rows as they were); weights
+    [D] of q's type, or None for ones.  q_out, k_out may be q and k themselves.
+    Returns (q_out, k_out)."""
+    qs, ks = _heads("q", q), _heads("k", k, q, q.shape[0])
+    T, Hq, D = q.shape
+    P, half = cos.shape
+    _dev_array("cos", cos, torch.float32, (P, half), q)
+    _dev_array("sin", sin, torch.float32, (P, half), q)
+    _dev_array("positions", positions, torch.int32, (T,), q)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _dev_array(name, w, q.dtype, (D,), q)
+    with _on(q, stream) as s:
+        outs, strides = [], []
+        for name, x, o in (("q_out", q, q_out), ("k_out", k, k_out)):
+            if o is None:
+                o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            strides.append(_heads(name, o, q, T))
+            if o.shape[1] != x.shape[1]:
+                raise ValueError(f"{name} has {o.shape[1]} heads, expected {x.shape[1]}")
+            outs.append(o)
+        _check(lib().wq_qk_norm_rope(_ptr(q), _ptr(k), _DT[q.dtype], T, Hq, k.shape[1], D, qs, ks, _ptr(q_weight),
+                                     _ptr(k_weight), eps, _ptr(positions), _ptr(cos), _ptr(sin), P, 2 * half,
+                                     int(interleaved), _ptr(outs[0]), _ptr(outs[1]), strides[0], strides[1], s),
+               "wq_qk_norm_rope")
+    return outs[0], outs[1]
+
+
+def _attn_out(q: torch.Tensor, out, lse):
+    """The output and the optional lse tensor (lse: False, True or a tensor)."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _dev_array("out", out, q.dtype, q.shape, q)
+    if lse is True:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    elif lse is False or lse is None:
+        lse = None
+    else:
+        _dev_array("lse", lse, torch.float32, q.shape[:2], q)
+    return out, lse
+
+
+def wq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_starts: torch.Tensor, *,
+                        scale: float | None = None, out: torch.Tensor | None = None, lse=False, stream=None):
+    """Causal attention over prompts packed one after another: q [T][Hq][D], k and
+    v [T][Hkv][D] (bf16 or fp16; slices of a fused projection are fine),
+    seq_starts int32 [B+1] on the GPU.  scale defaults to 1/sqrt(D).  Tokens
+    outside every sequence are not written.  Returns out [T][Hq][D], or (out,
+    lse) with lse=True or an fp32 [T][Hq] tensor."""
+    qs, ks, vs = _heads("q", q), _heads("k", k, q, q.shape[0]), _heads("v", v, q, q.shape[0])
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if v.shape[1] != Hkv:
+        raise ValueError(f"k has {Hkv} heads, v {v.shape[1]}")
+    if seq_starts.dim() != 1 or seq_starts.numel() < 1:
+        raise ValueError("seq_starts must hold B + 1 token numbers")
+    B = seq_starts.numel() - 1
+    _dev_array("seq_starts", seq_starts, torch.int32, (B + 1,), q)
+    with _on(q, stream) as s:
+        out, lse = _attn_out(q, out, lse)
+        _check(lib().wq_prompt_attention(_ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], T, Hq, Hkv, D, qs, ks, vs, B,
+                                         _ptr(seq_starts), D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse),
+                                         s), "wq_prompt_attention")
+    return out if lse is None else (out, lse)
+
+
+def wq_kv_attention_workspace_bytes(T: int, Hq: int, Hkv: int, D: int, B: int, page_size: int, max_context: int,
+                                    max_queries: int = 1) -> int:
+    return int(lib().wq_kv_attention_workspace_bytes(T, Hq, Hkv, D, B, page_size, max_context, max_queries))
+
+
+def wq_kv_attention_plan(T: int, Hq: int, Hkv: int, D: int, B: int, page_size: int, max_context: int,
+                         max_queries: int = 1) -> str:
+    buf = ctypes.create_string_buffer(256)
+    _check(lib().wq_kv_attention_plan(T, Hq, Hkv, D, B, page_size, max_context, max_queries, buf, len(buf)),
+           "wq_kv_attention_plan")
+    return buf.value.decode()
+
+
+def wq_kv_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, block_table: torch.Tensor,
+                    context_lens: torch.Tensor, *, page_size: int, max_context: int | None = None,
+                    q_starts: torch.Tensor | None = None, max_queries: int | None = None, scale: float | None = None,
+                    out: torch.Tensor | None = None, lse=False, workspace: torch.Tensor | None = None, stream=None):
+    """Attention of q [T][Hq][D] (bf16 or fp16) over INT4 K and V caches of
+    Hkv = hd / D heads in pages of page_size rows: token t of sequence b lies in
+    row block_table[b][t // page_size] * page_size + t % page_size (int32
+    [B][width]; page numbers outside the cache mark tokens that are not attended);
+    context_lens int32 [B] counts each sequence's cached tokens.  One query per
+    sequence, or those of sequence b at q_starts[b] .. q_starts[b+1] - 1 (int32
+    [B+1]; they are its last tokens, and see the tokens up to their own).
+    max_context and max_queries bound the lengths for the launch (defaults: the
+    table's width, all T).  scale defaults to 1/sqrt(D).  Queries that see nothing
+    give zeros; rows outside every sequence are not written.  Returns out
+    [T][Hq][D], or (out, lse) with lse=True or an fp32 [T][Hq] tensor.  Without a
+    workspace, each call that needs one allocates it on its stream."""
+    qs = _heads("q", q)
+    T, Hq, D = q.shape
+    S, hd = k_cache.S, k_cache.hd
+    if (v_cache.S, v_cache.hd) != (S, hd) or hd % D != 0:
+        raise ValueError(f"caches of {S} x {hd} and {v_cache.S} x {v_cache.hd} values, heads of {D}")
+    Hkv = hd // D
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _dev_array(name + ".codes", c.codes, torch.uint8, (S, hd // 2), q)
+        _dev_array(name + ".s", c.s, torch.float16, (S, hd // 128), q)
+        _dev_array(name + ".zpacked", c.zpacked, torch.uint8, (S, (hd // 128 + 1) // 2), q)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [sequences][pages]")
+    B, width = block_table.shape
+    _dev_array("block_table", block_table, torch.int32, (B, width), q)
+    _dev_array("context_lens", context_lens, torch.int32, (B,), q)
+    if q_starts is not None:
+        _dev_array("q_starts", q_starts, torch.int32, (B + 1,), q)
+        if max_queries is None:
+            max_queries = T
+        max_queries = min(max_queries, T)
+    else:
+        max_queries = min(T, 1)
+    if max_context is None:
+        max_context = width * page_size
+    with _on(q, stream) as s:
+        out, lse = _attn_out(q, out, lse)
+        if workspace is None:
+            need = lib().wq_kv_attention_workspace_bytes(T, Hq, Hkv, D, B, page_size, max_context, max_queries)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        _check(lib().wq_kv_attention(_ptr(q), _DT[q.dtype], T, Hq, Hkv, D, qs, _ptr(k_cache.codes), _ptr(k_cache.s),
+                                     _ptr(k_cache.zpacked), _ptr(v_cache.codes), _ptr(v_cache.s), _ptr(v_cache.zpacked),
+                                     S, B, _ptr(block_table), width, page_size, _ptr(context_lens), max_context,
+                                     _ptr(q_starts), max_queries, D ** -0.5 if scale is None else scale, _ptr(out),
+                                     _ptr(lse), _ptr(workspace),
+                                     0 if workspace is None else workspace.numel() * workspace.element_size(), s),
+               "wq_kv_attention")
+    return out if lse is None else (out, lse)
 
 
 # ---- AWQ-style per-input-channel scaling ---------------------------------------

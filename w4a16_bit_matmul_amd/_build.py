@@ -27,6 +27,9 @@ PER_FILE = {
     # VGPR form (the default AGPR form rotates them through copies every turn)
     "wq_probe.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "wq_noalloc.hip": [],
+    "wq_rope.hip": [],
+    "wq_kv_attn.hip": [],
+    "wq_prompt_attn.hip": [],
     "wq_api.cpp": [],
 }
 

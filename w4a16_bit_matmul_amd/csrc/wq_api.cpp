@@ -547,4 +547,137 @@ int wq_gemm_nvfp4_plan(int64_t M, int64_t N, int64_t K, int path, char* buf, siz
   return WQ_OK;
 }
 
+// ---- attention next to the INT4 KV cache --------------------------------------
+
+namespace {
+
+constexpr int64_t kMaxCount = int64_t(1) << 31;  // tokens, rows, table entries
+
+// Types, head counts and sizes the three operators share.
+int check_heads(int dtype, int64_t T, int Hq, int Hkv, int D) {
+  if (dtype != WQ_BF16 && dtype != WQ_F16) return WQ_EINVAL;
+  if (T < 0 || T >= kMaxCount || Hq <= 0 || Hkv <= 0 || Hq > 65536 || Hkv > 65536) return WQ_EINVAL;
+  if ((D != 64 && D != 128 && D != 256) || Hq % Hkv != 0) return WQ_EUNSUPPORTED;
+  return WQ_OK;
+}
+
+int check_rows(const void* p, int64_t stride, int64_t heads, int D) {
+  if (stride < heads * D || stride > (int64_t(1) << 40)) return WQ_EINVAL;
+  return !aligned(p, 16) || stride % 8 != 0 ? WQ_EALIGN : WQ_OK;
+}
+
+bool good_scale(float s) { return s > 0.0f && s <= 3.4028235e38f; }
+
+// Sizes of a cache attention call (host side of wq_kv_attention and its queries).
+int check_kv_attn(int dtype, int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size, int64_t max_context,
+                  int64_t max_queries) {
+  const int st = check_heads(dtype, T, Hq, Hkv, D);
+  if (st) return st;
+  if (B < 0 || B > (1 << 24) || max_context < 0 || max_context >= kMaxCount || max_queries < 0 || max_queries > T)
+    return WQ_EINVAL;
+  if (((int64_t)Hkv * D) % 128 != 0 || page_size < 1 || (page_size & (page_size - 1)) != 0) return WQ_EUNSUPPORTED;
+  // grids stay below 2^31 workgroups
+  if (max_queries > 0 && B * max_queries > kMaxCount / Hq) return WQ_EUNSUPPORTED;
+  return WQ_OK;
+}
+
+}  // namespace
+
+int wq_qk_norm_rope(const void* q, const void* k, int dtype, int64_t T, int Hq, int Hkv, int D, int64_t q_stride,
+                    int64_t k_stride, const void* q_weight, const void* k_weight, float eps, const int32_t* positions,
+                    const float* cos, const float* sin, int64_t P, int rot, int interleaved, void* q_out, void* k_out,
+                    int64_t q_out_stride, int64_t k_out_stride, void* stream) {
+  int st = check_heads(dtype, T, Hq, Hkv, D);
+  if (st) return st;
+  if (!(eps >= 0.0f && eps <= 3.4028235e38f) || P <= 0 || P > kMaxCount || (interleaved != 0 && interleaved != 1))
+    return WQ_EINVAL;
+  if (rot <= 0 || rot > D || rot % 16 != 0) return WQ_EUNSUPPORTED;
+  if (T == 0) return WQ_OK;
+  if (!q || !k || !positions || !cos || !sin || !q_out || !k_out) return WQ_EINVAL;
+  if ((st = check_rows(q, q_stride, Hq, D)) || (st = check_rows(k, k_stride, Hkv, D)) ||
+      (st = check_rows(q_out, q_out_stride, Hq, D)) || (st = check_rows(k_out, k_out_stride, Hkv, D)))
+    return st;
+  if (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(positions, 4) || !aligned(q_weight, 8) ||
+      !aligned(k_weight, 8))
+    return WQ_EALIGN;
+  // at most 2^31 workgroups of eight rows
+  if (T > (int64_t(1) << 34) / (Hq + Hkv)) return WQ_EUNSUPPORTED;
+  const wq::QkNormRopeArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), T, q_stride, k_stride,
+                             Hq, Hkv, D, rot, interleaved, dtype, static_cast<const uint16_t*>(q_weight),
+                             static_cast<const uint16_t*>(k_weight), eps, positions, cos, sin, P,
+                             static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_out), q_out_stride, k_out_stride};
+  return hip_status(wq::launch_qk_norm_rope(a, static_cast<hipStream_t>(stream)));
+}
+
+int wq_prompt_attention(const void* q, const void* k, const void* v, int dtype, int64_t T, int Hq, int Hkv, int D,
+                        int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t B, const int32_t* seq_starts,
+                        float scale, void* out, float* lse, void* stream) {
+  int st = check_heads(dtype, T, Hq, Hkv, D);
+  if (st) return st;
+  if (B < 0 || B > (1 << 24) || !good_scale(scale)) return WQ_EINVAL;
+  if (T == 0 || B == 0) return WQ_OK;
+  if (!q || !k || !v || !seq_starts || !out) return WQ_EINVAL;
+  if ((st = check_rows(q, q_stride, Hq, D)) || (st = check_rows(k, k_stride, Hkv, D)) ||
+      (st = check_rows(v, v_stride, Hkv, D)))
+    return st;
+  if (!aligned(out, 16) || !aligned(seq_starts, 4) || !aligned(lse, 4)) return WQ_EALIGN;
+  // at most 2^31 workgroups of 128 rows
+  if (T * (Hq / Hkv) / 128 + B >= kMaxCount / Hkv) return WQ_EUNSUPPORTED;
+  const wq::PromptAttnArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
+                             static_cast<const uint16_t*>(v), T, q_stride, k_stride, v_stride, dtype, Hq, Hkv, D,
+                             (int)B, seq_starts, scale, static_cast<uint16_t*>(out), lse};
+  return hip_status(wq::launch_prompt_attn(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t wq_kv_attention_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size,
+                                       int64_t max_context, int64_t max_queries) {
+  if (check_kv_attn(WQ_BF16, T, Hq, Hkv, D, B, page_size, max_context, max_queries)) return 0;
+  if (T == 0 || B == 0 || max_queries == 0) return 0;
+  return wq::kv_attn_workspace_bytes(T, (int)B, Hq, Hkv, D, page_size, max_context, max_queries);
+}
+
+int wq_kv_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size, int64_t max_context,
+                         int64_t max_queries, char* buf, size_t buf_len) {
+  if (!buf || buf_len == 0) return WQ_EINVAL;
+  buf[0] = 0;
+  const int st = check_kv_attn(WQ_BF16, T, Hq, Hkv, D, B, page_size, max_context, max_queries);
+  if (st) return st;
+  if (T == 0 || B == 0 || max_queries == 0) return WQ_OK;
+  wq::describe_kv_attn(T, (int)B, Hq, Hkv, D, page_size, max_context, max_queries, buf, buf_len);
+  return WQ_OK;
+}
+
+int wq_kv_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D, int64_t q_stride,
+                    const uint8_t* k_codes, const uint16_t* k_s_f16, const uint8_t* k_zpacked, const uint8_t* v_codes,
+                    const uint16_t* v_s_f16, const uint8_t* v_zpacked, int64_t S, int64_t B,
+                    const int32_t* block_table, int64_t table_width, int page_size, const int32_t* context_lens,
+                    int64_t max_context, const int32_t* q_starts, int64_t max_queries, float scale, void* out,
+                    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_kv_attn(dtype, T, Hq, Hkv, D, B, page_size, max_context, max_queries);
+  if (st) return st;
+  if (!good_scale(scale) || S <= 0 || S >= kMaxCount || table_width < 0 || table_width >= kMaxCount) return WQ_EINVAL;
+  if (page_size > S) return WQ_EUNSUPPORTED;
+  if (max_context > table_width * page_size) return WQ_EINVAL;
+  if (!q_starts && (T != B || max_queries != (T > 0 ? 1 : 0))) return WQ_EINVAL;
+  if (T == 0 || B == 0 || max_queries == 0) return WQ_OK;
+  if (!q || !k_codes || !k_s_f16 || !k_zpacked || !v_codes || !v_s_f16 || !v_zpacked || !block_table ||
+      !context_lens || !out)
+    return WQ_EINVAL;
+  if ((st = check_rows(q, q_stride, Hq, D))) return st;
+  if (!aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_s_f16, 2) || !aligned(v_s_f16, 2) ||
+      !aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(q_starts, 4) || !aligned(out, 16) ||
+      !aligned(lse, 4))
+    return WQ_EALIGN;
+  const size_t need =
+      wq::kv_attn_workspace_bytes(T, (int)B, Hq, Hkv, D, page_size, max_context, max_queries);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return WQ_EWORKSPACE;
+    if (!aligned(workspace, 256)) return WQ_EALIGN;
+  }
+  const wq::KvAttnArgs a{static_cast<const uint16_t*>(q), T, q_stride, dtype, Hq, Hkv, D, k_codes, k_s_f16, k_zpacked,
+                         v_codes, v_s_f16, v_zpacked, S, (int)B, block_table, table_width, page_size, context_lens,
+                         max_context, q_starts, max_queries, scale, static_cast<uint16_t*>(out), lse, workspace};
+  return hip_status(wq::launch_kv_attn(a, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

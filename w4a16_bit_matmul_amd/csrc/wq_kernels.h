@@ -76,6 +76,66 @@ hipError_t launch_kv_quantize(const void* X, int dtype, int64_t T, int64_t hd, c
 hipError_t launch_kv_dequant(const uint8_t* codes, const uint16_t* s, const uint8_t* zp, int64_t T, int64_t hd,
                              const int32_t* slot, int64_t S, int out_dtype, void* out, hipStream_t stream);
 
+// Norm of each query and key head, and its rotation, in one pass.  dtype: 1
+// bf16, 2 fp16 (q, k, weights and outputs); strides in values between tokens;
+// weights may be NULL (ones).
+struct QkNormRopeArgs {
+  const uint16_t *q, *k;
+  int64_t T, q_stride, k_stride;
+  int Hq, Hkv, D, rot, interleaved, dtype;
+  const uint16_t *q_weight, *k_weight;
+  float eps;
+  const int32_t* positions;
+  const float *cos, *sin;
+  int64_t P;
+  uint16_t *q_out, *k_out;
+  int64_t qo_stride, ko_stride;
+};
+hipError_t launch_qk_norm_rope(const QkNormRopeArgs& a, hipStream_t stream);
+
+// Attention over the INT4 KV cache (wq_kv_attn.hip).
+struct KvAttnArgs {
+  const uint16_t* q;
+  int64_t T, q_stride;
+  int dtype, Hq, Hkv, D;
+  const uint8_t* k_codes;
+  const uint16_t* k_s;
+  const uint8_t* k_zp;
+  const uint8_t* v_codes;
+  const uint16_t* v_s;
+  const uint8_t* v_zp;
+  int64_t S;
+  int B;
+  const int32_t* table;
+  int64_t table_width;
+  int page;
+  const int32_t* lens;
+  int64_t max_context;
+  const int32_t* q_starts;
+  int64_t max_queries;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  void* workspace;
+};
+size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context,
+                               int64_t max_queries);
+int describe_kv_attn(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries,
+                     char* buf, size_t len);
+hipError_t launch_kv_attn(const KvAttnArgs& a, hipStream_t stream);
+
+// Causal attention over packed prompts (wq_prompt_attn.hip).
+struct PromptAttnArgs {
+  const uint16_t *q, *k, *v;
+  int64_t T, q_stride, k_stride, v_stride;
+  int dtype, Hq, Hkv, D, B;
+  const int32_t* starts;
+  float scale;
+  uint16_t* out;
+  float* lse;
+};
+hipError_t launch_prompt_attn(const PromptAttnArgs& a, hipStream_t stream);
+
 // Split-K GEMV for small M (dot products on the matrix cores).  It needs a workspace (a counter region that
 // is zero on entry and left zero, then fp32 partial sums) only when it splits K
 // across workgroups; gemv_workspace_bytes gives the size (0 otherwise).

@@ -1,0 +1,636 @@
+// Attention over the INT4 KV cache (gfx950).
+//
+// For a query row q (one query token and head) and the tokens t it sees,
+//   out = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale * q.k_t - max),
+// with k_t = s_t (c_t - z_t) and v_t alike, read from the codes in one pass: a
+// running maximum and sum per row, no scores in memory.
+//
+// The matrix cores take the exact integers c - z in fp16 (four bits and a
+// zero-point: |c - z| <= 15); the scale of a token multiplies its score in fp32
+// (K) and its softmax weight in fp32 before that weight is rounded to fp16 (V).
+// So the codes are decoded with the GEMV's four AND-ORs and four packed
+// subtractions a word and nothing is rounded but q (bf16 rows are moved into
+// fp16's range by a power of two) and the weights p_t s_t (fp16, 2^-12 of each
+// at most, after a power of two that puts the largest scale so far below 1).
+//
+// Both products are computed transposed, S^T = K q^T and O^T = V^T P^T, with
+// v_mfma_f32_16x16x32_f16 and 16 query rows as its columns (the heads of one KV
+// head's group and the query tokens).  Then every value of a row lies in the
+// lanes of that row (lane r + 16 c holds row r): the maximum is over a lane's
+// eight scores and two lane swaps, rescaling needs no exchange, and a lane's
+// scores of tokens {4c..4c+3, 16+4c..16+4c+3} of a 32-token tile are, in order,
+// its operand of the second product.  For V that product needs eight tokens of
+// one channel in a lane while a cache word holds eight channels of one token:
+// a lane reads the same word of its eight tokens, and since the even channels of
+// a word lie in its low half and the odd ones in its high half, one v_perm per
+// pair of tokens turns them into words of one channel's token pairs.
+//
+// Reading is the bound: 2 (D/2 + 2.5 D/128) bytes a token and KV head.  A wave
+// walks 32-token tiles of one KV head, the next tile's codes in flight while it
+// computes; a workgroup's waves take neighbouring KV heads of the same tokens
+// (whole cache rows are read) or, for short contexts, different tiles of one
+// head.  Contexts split across workgroups leave fp32 partial results that a
+// second kernel joins.
+#include <stdio.h>
+
+#include "wq_device.h"
+#include "wq_kernels.h"
+
+namespace wq {
+namespace {
+
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
+constexpr float kNegInf = -__builtin_inff();
+constexpr uint32_t kTokenOff = 0x80000000u;  // metadata word of a token that is not attended
+
+struct KvPlan {
+  int HW;          // KV heads of a workgroup (its W / HW waves per head take different tiles)
+  int RT;          // 16-row tiles of a wave
+  int W;           // waves of a workgroup
+  int64_t rtiles;  // workgroups along the query rows of one KV head
+  int64_t chunk;   // tokens of a split
+  int64_t KS;      // splits of max_context
+};
+
+// Tokens read past a chunk are never attended: a chunk is whole tiles of 32.
+KvPlan plan_kv(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries) {
+  KvPlan p;
+  const int64_t G = Hq / Hkv, rows = max_queries * G;
+  p.RT = rows <= 16 ? 1 : 2;
+  p.W = 8;
+  p.rtiles = (rows + 16 * p.RT - 1) / (16 * p.RT);
+  p.HW = Hkv % 8 == 0 ? 8 : Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
+  if (max_context <= 2048) p.HW = 1;
+  const int64_t TW = p.W / p.HW;
+  const int64_t base = (int64_t)B * (Hkv / p.HW) * p.rtiles;
+  const int64_t want = (1024 + base - 1) / base;
+  const int64_t unit = 32 * TW;
+  int64_t chunk = (max_context + want - 1) / want;
+  chunk = (chunk + unit - 1) / unit * unit;
+  if (chunk < 2 * unit) chunk = 2 * unit;
+  p.chunk = chunk;
+  p.KS = (max_context + chunk - 1) / chunk;
+  if (p.KS < 1) p.KS = 1;
+  return p;
+}
+
+__device__ __forceinline__ float max_over_rows16(float v) {  // over the lanes l, l ^ 16, l ^ 32, l ^ 48
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  v = fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+  const uint32_t w = __builtin_bit_cast(uint32_t, v);
+  auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
+}
+__device__ __forceinline__ float sum_over_rows16(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  v = __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
+  const uint32_t w = __builtin_bit_cast(uint32_t, v);
+  auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  return __builtin_bit_cast(float, (uint32_t)b[0]) + __builtin_bit_cast(float, (uint32_t)b[1]);
+}
+
+// Two fp16 pairs (c - z) of the nibbles 0, 4 and 1, 5 of a word: (1024 + c) and
+// (64 + c) by OR-ing an exponent in (wq_device.h), less the same of z.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, h2 z1024) {
+  return as_u32(as_h2((w & 0x000F000Fu) | 0x64006400u) - z1024);
+}
+__device__ __forceinline__ uint32_t code_pair16(uint32_t w, h2 z64) {
+  return as_u32(as_h2((w & 0x00F000F0u) | 0x54005400u) - z64);
+}
+__device__ __forceinline__ h2 zero1024(uint32_t zz) { return as_h2(zz | 0x64006400u); }
+__device__ __forceinline__ h2 zero64(uint32_t zz) { return as_h2((zz << 4) | 0x54005400u); }
+
+// One 32-token tile of one KV head as loaded, untouched.
+template <int D>
+struct Tile {
+  static constexpr int NB = D == 256 ? 2 : 1;   // cache blocks of a head
+  static constexpr int KW = D / 32;             // code words of a K lane and 16-token group
+  static constexpr int VW = D == 256 ? 2 : 1;   // words (D = 64: half words) of a V lane and token
+  uint32_t k[2][KW];
+  uint32_t v[8][VW];
+  uint32_t s[NB];  // lanes 0..31: K scale of token l, lanes 32..63: V scale of token l - 32
+  uint32_t z;      // the zero-point byte beside it
+  bool off;        // the lane's token is not attended (no such page, or past the context)
+};
+
+template <int D, int RT, int W, bool P32>
+__global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? 2 * W / 4 : W / 4) void kv_attn_kernel(KvAttnArgs a, int HW, int64_t chunk, int KS,
+                                                                int rtiles) {
+  constexpr int NB = Tile<D>::NB, KW = Tile<D>::KW, VW = Tile<D>::VW;
+  constexpr int NS = D / 32;             // MFMA steps of a score
+  constexpr int NE = D / 16;             // MFMAs of an output tile: 16 channels each
+  extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
+  const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int TW = W / HW, tg = wave / HW;
+  const int HG = a.Hkv / HW;
+  int64_t id = blockIdx.x;
+  const int rt0 = (int)(id % rtiles);
+  id /= rtiles;
+  const int hg = (int)(id % HG);
+  id /= HG;
+  const int split = (int)(id % KS);
+  const int b = (int)(id / KS);
+  const int h = hg * HW + wave % HW;
+  const int G = a.Hq / a.Hkv;
+
+  int64_t q0 = b, nq = 1;
+  if (a.q_starts) {
+    q0 = max((int64_t)a.q_starts[b], (int64_t)0);
+    nq = min((int64_t)a.q_starts[b + 1], a.T) - q0;
+    nq = min(nq, a.max_queries);
+  }
+  const int64_t len = min((int64_t)a.lens[b], a.max_context);
+  const int64_t row0 = (int64_t)rt0 * (16 * RT);
+  if (row0 >= nq * G) return;
+  if (split > 0 && split * chunk >= len) return;
+  const bool whole = len <= chunk;  // the sequence is not split
+  // rows of this workgroup see at most the first `top` tokens, and all of its
+  // rows see the first `low`
+  const int64_t row1 = min(row0 + 16 * RT, nq * G) - 1;
+  const int64_t top = max(len - nq + row1 / G + 1, (int64_t)0), low = len - nq + row0 / G + 1;
+  const int64_t t_begin = (int64_t)split * chunk, t_end = min(t_begin + chunk, top);
+
+  // the wave's queries, as the B operand of the scores: lane (r, c) channels
+  // 32 c + 8 j (D = 64: 16 c + 8 j) of each block, brought into fp16's range by
+  // the power of two that takes the row's largest value into [1, 2)
+  h8 qf[RT][NS];
+  float f[RT];            // score of a row in units of log2: raw * f
+  int64_t lim[RT];        // tokens the row sees
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int64_t row = min(row0 + 16 * t + r, nq * G - 1);  // rows past the end repeat the last, not stored
+    const int64_t qi = row / G;
+    lim[t] = len - nq + qi + 1;
+    const uint16_t* qp = a.q + (q0 + qi) * a.q_stride + ((int64_t)h * G + row % G) * D;
+    u4 raw[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      const int ch = D == 64 ? 16 * c + 8 * j : 128 * (j / 4) + 32 * c + 8 * (j % 4);
+      raw[j] = *reinterpret_cast<const u4*>(qp + ch);
+    }
+    float x[NS][8], top_q = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t hw = raw[j][e / 2] >> (16 * (e % 2)) & 0xffffu;
+        x[j][e] = a.dtype == 1 ? __builtin_bit_cast(float, hw << 16) : f16_bits_to_f32((uint16_t)hw);
+        top_q = fmaxf(top_q, fabsf(x[j][e]));
+      }
+    top_q = max_over_rows16(top_q);
+    int ex = (int)(__builtin_bit_cast(uint32_t, top_q) >> 23) - 127;
+    ex = min(max(ex, -126), 126);  // zeros, subnormals and infinities: the nearest power
+    const float down = __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23);
+    const float up = __builtin_bit_cast(float, (uint32_t)(127 + ex) << 23);
+    f[t] = a.scale * 1.4426950408889634f * up;
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) qf[t][j][e] = (_Float16)(x[j][e] * down);
+  }
+
+  f4 acc[RT][NE];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    m[t] = kNegInf;
+    l[t] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) acc[t][e] = f4{0, 0, 0, 0};
+  }
+  float v_top = 0.0f, v_down = 1.0f;  // V scales so far lie below v_top = 1 / v_down (a power of two)
+
+  const int64_t rowb = (int64_t)a.Hkv * D / 2;  // code bytes of a cache row
+  const int nbt = a.Hkv * D / 128, zb = (nbt + 1) / 2;
+  const int blk = h * D / 128;                   // first block of the head
+  const int64_t hoff = (int64_t)h * D / 2;       // its code bytes
+  const int zshift = (D == 256) ? 0 : (blk & 1) * 4;
+  const int lg = 31 - __builtin_clz(a.page);
+  const int64_t pages = a.S >> lg;
+  const int32_t* table = a.table + (int64_t)b * a.table_width;
+  uint32_t* meta = lds + wave * (64 * NB);
+  const int ml = lane & 31;
+
+  // page entries of a tile: one of the whole tile (P32) or one of lane ml's token
+  auto page_entry = [&](int64_t tk) -> int {
+    if constexpr (P32) return table[min(tk, t_end - 1) >> lg];
+    return table[min(tk + ml, t_end - 1) >> lg];
+  };
+  auto load = [&](Tile<D>& T, int64_t tk, int pg) {
+    int64_t krow[2], vrow[8], mrow;
+    if constexpr (P32) {
+      const bool ok = pg >= 0 && pg < pages;
+      const int64_t base = ok ? ((int64_t)pg << lg) + (tk & (a.page - 1)) : 0;
+      T.off = !ok || tk + ml >= t_end;
+      // a tile lies inside one page; with no page it reads row 0 alone
+      const int64_t step = ok ? 1 : 0;
+      mrow = base + step * ml;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) krow[g] = base + step * (16 * g + r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vrow[i] = base + step * (16 * (i / 4) + 4 * c + i % 4);
+    } else {
+      const bool ok = pg >= 0 && pg < pages && tk + ml < t_end;
+      T.off = !ok;
+      const int own = ok ? (int)(((int64_t)pg << lg) + ((tk + ml) & (a.page - 1))) : 0;
+      mrow = own;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) krow[g] = __shfl(own, 16 * g + r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vrow[i] = __shfl(own, 16 * (i / 4) + 4 * c + i % 4);
+    }
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const uint8_t* p = a.k_codes + krow[g] * rowb + hoff;
+      if constexpr (D == 64) {
+        const u2 w = *reinterpret_cast<const u2*>(p + 8 * c);
+        T.k[g][0] = w[0];
+        T.k[g][1] = w[1];
+      } else {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const u4 w = *reinterpret_cast<const u4*>(p + 64 * n + 16 * c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) T.k[g][4 * n + j] = w[j];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint8_t* p = a.v_codes + vrow[i] * rowb + hoff;
+      if constexpr (D == 64) {
+        T.v[i][0] = *reinterpret_cast<const uint16_t*>(p + 2 * r);
+      } else {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) T.v[i][n] = *reinterpret_cast<const uint32_t*>(p + 64 * n + 4 * r);
+      }
+    }
+    const uint16_t* sp = (lane < 32 ? a.k_s : a.v_s) + mrow * nbt + blk;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) T.s[n] = sp[n];
+    T.z = ((lane < 32 ? a.k_zp : a.v_zp) + mrow * zb)[blk / 2];
+  };
+
+  auto compute = [&](Tile<D>& T, int64_t tk) {
+    // scale (low half) and zero-point (bits 16..19) of every token and cache
+    // through LDS to the lanes that need them; a token that is not attended has
+    // scale and zero-point 0, whatever its cache row holds
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const uint32_t zp = (D == 256 ? T.z >> (4 * n) : T.z >> zshift) & 15u;
+      meta[64 * n + lane] = T.off ? kTokenOff : (T.s[n] | (zp << 16));
+    }
+    f4 sc[RT][2][NB];
+    float ksc[NB][8];
+    bool any_off = false;
+    uint32_t km[NB][8];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const u4 w = *reinterpret_cast<const u4*>(meta + 64 * n + 16 * g + 4 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          km[n][4 * g + i] = w[i];
+          ksc[n][4 * g + i] = f16_bits_to_f32((uint16_t)w[i]);
+        }
+      }
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const uint32_t zw = (meta[64 * n + 16 * g + r] >> 16) & 15u;
+        const uint32_t zz = zw * 0x00010001u;
+        const h2 z1 = zero1024(zz), z6 = zero64(zz);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) sc[t][g][n] = f4{0, 0, 0, 0};
+        constexpr int SB = NS / NB;
+#pragma unroll
+        for (int j = 0; j < SB; ++j) {
+          const uint32_t w = T.k[g][SB * n + j], w8 = w >> 8;
+          const u4 d = {code_pair(w, z1), code_pair16(w, z6), code_pair(w8, z1), code_pair16(w8, z6)};
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+            sc[t][g][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, d), qf[t][SB * n + j],
+                                                                 sc[t][g][n], 0, 0, 0);
+        }
+      }
+    // V: scales below 1 by a power of two that follows the largest so far
+    float vsc[NB][8];
+    uint32_t vm[NB][8];
+    float vmax = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const u4 w = *reinterpret_cast<const u4*>(meta + 64 * n + 32 + 16 * g + 4 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vm[n][4 * g + i] = w[i];
+          vsc[n][4 * g + i] = f16_bits_to_f32((uint16_t)w[i]);
+          vmax = fmaxf(vmax, vsc[n][4 * g + i]);
+        }
+      }
+    vmax = max_over_rows16(vmax);
+    if (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(uint32_t, vmax)) >
+        __builtin_bit_cast(uint32_t, v_top)) {  // both positive: bits order as values
+      const uint32_t ex = min((__builtin_amdgcn_readfirstlane(__builtin_bit_cast(uint32_t, vmax)) >> 23) + 1, 200u);
+      const float n_top = __builtin_bit_cast(float, ex << 23);
+      const float n_down = __builtin_bit_cast(float, (254u - ex) << 23);
+      const float k = v_top * n_down;
+      v_top = n_top;
+      v_down = n_down;
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int e = 0; e < NE; ++e) acc[t][e] *= k;
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        vsc[n][i] *= v_down;
+        any_off |= (km[n][i] & kTokenOff) != 0;
+      }
+    const bool masked = tk + 32 > low || __ballot(any_off) != 0;
+    h8 pf[RT][NB];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      float s8[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s8[i] = sc[t][i / 4][0][i % 4] * ksc[0][i];
+        if constexpr (NB == 2) s8[i] += sc[t][i / 4][1][i % 4] * ksc[1][i];
+      }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t tok = tk + 16 * (i / 4) + 4 * c + i % 4;
+          if (tok >= lim[t] || (km[0][i] & kTokenOff)) s8[i] = kNegInf;
+        }
+      }
+      float mx = s8[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s8[i]);
+      mx = max_over_rows16(mx) * f[t];
+      if (__ballot(mx > m[t])) {
+        const float mn = fmaxf(m[t], mx);
+        const float al = m[t] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[t] - mn);
+        m[t] = mn;
+        l[t] *= al;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) acc[t][e] *= al;
+      }
+      const float ms = m[t] == kNegInf ? 0.0f : m[t];
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s8[i], f[t], -ms));
+        l[t] += p[i];
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pf[t][n][i] = (_Float16)(p[i] * vsc[n][i]);
+    }
+    // O^T += V^T P^T, 16 channels an MFMA
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      h2 z1[4], z6[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t zz = __builtin_amdgcn_perm(vm[n][2 * i + 1], vm[n][2 * i], 0x07060302u) & 0x000F000Fu;
+        z1[i] = zero1024(zz);
+        z6[i] = zero64(zz);
+      }
+      auto product = [&](int e, u4 d) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          acc[t][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, d), pf[t][n], acc[t][e], 0, 0, 0);
+      };
+      uint32_t x[4], y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = __builtin_amdgcn_perm(T.v[2 * i + 1][n], T.v[2 * i][n], 0x05040100u);  // even channels of two tokens
+        if constexpr (D != 64) y[i] = __builtin_amdgcn_perm(T.v[2 * i + 1][n], T.v[2 * i][n], 0x07060302u);
+      }
+#pragma unroll
+      for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
+        u4 d[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = half ? y[i] : x[i], w8 = w >> 8;
+          d[0][i] = code_pair(w, z1[i]);
+          d[1][i] = code_pair16(w, z6[i]);
+          d[2][i] = code_pair(w8, z1[i]);
+          d[3][i] = code_pair16(w8, z6[i]);
+        }
+        // MFMA e of a block: channel 8 m + e of row m (D = 64: channel
+        // 8 (m / 2) + m % 2 + 2 e)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) product(D == 64 ? p : 8 * n + 2 * p + half, d[p]);
+      }
+    }
+  };
+
+  Tile<D> ta, tb;
+  const int64_t stride = 32 * TW;
+  int64_t tk = t_begin + 32 * tg;
+  if (tk < t_end) {
+    load(ta, tk, page_entry(tk));
+    int pg = page_entry(tk + stride);
+    while (true) {
+      // past the end the next tile repeats real rows and is not computed
+      load(tb, min(tk + stride, (t_end - 1) & ~(int64_t)31), pg);
+      pg = page_entry(tk + 2 * stride);
+      compute(ta, tk);
+      tk += stride;
+      if (tk >= t_end) break;
+      load(ta, min(tk + stride, (t_end - 1) & ~(int64_t)31), pg);
+      pg = page_entry(tk + 2 * stride);
+      compute(tb, tk);
+      tk += stride;
+      if (tk >= t_end) break;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    l[t] = sum_over_rows16(l[t]);
+#pragma unroll
+    for (int e = 0; e < NE; ++e) acc[t][e] *= v_top;
+  }
+
+  // Waves of one head join through LDS: the largest maximum, every wave's sums
+  // scaled to it, added in wave order.  Slab: the 16 rows of one row tile and
+  // block, [channel][row] per wave.
+  constexpr int DB = D < 128 ? D : 128, NEB = DB / 16;
+  float* slab = reinterpret_cast<float*>(lds) + W * 64 * NB;
+  float* stat = slab + W * 16 * DB;  // [wave][2][16]
+  for (int t = 0; t < RT; ++t) {
+    float mt = kNegInf, lt = 0.0f;
+#pragma unroll
+    for (int u = 0; u < RT; ++u)
+      if (u == t) mt = m[u], lt = l[u];
+    __syncthreads();
+    if (c == 0) {
+      stat[wave * 32 + r] = mt;
+      stat[wave * 32 + 16 + r] = lt;
+    }
+    __syncthreads();
+    float M = kNegInf;
+    for (int g = 0; g < TW; ++g) M = fmaxf(M, stat[(wave % HW + HW * g) * 32 + r]);
+    // a wave whose sum is 0 saw nothing (a NaN sum stays one)
+    const float k = lt == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(mt - M);
+    for (int n = 0; n < NB; ++n) {
+      if (n) __syncthreads();
+#pragma unroll
+      for (int u = 0; u < RT; ++u)
+#pragma unroll
+        for (int nn = 0; nn < NB; ++nn)
+          if (u == t && nn == n) {
+#pragma unroll
+            for (int e = 0; e < NEB; ++e)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int mrow = 4 * c + i;
+                const int ch = D == 64 ? 8 * (mrow / 2) + mrow % 2 + 2 * e : 8 * mrow + e;
+                slab[wave * 16 * DB + r * DB + ch] = acc[u][NEB * nn + e][i] * k;
+              }
+          }
+      __syncthreads();
+      // thread: two channels of one row and head
+      const int per_head = 16 * DB / 2;
+      for (int x = threadIdx.x; x < HW * per_head; x += 64 * W) {
+        const int hw = x / per_head, rest = x % per_head, rr = rest / (DB / 2), ch = 2 * (rest % (DB / 2));
+        const int64_t row = row0 + 16 * t + rr;
+        if (row > row1) continue;
+        float o0 = 0.0f, o1 = 0.0f, Mr = kNegInf, L = 0.0f;
+        for (int g = 0; g < TW; ++g) Mr = fmaxf(Mr, stat[(hw + HW * g) * 32 + rr]);
+        for (int g = 0; g < TW; ++g) {
+          const int wv = hw + HW * g;
+          const float lw = stat[wv * 32 + 16 + rr];
+          if (lw == 0.0f) continue;
+          o0 += slab[wv * 16 * DB + rr * DB + ch];
+          o1 += slab[wv * 16 * DB + rr * DB + ch + 1];
+          L += lw * __builtin_amdgcn_exp2f(stat[wv * 32 + rr] - Mr);
+        }
+        const int64_t hq = (int64_t)(hg * HW + hw) * G + row % G;
+        const int64_t at = (q0 + row / G) * a.Hq + hq;
+        if (whole) {
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          const uint32_t lo = a.dtype == 1 ? f32_to_bf16_bits(o0 * inv) : f32_to_f16_bits(o0 * inv);
+          const uint32_t hi = a.dtype == 1 ? f32_to_bf16_bits(o1 * inv) : f32_to_f16_bits(o1 * inv);
+          *reinterpret_cast<uint32_t*>(a.out + at * D + 128 * n + ch) = lo | (hi << 16);
+          if (a.lse && ch == 0 && n == 0)
+            a.lse[at] = L == 0.0f ? kNegInf : (Mr + __builtin_log2f(L)) * 0.6931471805599453f;
+        } else {
+          const int64_t nrow = a.T * a.Hq;
+          float* ws = static_cast<float*>(a.workspace);
+          float* part = ws + 2 * nrow * KS + ((int64_t)split * nrow + at) * D + 128 * n + ch;
+          *reinterpret_cast<float2*>(part) = make_float2(o0, o1);
+          if (ch == 0 && n == 0) *reinterpret_cast<float2*>(ws + 2 * ((int64_t)split * nrow + at)) = make_float2(Mr, L);
+        }
+      }
+    }
+  }
+}
+
+// Joins the partial results of the sequences that were split: one wave per
+// query row, D / 64 channels a lane, splits in order.
+template <int D>
+__global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int64_t chunk, int KS) {
+  const int lane = threadIdx.x & 63;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t hq = id % a.Hq, qi = (id / a.Hq) % a.max_queries, b = id / a.Hq / a.max_queries;
+  if (b >= a.B) return;
+  int64_t q0 = b, nq = 1;
+  if (a.q_starts) {
+    q0 = max((int64_t)a.q_starts[b], (int64_t)0);
+    nq = min((int64_t)a.q_starts[b + 1], a.T) - q0;
+  }
+  const int64_t len = min((int64_t)a.lens[b], a.max_context);
+  if (qi >= nq || len <= chunk) return;
+  const int n = (int)((len + chunk - 1) / chunk);
+  const int64_t nrow = a.T * a.Hq, at = (q0 + qi) * a.Hq + hq;
+  const float* ws = static_cast<const float*>(a.workspace);
+  float M = kNegInf;
+  for (int s = 0; s < n; ++s) M = fmaxf(M, ws[2 * (s * nrow + at)]);
+  constexpr int C = D / 64;
+  float o[C], L = 0.0f;
+#pragma unroll
+  for (int i = 0; i < C; ++i) o[i] = 0.0f;
+  for (int s = 0; s < n; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(ws + 2 * (s * nrow + at));
+    if (ml.y == 0.0f) continue;
+    const float k = __builtin_amdgcn_exp2f(ml.x - M);
+    L += ml.y * k;
+    const float* part = ws + 2 * nrow * KS + (s * nrow + at) * D + lane * C;
+#pragma unroll
+    for (int i = 0; i < C; ++i) o[i] += part[i] * k;
+  }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    a.out[at * D + lane * C + i] = a.dtype == 1 ? f32_to_bf16_bits(o[i] * inv) : f32_to_f16_bits(o[i] * inv);
+  if (a.lse && lane == 0) a.lse[at] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
+}
+
+template <int D>
+size_t lds_bytes(int W) {
+  constexpr int DB = D < 128 ? D : 128;
+  return (size_t)W * (64 * Tile<D>::NB + 16 * DB + 32) * 4;
+}
+
+template <int D, int RT, int W, bool P32>
+hipError_t launch_main(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream) {
+  static std::atomic<uint64_t> raised{0};
+  const size_t lds = lds_bytes<D>(W);
+  hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&kv_attn_kernel<D, RT, W, P32>), lds, raised);
+  if (e != hipSuccess) return e;
+  const int64_t grid = (int64_t)a.B * p.KS * (a.Hkv / p.HW) * p.rtiles;
+  kv_attn_kernel<D, RT, W, P32><<<(unsigned)grid, 64 * W, lds, stream>>>(a, p.HW, p.chunk, (int)p.KS, (int)p.rtiles);
+  e = hipGetLastError();
+  if (e != hipSuccess || p.KS == 1) return e;
+  const int64_t rows = (int64_t)a.B * a.max_queries * a.Hq;
+  kv_attn_join_kernel<D><<<(unsigned)((rows + 3) / 4), 256, 0, stream>>>(a, p.chunk, (int)p.KS);
+  return hipGetLastError();
+}
+
+template <int D, int RT, int W>
+hipError_t launch_p(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream) {
+  return a.page % 32 == 0 ? launch_main<D, RT, W, true>(a, p, stream) : launch_main<D, RT, W, false>(a, p, stream);
+}
+
+template <int D>
+hipError_t launch_rt(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream) {
+  return p.RT == 1 ? launch_p<D, 1, 8>(a, p, stream) : launch_p<D, 2, 8>(a, p, stream);
+}
+
+}  // namespace
+
+size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context,
+                               int64_t max_queries) {
+  const KvPlan p = plan_kv(T, B, Hq, Hkv, D, page, max_context, max_queries);
+  return p.KS == 1 ? 0 : (size_t)p.KS * T * Hq * (D + 2) * 4;
+}
+
+int describe_kv_attn(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries,
+                     char* buf, size_t len) {
+  const KvPlan p = plan_kv(T, B, Hq, Hkv, D, page, max_context, max_queries);
+  return snprintf(buf, len, "kv_attn_kernel<D=%d, RT=%d, W=%d, P32=%d> grid=%lld block=%d heads=%d chunk=%lld splits=%lld",
+                  D, p.RT, p.W, page % 32 == 0 ? 1 : 0, (long long)(B * p.KS * (Hkv / p.HW) * p.rtiles), 64 * p.W, p.HW,
+                  (long long)p.chunk, (long long)p.KS);
+}
+
+hipError_t launch_kv_attn(const KvAttnArgs& a, hipStream_t stream) {
+  const KvPlan p = plan_kv(a.T, a.B, a.Hq, a.Hkv, a.D, a.page, a.max_context, a.max_queries);
+  if (a.D == 64) return launch_rt<64>(a, p, stream);
+  if (a.D == 128) return launch_rt<128>(a, p, stream);
+  return launch_rt<256>(a, p, stream);
+}
+
+}  // namespace wq

@@ -1,0 +1,346 @@
+// Causal attention over whole prompts, packed one after another, with grouped
+// heads (gfx950).
+//
+// For query i of a sequence and head h of KV head h / G:
+//   out = sum_{t <= i} p_t v_t / sum p_t,  p_t = exp(scale * q.k_t - max),
+// in one pass over the keys with a running maximum and sum in fp32.
+//
+// A workgroup owns 128 rows of one KV head, a row being (token, head of the
+// group): its 128 / G tokens share every K and V tile it reads, and a short
+// sequence still fills its rows.  Four waves of 32 rows walk tiles of keys that
+// the workgroup keeps in LDS, double buffered, the next tile's loads in flight.
+// Both products are computed transposed, S^T = K q^T and O^T = V^T P^T, with
+// v_mfma_f32_32x32x16: a row is a column there, all its scores lie in lanes r
+// and r + 32 (one lane swap for its maximum), and a lane's scores are, in order,
+// its operand of the second product (tokens {8a + 4h .. + 3} of half h).  V^T
+// comes out of the row-major tile by ds_read_b64_tr_b16, which transposes 4 x 16
+// blocks as it reads.
+//
+// LDS rows hold D values as 16-byte chunks; chunk j of K's token t sits at
+// j ^ (t mod 16) (the 16 tokens a b128 read takes at once then fall in
+// different banks), V's at j ^ 4 (t mod 4) (the four rows of a transposed read).
+//
+// A weight of exactly 0 does not hide a value that is no number (0 * inf), and
+// one V operand serves rows that see a key and rows that do not.  So a tile that
+// some rows see only in part is looked through for such values as it is staged;
+// if there are any, they enter the product as 0 and reach the rows that do see
+// them as an infinity of their sign (a NaN: of both) from two more products.
+//
+// Workgroups find their sequence from the device's starts: sequence b owns the
+// tile slots from floor(start_b G / 128) + b on, at least as many as it has
+// tiles and increasing in b, so no host needs the lengths.  Later (longer) tiles
+// go first.
+#include "wq_device.h"
+#include "wq_kernels.h"
+
+namespace wq {
+namespace {
+
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+
+constexpr float kNegInf = -__builtin_inff();
+constexpr int kRows = 128;
+
+template <bool BF>
+__device__ __forceinline__ f16v mfma32(u4 x, u4 y, f16v c) {
+  if constexpr (BF)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, x), __builtin_bit_cast(b8, y), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, x), __builtin_bit_cast(h8, y), c, 0, 0, 0);
+}
+
+// fp32 pair -> 16-bit pair, round to nearest even
+template <bool BF>
+__device__ __forceinline__ uint32_t pack_pair(float x, float y) {
+  if constexpr (BF) {
+    const b2 v = {(__bf16)x, (__bf16)y};
+    return __builtin_bit_cast(uint32_t, v);
+  } else {
+    const h2 v = {(_Float16)x, (_Float16)y};
+    return as_u32(v);
+  }
+}
+
+__device__ __forceinline__ float max_over_halves(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+}
+
+// Whether one of the two 16-bit values of a word is infinite or NaN.
+template <bool BF>
+__device__ __forceinline__ bool odd_pair(uint32_t w) {
+  constexpr uint32_t lo = BF ? 0x7f80u : 0x7c00u, hi = lo << 16;
+  return (w & lo) == lo || (w & hi) == hi;
+}
+
+template <int D>
+__device__ __forceinline__ int k_chunk(int t, int j) {
+  return D == 64 ? j ^ ((t >> 1) & 7) : j ^ (t & 15);
+}
+template <int D>
+__device__ __forceinline__ int v_chunk(int t, int j) {
+  return D == 64 ? j ^ ((t & 2) << 1) : j ^ ((t & 3) << 2);
+}
+
+// First sequence whose slots start past i, less one: the sequence of slot i.
+// Every lane takes part; starts are clamped to [0, T].
+__device__ __forceinline__ int64_t clamp_start(const int32_t* starts, int b, int64_t T) {
+  return min(max((int64_t)starts[b], (int64_t)0), T);
+}
+__device__ __forceinline__ int find_sequence(const int32_t* starts, int B, int64_t T, int64_t G, int64_t i, int lane) {
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 63) / 64;
+    const int b = lo + lane * step;
+    const bool le = lane * step < n && clamp_start(starts, b, T) * G / kRows + b <= i;
+    const int k = __builtin_popcountll(__ballot(le));
+    if (k == 0) return lo;  // the slot lies before the first sequence's
+    lo += (k - 1) * step;
+    n = min(step, n - (k - 1) * step);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+template <int D, bool BF>
+__global__ __launch_bounds__(256, 2) void prompt_attn_kernel(PromptAttnArgs a, int64_t slots) {
+  constexpr int KT = D == 256 ? 32 : 64;    // keys of a tile
+  constexpr int TB = KT / 32;               // 32-key MFMA blocks
+  constexpr int NC = D / 8;                 // 16-byte chunks of a row
+  constexpr int NS = D / 16;                // MFMA steps of a score
+  constexpr int NB = D / 32;                // output blocks of 32 channels
+  constexpr int LD = KT * NC / 256;         // chunks a thread stages of K, and of V
+  extern __shared__ __attribute__((aligned(16))) u4 tile[];  // [2][K, V][KT * NC]
+  __shared__ uint32_t odd;  // a tile with hidden keys held an infinity or a NaN in V
+  const int lane = threadIdx.x & 63, r = lane & 31, hf = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int G = a.Hq / a.Hkv;
+  const int kvh = (int)(blockIdx.x % a.Hkv);
+  const int64_t slot = slots - 1 - blockIdx.x / a.Hkv;
+  const int b = find_sequence(a.starts, a.B, a.T, G, slot, lane);
+  const int64_t q0 = clamp_start(a.starts, b, a.T);
+  const int64_t n = clamp_start(a.starts, b + 1, a.T) - q0;
+  const int64_t R0 = (slot - (q0 * G / kRows + b)) * kRows;
+  if (R0 < 0 || R0 >= n * G) return;
+  const int64_t Rw = R0 + 32 * wave;                        // the wave's first row
+  const int64_t row = min(Rw + r, n * G - 1);               // past the end: the last row again, not stored
+  const int64_t qi = row / G;                               // the row's token; it sees keys 0..qi
+  const int64_t head = (int64_t)kvh * G + row % G;
+  const int64_t first = min(Rw, n * G - 1) / G;             // fewest and most keys of the wave's rows
+  const int64_t last = min(R0 + kRows, n * G) - 1;
+  const int tiles = (int)((last / G) / KT) + 1;
+
+  // the wave's queries, B operand: lane (r, hf) channels 16 j + 8 hf
+  u4 qf[NS];
+  {
+    const uint16_t* qp = a.q + (q0 + qi) * a.q_stride + head * D + 8 * hf;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) qf[j] = *reinterpret_cast<const u4*>(qp + 16 * j);
+  }
+  const float f = a.scale * 1.4426950408889634f;
+
+  f16v acc[NB];
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+  float m = kNegInf, l = 0.0f;
+
+  const uint16_t* kp = a.k + q0 * a.k_stride + (int64_t)kvh * D;
+  const uint16_t* vp = a.v + q0 * a.v_stride + (int64_t)kvh * D;
+  u4 kreg[LD], vreg[LD];
+  auto fetch = [&](int kt) {
+#pragma unroll
+    for (int x = 0; x < LD; ++x) {
+      const int p = x * 256 + threadIdx.x, t = p / NC, j = p % NC;
+      const int64_t tok = min((int64_t)kt * KT + t, n - 1);  // past the sequence: its last key again
+      kreg[x] = *reinterpret_cast<const u4*>(kp + tok * a.k_stride + 8 * j);
+      vreg[x] = *reinterpret_cast<const u4*>(vp + tok * a.v_stride + 8 * j);
+    }
+  };
+  const int64_t wg_first = R0 / G;
+  auto stage = [&](int kt) {
+    const int buf = kt & 1;
+    if ((int64_t)kt * KT + KT - 1 > wg_first) {
+      bool any = false;
+#pragma unroll
+      for (int x = 0; x < LD; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) any |= odd_pair<BF>(vreg[x][i]);
+      if (any) odd = 1;
+    }
+    u4* kd = tile + buf * (2 * KT * NC);
+    u4* vd = kd + KT * NC;
+#pragma unroll
+    for (int x = 0; x < LD; ++x) {
+      const int p = x * 256 + threadIdx.x, t = p / NC, j = p % NC;
+      kd[t * NC + k_chunk<D>(t, j)] = kreg[x];
+      vd[t * NC + v_chunk<D>(t, j)] = vreg[x];
+    }
+  };
+
+  fetch(0);
+  if (threadIdx.x == 0) odd = 0;
+  __syncthreads();
+  stage(0);
+  __syncthreads();
+  for (int kt = 0; kt < tiles; ++kt) {
+    if (kt + 1 < tiles) fetch(kt + 1);
+    const u4* kd = tile + (kt & 1) * (2 * KT * NC);
+    const u4* vd = kd + KT * NC;
+    f16v s[TB];
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[tb][i] = 0.0f;
+      const int t = 32 * tb + r;
+#pragma unroll
+      for (int j = 0; j < NS; ++j) s[tb] = mfma32<BF>(kd[t * NC + k_chunk<D>(t, 2 * j + hf)], qf[j], s[tb]);
+    }
+    const int64_t key0 = (int64_t)kt * KT;
+    const bool partly = key0 + KT - 1 > first;
+    if (partly) {
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (key0 + 32 * tb + 8 * (i / 4) + 4 * hf + i % 4 > qi) s[tb][i] = kNegInf;
+    }
+    float mx = kNegInf;
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[tb][i]);
+    mx = max_over_halves(mx) * f;
+    if (__ballot(mx > m)) {
+      const float mn = fmaxf(m, mx);
+      const float al = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= al;
+#pragma unroll
+      for (int d = 0; d < NB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[d][i] *= al;
+    }
+    const float ms = m == kNegInf ? 0.0f : m;
+    u4 pf[2 * TB];
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][i], f, -ms));
+        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][i + 1], f, -ms));
+        l += p0 + p1;
+        pf[2 * tb + i / 8][(i % 8) / 2] = pack_pair<BF>(p0, p1);
+      }
+    auto v_operand = [&](int kk, int d) {
+      u2 half[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int t = 16 * kk + 8 * x + 4 * hf + (lane & 15) / 4;
+        const int j = 4 * d + 2 * ((lane >> 4) & 1) + (lane & 3) / 2;
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(vd + t * NC + v_chunk<D>(t, j)) + 4 * (lane & 1);
+        half[x] = __builtin_bit_cast(
+            u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p));
+      }
+      return u4{half[0][0], half[0][1], half[1][0], half[1][1]};
+    };
+    if (!partly || __builtin_amdgcn_readfirstlane(odd) == 0) {
+#pragma unroll
+      for (int kk = 0; kk < 2 * TB; ++kk)
+#pragma unroll
+        for (int d = 0; d < NB; ++d) acc[d] = mfma32<BF>(v_operand(kk, d), pf[kk], acc[d]);
+    } else {
+      constexpr uint32_t one = BF ? 0x3f80u : 0x3c00u, top = BF ? 0x7f80u : 0x7c00u;
+      for (int kk = 0; kk < 2 * TB; ++kk) {
+        u4 p, seen;
+#pragma unroll
+        for (int k = 0; k < 2 * TB; ++k)
+          if (k == kk) p = pf[k];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool see = key0 + 16 * kk + 8 * (i / 4) + 4 * hf + i % 4 <= qi;
+          seen[i / 2] = (i % 2 ? seen[i / 2] : 0) | (see ? one << (16 * (i % 2)) : 0);
+        }
+#pragma unroll
+        for (int d = 0; d < NB; ++d) {
+          u4 v = v_operand(kk, d), plus, minus;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            plus[i] = minus[i] = 0;
+#pragma unroll
+            for (int x = 0; x < 32; x += 16) {
+              const uint32_t h = v[i] >> x & 0xffffu;
+              if ((h & top) != top) continue;
+              const bool nan = (h & 0x7fffu) != top;
+              if (nan || !(h >> 15)) plus[i] |= one << x;
+              if (nan || h >> 15) minus[i] |= one << x;
+              v[i] &= 0xffff0000u >> x;
+            }
+          }
+          acc[d] = mfma32<BF>(v, p, acc[d]);
+          f16v np, nm;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) np[i] = nm[i] = 0.0f;
+          np = mfma32<BF>(plus, seen, np);
+          nm = mfma32<BF>(minus, seen, nm);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (np[i] > 0.0f) acc[d][i] += -kNegInf;
+            if (nm[i] > 0.0f) acc[d][i] += kNegInf;
+          }
+        }
+      }
+    }
+    if (kt + 1 < tiles) stage(kt + 1);
+    __syncthreads();
+  }
+  {
+    const uint32_t u = __builtin_bit_cast(uint32_t, l);
+    auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    l = __builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]);
+  }
+  if (Rw + r >= n * G) return;
+  const float inv = 1.0f / l;
+  const int64_t at = (q0 + qi) * a.Hq + head;
+  uint16_t* o = a.out + at * D;
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const u2 w = {pack_pair<BF>(acc[d][i] * inv, acc[d][i + 1] * inv),
+                    pack_pair<BF>(acc[d][i + 2] * inv, acc[d][i + 3] * inv)};
+      *reinterpret_cast<u2*>(o + 32 * d + 2 * i + 4 * hf) = w;
+    }
+  if (a.lse && hf == 0) a.lse[at] = (m + __builtin_log2f(l)) * 0.6931471805599453f;
+}
+
+template <int D, bool BF>
+hipError_t launch_one(const PromptAttnArgs& a, hipStream_t stream) {
+  static std::atomic<uint64_t> raised{0};
+  constexpr size_t lds = (size_t)2 * 2 * (D == 256 ? 32 : 64) * D * 2;
+  const hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&prompt_attn_kernel<D, BF>), lds, raised);
+  if (e != hipSuccess) return e;
+  const int64_t slots = a.T * (a.Hq / a.Hkv) / kRows + a.B;
+  prompt_attn_kernel<D, BF><<<(unsigned)(slots * a.Hkv), 256, lds, stream>>>(a, slots);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_d(const PromptAttnArgs& a, hipStream_t stream) {
+  return a.dtype == 1 ? launch_one<D, true>(a, stream) : launch_one<D, false>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_prompt_attn(const PromptAttnArgs& a, hipStream_t stream) {
+  if (a.D == 64) return launch_d<64>(a, stream);
+  if (a.D == 128) return launch_d<128>(a, stream);
+  return launch_d<256>(a, stream);
+}
+
+}  // namespace wq
