@@ -22,9 +22,9 @@
 //
 // A weight of exactly 0 does not hide a value that is no number (0 * inf), and
 // one V operand serves rows that see a key and rows that do not.  So a tile that
-// some rows see only in part is looked through for such values as it is staged;
-// if there are any, they enter the product as 0 and reach the rows that do see
-// them as an infinity of their sign (a NaN: of both) from two more products.
+// some rows see only in part is looked through as it is staged: an infinity or
+// a NaN in its values enters the product as 0 and is added, after the outputs are
+// stored, to the rows that do see it.
 //
 // Workgroups find their sequence from the device's starts: sequence b owns the
 // tile slots from floor(start_b G / 128) + b on, at least as many as it has
@@ -44,6 +44,7 @@ typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kRows = 128;
+constexpr float kLag = 8.0f;
 
 template <bool BF>
 __device__ __forceinline__ f16v mfma32(u4 x, u4 y, f16v c) {
@@ -71,11 +72,21 @@ __device__ __forceinline__ float max_over_halves(float v) {
   return fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
 }
 
-// Whether one of the two 16-bit values of a word is infinite or NaN.
+// Ones over each 16-bit half of a word that holds a finite value.
 template <bool BF>
-__device__ __forceinline__ bool odd_pair(uint32_t w) {
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
   constexpr uint32_t lo = BF ? 0x7f80u : 0x7c00u, hi = lo << 16;
-  return (w & lo) == lo || (w & hi) == hi;
+  return ((w & lo) == lo ? 0u : 0xffffu) | ((w & hi) == hi ? 0u : 0xffff0000u);
+}
+template <bool BF>
+__device__ __forceinline__ float to_f32(uint32_t h) {
+  return BF ? __builtin_bit_cast(float, h << 16) : f16_bits_to_f32((uint16_t)h);
+}
+
+// Four 16-bit values of each lane of 16, transposed in blocks of 4 x 16: lane i
+// gets value i % 4 of lanes i / 4, i / 4 + 4, i / 4 + 8, i / 4 + 12.
+__device__ __forceinline__ u2 read_transposed(const u2* p) {
+  return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p));
 }
 
 template <int D>
@@ -115,7 +126,6 @@ __global__ __launch_bounds__(256, 2) void prompt_attn_kernel(PromptAttnArgs a, i
   constexpr int NB = D / 32;                // output blocks of 32 channels
   constexpr int LD = KT * NC / 256;         // chunks a thread stages of K, and of V
   extern __shared__ __attribute__((aligned(16))) u4 tile[];  // [2][K, V][KT * NC]
-  __shared__ uint32_t odd;  // a tile with hidden keys held an infinity or a NaN in V
   const int lane = threadIdx.x & 63, r = lane & 31, hf = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = a.Hq / a.Hkv;
@@ -152,7 +162,9 @@ __global__ __launch_bounds__(256, 2) void prompt_attn_kernel(PromptAttnArgs a, i
 
   const uint16_t* kp = a.k + q0 * a.k_stride + (int64_t)kvh * D;
   const uint16_t* vp = a.v + q0 * a.v_stride + (int64_t)kvh * D;
+  const int64_t wg_first = R0 / G;  // every row of the workgroup sees keys 0..wg_first
   u4 kreg[LD], vreg[LD];
+  uint32_t odd = 0;
   auto fetch = [&](int kt) {
 #pragma unroll
     for (int x = 0; x < LD; ++x) {
@@ -162,16 +174,16 @@ __global__ __launch_bounds__(256, 2) void prompt_attn_kernel(PromptAttnArgs a, i
       vreg[x] = *reinterpret_cast<const u4*>(vp + tok * a.v_stride + 8 * j);
     }
   };
-  const int64_t wg_first = R0 / G;
-  auto stage = [&](int kt) {
-    const int buf = kt & 1;
+  auto stage = [&](int kt, int buf) {
     if ((int64_t)kt * KT + KT - 1 > wg_first) {
-      bool any = false;
 #pragma unroll
       for (int x = 0; x < LD; ++x)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) any |= odd_pair<BF>(vreg[x][i]);
-      if (any) odd = 1;
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t keep = finite_halves<BF>(vreg[x][i]);
+          odd |= ~keep;
+          vreg[x][i] &= keep;
+        }
     }
     u4* kd = tile + buf * (2 * KT * NC);
     u4* vd = kd + KT * NC;
@@ -182,33 +194,38 @@ __global__ __launch_bounds__(256, 2) void prompt_attn_kernel(PromptAttnArgs a, i
       vd[t * NC + v_chunk<D>(t, j)] = vreg[x];
     }
   };
+  // the lane's places in a tile: of K, chunk 2 j + hf of token r (a block of 32
+  // tokens further on: the same chunk); of V, the 8 bytes it hands to a
+  // transposed read of channels 32 d.. (16 kk + 8 x tokens further on: the same)
+  int kat[NS], vat[NB];
+#pragma unroll
+  for (int j = 0; j < NS; ++j) kat[j] = r * NC + k_chunk<D>(r, 2 * j + hf);
+#pragma unroll
+  for (int d = 0; d < NB; ++d) {
+    const int t = 4 * hf + (lane & 15) / 4;
+    vat[d] = 2 * (t * NC + v_chunk<D>(t, 4 * d + 2 * ((lane >> 4) & 1) + (lane & 3) / 2)) + (lane & 1);
+  }
 
-  fetch(0);
-  if (threadIdx.x == 0) odd = 0;
-  __syncthreads();
-  stage(0);
-  __syncthreads();
-  for (int kt = 0; kt < tiles; ++kt) {
+  auto step = [&](int kt, int buf) {
     if (kt + 1 < tiles) fetch(kt + 1);
-    const u4* kd = tile + (kt & 1) * (2 * KT * NC);
-    const u4* vd = kd + KT * NC;
+    const u4* kd = tile + buf * (2 * KT * NC);
+    const u2* vd = reinterpret_cast<const u2*>(kd + KT * NC);
     f16v s[TB];
 #pragma unroll
     for (int tb = 0; tb < TB; ++tb) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[tb][i] = 0.0f;
-      const int t = 32 * tb + r;
 #pragma unroll
-      for (int j = 0; j < NS; ++j) s[tb] = mfma32<BF>(kd[t * NC + k_chunk<D>(t, 2 * j + hf)], qf[j], s[tb]);
+      for (int j = 0; j < NS; ++j) s[tb] = mfma32<BF>(kd[32 * tb * NC + kat[j]], qf[j], s[tb]);
     }
     const int64_t key0 = (int64_t)kt * KT;
-    const bool partly = key0 + KT - 1 > first;
-    if (partly) {
+    if (key0 + KT - 1 > first) {
+      const int seen = (int)min(qi - key0, (int64_t)KT);  // the row sees the tile's keys 0..seen
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (key0 + 32 * tb + 8 * (i / 4) + 4 * hf + i % 4 > qi) s[tb][i] = kNegInf;
+          if (32 * tb + 8 * (i / 4) + 4 * hf + i % 4 > seen) s[tb][i] = kNegInf;
     }
     float mx = kNegInf;
 #pragma unroll
@@ -216,7 +233,8 @@ __global__ __launch_bounds__(256, 2) void prompt_attn_kernel(PromptAttnArgs a, i
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[tb][i]);
     mx = max_over_halves(mx) * f;
-    if (__ballot(mx > m)) {
+    // the maximum in use may lag the true one by kLag: weights up to 2^kLag
+    if (__ballot(mx > m + kLag)) {
       const float mn = fmaxf(m, mx);
       const float al = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
       m = mn;
@@ -237,86 +255,57 @@ __global__ __launch_bounds__(256, 2) void prompt_attn_kernel(PromptAttnArgs a, i
         l += p0 + p1;
         pf[2 * tb + i / 8][(i % 8) / 2] = pack_pair<BF>(p0, p1);
       }
-    auto v_operand = [&](int kk, int d) {
-      u2 half[2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int t = 16 * kk + 8 * x + 4 * hf + (lane & 15) / 4;
-        const int j = 4 * d + 2 * ((lane >> 4) & 1) + (lane & 3) / 2;
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(vd + t * NC + v_chunk<D>(t, j)) + 4 * (lane & 1);
-        half[x] = __builtin_bit_cast(
-            u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p));
+    for (int kk = 0; kk < 2 * TB; ++kk)
+#pragma unroll
+      for (int d = 0; d < NB; ++d) {
+        const u2 lo = read_transposed(vd + 2 * (16 * kk * NC) + vat[d]);
+        const u2 hi = read_transposed(vd + 2 * ((16 * kk + 8) * NC) + vat[d]);
+        acc[d] = mfma32<BF>(u4{lo[0], lo[1], hi[0], hi[1]}, pf[kk], acc[d]);
       }
-      return u4{half[0][0], half[0][1], half[1][0], half[1][1]};
-    };
-    if (!partly || __builtin_amdgcn_readfirstlane(odd) == 0) {
-#pragma unroll
-      for (int kk = 0; kk < 2 * TB; ++kk)
-#pragma unroll
-        for (int d = 0; d < NB; ++d) acc[d] = mfma32<BF>(v_operand(kk, d), pf[kk], acc[d]);
-    } else {
-      constexpr uint32_t one = BF ? 0x3f80u : 0x3c00u, top = BF ? 0x7f80u : 0x7c00u;
-      for (int kk = 0; kk < 2 * TB; ++kk) {
-        u4 p, seen;
-#pragma unroll
-        for (int k = 0; k < 2 * TB; ++k)
-          if (k == kk) p = pf[k];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool see = key0 + 16 * kk + 8 * (i / 4) + 4 * hf + i % 4 <= qi;
-          seen[i / 2] = (i % 2 ? seen[i / 2] : 0) | (see ? one << (16 * (i % 2)) : 0);
-        }
-#pragma unroll
-        for (int d = 0; d < NB; ++d) {
-          u4 v = v_operand(kk, d), plus, minus;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            plus[i] = minus[i] = 0;
-#pragma unroll
-            for (int x = 0; x < 32; x += 16) {
-              const uint32_t h = v[i] >> x & 0xffffu;
-              if ((h & top) != top) continue;
-              const bool nan = (h & 0x7fffu) != top;
-              if (nan || !(h >> 15)) plus[i] |= one << x;
-              if (nan || h >> 15) minus[i] |= one << x;
-              v[i] &= 0xffff0000u >> x;
-            }
-          }
-          acc[d] = mfma32<BF>(v, p, acc[d]);
-          f16v np, nm;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) np[i] = nm[i] = 0.0f;
-          np = mfma32<BF>(plus, seen, np);
-          nm = mfma32<BF>(minus, seen, nm);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (np[i] > 0.0f) acc[d][i] += -kNegInf;
-            if (nm[i] > 0.0f) acc[d][i] += kNegInf;
-          }
-        }
-      }
-    }
-    if (kt + 1 < tiles) stage(kt + 1);
+    if (kt + 1 < tiles) stage(kt + 1, buf ^ 1);
     __syncthreads();
+  };
+
+  fetch(0);
+  stage(0, 0);
+  __syncthreads();
+  for (int kt = 0; kt < tiles; kt += 2) {
+    step(kt, 0);
+    if (kt + 1 < tiles) step(kt + 1, 1);
   }
   {
     const uint32_t u = __builtin_bit_cast(uint32_t, l);
     auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
     l = __builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]);
   }
-  if (Rw + r >= n * G) return;
-  const float inv = 1.0f / l;
-  const int64_t at = (q0 + qi) * a.Hq + head;
-  uint16_t* o = a.out + at * D;
+  if (Rw + r < n * G) {
+    const float inv = 1.0f / l;
+    const int64_t at = (q0 + qi) * a.Hq + head;
+    uint16_t* o = a.out + at * D;
 #pragma unroll
-  for (int d = 0; d < NB; ++d)
+    for (int d = 0; d < NB; ++d)
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const u2 w = {pack_pair<BF>(acc[d][i] * inv, acc[d][i + 1] * inv),
-                    pack_pair<BF>(acc[d][i + 2] * inv, acc[d][i + 3] * inv)};
-      *reinterpret_cast<u2*>(o + 32 * d + 2 * i + 4 * hf) = w;
+      for (int i = 0; i < 16; i += 4) {
+        const u2 w = {pack_pair<BF>(acc[d][i] * inv, acc[d][i + 1] * inv),
+                      pack_pair<BF>(acc[d][i + 2] * inv, acc[d][i + 3] * inv)};
+        *reinterpret_cast<u2*>(o + 32 * d + 2 * i + 4 * hf) = w;
+      }
+    if (a.lse && hf == 0) a.lse[at] = (m + __builtin_log2f(l)) * 0.6931471805599453f;
+  }
+  // infinities and NaNs of the partly seen tiles: a thread per channel adds them,
+  // key by key, to the stored rows that see the key
+  if (__syncthreads_or(odd != 0) && threadIdx.x < D) {
+    const int ch = threadIdx.x;
+    for (int64_t t = (wg_first + 1) / KT * KT; t <= last / G; ++t) {
+      const uint32_t v = vp[t * a.v_stride + ch];
+      if (finite_halves<BF>(v) == 0xffffffffu) continue;
+      for (int64_t x = max(t * G, R0); x <= last; ++x) {
+        uint16_t* o = a.out + ((q0 + x / G) * a.Hq + (int64_t)kvh * G + x % G) * D + ch;
+        *o = (uint16_t)pack_pair<BF>(to_f32<BF>(*o) + to_f32<BF>(v), 0.0f);
+      }
     }
-  if (a.lse && hf == 0) a.lse[at] = (m + __builtin_log2f(l)) * 0.6931471805599453f;
+  }
 }
 
 template <int D, bool BF>
