@@ -573,7 +573,7 @@ int check_kv_attn(int dtype, int64_t T, int Hq, int Hkv, int D, int64_t B, int p
                   int64_t max_queries) {
   const int st = check_heads(dtype, T, Hq, Hkv, D);
   if (st) return st;
-  if (B < 0 || B > (1 << 24) || max_context < 0 || max_context >= kMaxCount || max_queries < 0 || max_queries > T)
+  if (B < 0 || B > (1 << 24) || max_context < 0 || max_context > (1 << 30) || max_queries < 0 || max_queries > T)
     return WQ_EINVAL;
   if (((int64_t)Hkv * D) % 128 != 0 || page_size < 1 || (page_size & (page_size - 1)) != 0) return WQ_EUNSUPPORTED;
   // grids stay below 2^31 workgroups

@@ -10,8 +10,9 @@
 // (K) and its softmax weight in fp32 before that weight is rounded to fp16 (V).
 // So the codes are decoded with the GEMV's four AND-ORs and four packed
 // subtractions a word and nothing is rounded but q (bf16 rows are moved into
-// fp16's range by a power of two) and the weights p_t s_t (fp16, 2^-12 of each
-// at most, after a power of two that puts the largest scale so far below 1).
+// fp16's range by a power of two) and the weights p_t s_t (to fp16, half a step
+// of 2^-11 at most: their reference point is the largest score plus the exponent
+// of the largest V scale so far, so the large ones lie near 1 for any scale).
 //
 // Both products are computed transposed, S^T = K q^T and O^T = V^T P^T, with
 // v_mfma_f32_16x16x32_f16 and 16 query rows as its columns (the heads of one KV
@@ -42,7 +43,10 @@ namespace {
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 constexpr float kNegInf = -__builtin_inff();
-constexpr uint32_t kTokenOff = 0x80000000u;  // metadata word of a token that is not attended
+// A row's reference point may lag its largest weight by this many powers of two
+// (fp16 weights stay below 2^9, the fp32 sums far below their limits), so that it
+// rarely moves.
+constexpr float kLag = 8.0f;
 
 struct KvPlan {
   int HW;          // KV heads of a workgroup (its W / HW waves per head take different tiles)
@@ -108,64 +112,65 @@ template <int D>
 struct Tile {
   static constexpr int NB = D == 256 ? 2 : 1;   // cache blocks of a head
   static constexpr int KW = D / 32;             // code words of a K lane and 16-token group
-  static constexpr int VW = D == 256 ? 2 : 1;   // words (D = 64: half words) of a V lane and token
   uint32_t k[2][KW];
-  uint32_t v[8][VW];
-  uint32_t s[NB];  // lanes 0..31: K scale of token l, lanes 32..63: V scale of token l - 32
-  uint32_t z;      // the zero-point byte beside it
-  bool off;        // the lane's token is not attended (no such page, or past the context)
+  uint32_t v[8][NB];  // (D = 64: half words)
+  uint32_t s[NB];     // lanes 0..31: K scale of token l, lanes 32..63: V scale of token l - 32
+  uint32_t z;         // the zero-point byte beside it
+  bool ok;            // the tile's page (small pages: the page of the lane's token) exists
 };
 
 template <int D, int RT, int W, bool P32>
-__global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? 2 * W / 4 : W / 4) void kv_attn_kernel(KvAttnArgs a, int HW, int64_t chunk, int KS,
-                                                                int rtiles) {
-  constexpr int NB = Tile<D>::NB, KW = Tile<D>::KW, VW = Tile<D>::VW;
-  constexpr int NS = D / 32;             // MFMA steps of a score
-  constexpr int NE = D / 16;             // MFMAs of an output tile: 16 channels each
+__global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? W / 2 : W / 4) void kv_attn_kernel(KvAttnArgs a, int HW,
+                                                                                             int chunk, int KS,
+                                                                                             int rtiles) {
+  constexpr int NB = Tile<D>::NB;
+  constexpr int NS = D / 32;  // MFMA steps of a score
+  constexpr int SB = NS / NB;
+  constexpr int NE = D / 16;  // MFMAs of an output tile: 16 channels each
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
-  const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+  const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4, ml = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int TW = W / HW, tg = wave / HW;
-  const int HG = a.Hkv / HW;
-  int64_t id = blockIdx.x;
-  const int rt0 = (int)(id % rtiles);
-  id /= rtiles;
-  const int hg = (int)(id % HG);
+  const int TW = W / HW, tg = wave / HW, hw = wave - tg * HW;
+  const uint32_t HG = a.Hkv / HW;
+  uint32_t id = blockIdx.x;
+  const int rt0 = id % (uint32_t)rtiles;
+  id /= (uint32_t)rtiles;
+  const int hg = id % HG;
   id /= HG;
-  const int split = (int)(id % KS);
-  const int b = (int)(id / KS);
-  const int h = hg * HW + wave % HW;
+  const int split = id % (uint32_t)KS;
+  const int b = id / (uint32_t)KS;
+  const int h = hg * HW + hw;
   const int G = a.Hq / a.Hkv;
 
-  int64_t q0 = b, nq = 1;
+  int q0 = b, nq = 1;
   if (a.q_starts) {
-    q0 = max((int64_t)a.q_starts[b], (int64_t)0);
-    nq = min((int64_t)a.q_starts[b + 1], a.T) - q0;
-    nq = min(nq, a.max_queries);
+    q0 = max(a.q_starts[b], 0);
+    nq = (int)min(min((int64_t)a.q_starts[b + 1], a.T) - q0, a.max_queries);
   }
-  const int64_t len = min((int64_t)a.lens[b], a.max_context);
-  const int64_t row0 = (int64_t)rt0 * (16 * RT);
-  if (row0 >= nq * G) return;
-  if (split > 0 && split * chunk >= len) return;
+  const int len = (int)min((int64_t)a.lens[b], a.max_context);
+  const int row0 = rt0 * (16 * RT), rows = nq * G;
+  if (row0 >= rows) return;
+  if (split > 0 && split * (int64_t)chunk >= len) return;
   const bool whole = len <= chunk;  // the sequence is not split
-  // rows of this workgroup see at most the first `top` tokens, and all of its
-  // rows see the first `low`
-  const int64_t row1 = min(row0 + 16 * RT, nq * G) - 1;
-  const int64_t top = max(len - nq + row1 / G + 1, (int64_t)0), low = len - nq + row0 / G + 1;
-  const int64_t t_begin = (int64_t)split * chunk, t_end = min(t_begin + chunk, top);
+  const int row1 = min(row0 + 16 * RT, rows) - 1;
+  // of these rows' tokens: what the last row sees ends the walk, what the first
+  // sees ends the tiles that need no mask
+  const int t_begin = split * chunk;
+  const int t_end = min(min(t_begin + chunk, len), len - nq + (int)((uint32_t)row1 / (uint32_t)G) + 1);
+  const int low = min(t_end, len - nq + (int)((uint32_t)row0 / (uint32_t)G) + 1);
 
   // the wave's queries, as the B operand of the scores: lane (r, c) channels
   // 32 c + 8 j (D = 64: 16 c + 8 j) of each block, brought into fp16's range by
   // the power of two that takes the row's largest value into [1, 2)
   h8 qf[RT][NS];
-  float f[RT];            // score of a row in units of log2: raw * f
-  int64_t lim[RT];        // tokens the row sees
+  float f[RT];   // score of a row in units of log2: raw * f
+  int lim[RT];   // tokens the row sees, of those of this walk
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    const int64_t row = min(row0 + 16 * t + r, nq * G - 1);  // rows past the end repeat the last, not stored
-    const int64_t qi = row / G;
-    lim[t] = len - nq + qi + 1;
-    const uint16_t* qp = a.q + (q0 + qi) * a.q_stride + ((int64_t)h * G + row % G) * D;
+    const uint32_t row = min(row0 + 16 * t + r, rows - 1);  // rows past the end repeat the last, not stored
+    const uint32_t qi = row / (uint32_t)G;
+    lim[t] = min(t_end, len - nq + (int)qi + 1);
+    const uint16_t* qp = a.q + (int64_t)(q0 + qi) * a.q_stride + (int64_t)(h * G + (int)(row - qi * G)) * D;
     u4 raw[NS];
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
@@ -173,14 +178,22 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? 2 * W / 4 : W / 4) vo
       raw[j] = *reinterpret_cast<const u4*>(qp + ch);
     }
     float x[NS][8], top_q = 0.0f;
+    if (a.dtype == 1) {
+#pragma unroll
+      for (int j = 0; j < NS; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[j][e] = __builtin_bit_cast(float, e % 2 ? raw[j][e / 2] & 0xffff0000u : raw[j][e / 2] << 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NS; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[j][e] = (float)__builtin_bit_cast(h8, raw[j])[e];
+    }
 #pragma unroll
     for (int j = 0; j < NS; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t hw = raw[j][e / 2] >> (16 * (e % 2)) & 0xffffu;
-        x[j][e] = a.dtype == 1 ? __builtin_bit_cast(float, hw << 16) : f16_bits_to_f32((uint16_t)hw);
-        top_q = fmaxf(top_q, fabsf(x[j][e]));
-      }
+      for (int e = 0; e < 8; ++e) top_q = fmaxf(top_q, fabsf(x[j][e]));
     top_q = max_over_rows16(top_q);
     int ex = (int)(__builtin_bit_cast(uint32_t, top_q) >> 23) - 127;
     ex = min(max(ex, -126), 126);  // zeros, subnormals and infinities: the nearest power
@@ -194,7 +207,7 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? 2 * W / 4 : W / 4) vo
   }
 
   f4 acc[RT][NE];
-  float m[RT], l[RT];
+  float m[RT], l[RT];  // weights are 2^(score - m); m follows the largest score + v_exp
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     m[t] = kNegInf;
@@ -202,58 +215,64 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? 2 * W / 4 : W / 4) vo
 #pragma unroll
     for (int e = 0; e < NE; ++e) acc[t][e] = f4{0, 0, 0, 0};
   }
-  float v_top = 0.0f, v_down = 1.0f;  // V scales so far lie below v_top = 1 / v_down (a power of two)
+  // V scales so far are at most v_top (fp16 bits) < 2^v_exp
+  uint32_t v_top = 0;
+  float v_exp = -25.0f;
 
-  const int64_t rowb = (int64_t)a.Hkv * D / 2;  // code bytes of a cache row
-  const int nbt = a.Hkv * D / 128, zb = (nbt + 1) / 2;
-  const int blk = h * D / 128;                   // first block of the head
-  const int64_t hoff = (int64_t)h * D / 2;       // its code bytes
-  const int zshift = (D == 256) ? 0 : (blk & 1) * 4;
+  const uint32_t rowb = (uint32_t)a.Hkv * (D / 2);  // code bytes of a cache row
+  const uint32_t nbt = (uint32_t)a.Hkv * D / 128, zb = (nbt + 1) / 2;
+  const uint32_t blk = (uint32_t)h * D / 128;       // first block of the head
+  const int zshift = D == 256 ? 0 : (blk & 1) * 4;
   const int lg = 31 - __builtin_clz(a.page);
-  const int64_t pages = a.S >> lg;
+  const int pages = (int)(a.S >> lg);
   const int32_t* table = a.table + (int64_t)b * a.table_width;
   uint32_t* meta = lds + wave * (64 * NB);
-  const int ml = lane & 31;
+  const uint8_t* kc = a.k_codes + (uint32_t)h * (D / 2);
+  const uint8_t* vc = a.v_codes + (uint32_t)h * (D / 2);
+  const uint16_t* sp = (lane < 32 ? a.k_s : a.v_s) + blk + (P32 ? ml * nbt : 0);
+  const uint8_t* zp = (lane < 32 ? a.k_zp : a.v_zp) + blk / 2 + (P32 ? ml * zb : 0);
+  const uint32_t k_at = (D == 64 ? 8 : 16) * c + (P32 ? r * rowb : 0);
+  const uint32_t v_at = (D == 64 ? 2 : 4) * r + (P32 ? 4 * c * rowb : 0);
 
   // page entries of a tile: one of the whole tile (P32) or one of lane ml's token
-  auto page_entry = [&](int64_t tk) -> int {
+  auto page_entry = [&](int tk) -> int {
     if constexpr (P32) return table[min(tk, t_end - 1) >> lg];
     return table[min(tk + ml, t_end - 1) >> lg];
   };
-  auto load = [&](Tile<D>& T, int64_t tk, int pg) {
-    int64_t krow[2], vrow[8], mrow;
+  auto load = [&](Tile<D>& T, int tk, int pg) {
+    const uint8_t *kr[2], *vr[8];
+    const bool page_ok = pg >= 0 && pg < pages;
+    T.ok = page_ok;
     if constexpr (P32) {
-      const bool ok = pg >= 0 && pg < pages;
-      const int64_t base = ok ? ((int64_t)pg << lg) + (tk & (a.page - 1)) : 0;
-      T.off = !ok || tk + ml >= t_end;
-      // a tile lies inside one page; with no page it reads row 0 alone
-      const int64_t step = ok ? 1 : 0;
-      mrow = base + step * ml;
+      // the tile lies inside one page (none: it reads the first rows of the cache)
+      const int64_t base = page_ok ? ((int64_t)pg << lg) + (tk & (a.page - 1)) : 0;
 #pragma unroll
-      for (int g = 0; g < 2; ++g) krow[g] = base + step * (16 * g + r);
+      for (int g = 0; g < 2; ++g) kr[g] = kc + (base + 16 * g) * rowb;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) vrow[i] = base + step * (16 * (i / 4) + 4 * c + i % 4);
+      for (int i = 0; i < 8; ++i) vr[i] = vc + (base + 16 * (i / 4) + i % 4) * rowb;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) T.s[n] = (sp + base * nbt)[n];
+      T.z = (zp + base * zb)[0];
     } else {
-      const bool ok = pg >= 0 && pg < pages && tk + ml < t_end;
-      T.off = !ok;
-      const int own = ok ? (int)(((int64_t)pg << lg) + ((tk + ml) & (a.page - 1))) : 0;
-      mrow = own;
+      const int own = !page_ok ? 0 : (pg << lg) + ((tk + ml) & (a.page - 1));
 #pragma unroll
-      for (int g = 0; g < 2; ++g) krow[g] = __shfl(own, 16 * g + r);
+      for (int g = 0; g < 2; ++g) kr[g] = kc + (uint64_t)(uint32_t)__shfl(own, 16 * g + r) * rowb;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) vrow[i] = __shfl(own, 16 * (i / 4) + 4 * c + i % 4);
+      for (int i = 0; i < 8; ++i) vr[i] = vc + (uint64_t)(uint32_t)__shfl(own, 16 * (i / 4) + 4 * c + i % 4) * rowb;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) T.s[n] = (sp + (uint64_t)(uint32_t)own * nbt)[n];
+      T.z = (zp + (uint64_t)(uint32_t)own * zb)[0];
     }
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const uint8_t* p = a.k_codes + krow[g] * rowb + hoff;
       if constexpr (D == 64) {
-        const u2 w = *reinterpret_cast<const u2*>(p + 8 * c);
+        const u2 w = *reinterpret_cast<const u2*>(kr[g] + k_at);
         T.k[g][0] = w[0];
         T.k[g][1] = w[1];
       } else {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-          const u4 w = *reinterpret_cast<const u4*>(p + 64 * n + 16 * c);
+          const u4 w = *reinterpret_cast<const u4*>(kr[g] + k_at + 64 * n);
 #pragma unroll
           for (int j = 0; j < 4; ++j) T.k[g][4 * n + j] = w[j];
         }
@@ -261,54 +280,47 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? 2 * W / 4 : W / 4) vo
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint8_t* p = a.v_codes + vrow[i] * rowb + hoff;
       if constexpr (D == 64) {
-        T.v[i][0] = *reinterpret_cast<const uint16_t*>(p + 2 * r);
+        T.v[i][0] = *reinterpret_cast<const uint16_t*>(vr[i] + v_at);
       } else {
 #pragma unroll
-        for (int n = 0; n < NB; ++n) T.v[i][n] = *reinterpret_cast<const uint32_t*>(p + 64 * n + 4 * r);
+        for (int n = 0; n < NB; ++n) T.v[i][n] = *reinterpret_cast<const uint32_t*>(vr[i] + v_at + 64 * n);
       }
     }
-    const uint16_t* sp = (lane < 32 ? a.k_s : a.v_s) + mrow * nbt + blk;
-#pragma unroll
-    for (int n = 0; n < NB; ++n) T.s[n] = sp[n];
-    T.z = ((lane < 32 ? a.k_zp : a.v_zp) + mrow * zb)[blk / 2];
   };
 
-  auto compute = [&](Tile<D>& T, int64_t tk) {
+  auto compute = [&](Tile<D>& T, int tk) {
     // scale (low half) and zero-point (bits 16..19) of every token and cache
     // through LDS to the lanes that need them; a token that is not attended has
     // scale and zero-point 0, whatever its cache row holds
+    const bool off = !T.ok || tk + ml >= t_end;
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      const uint32_t zp = (D == 256 ? T.z >> (4 * n) : T.z >> zshift) & 15u;
-      meta[64 * n + lane] = T.off ? kTokenOff : (T.s[n] | (zp << 16));
-    }
-    f4 sc[RT][2][NB];
-    float ksc[NB][8];
-    bool any_off = false;
-    uint32_t km[NB][8];
+      const uint32_t z = (D == 256 ? T.z >> (4 * n) : T.z >> zshift) & 15u;
+      const uint32_t w = off ? 0u : T.s[n] | (z << 16);
+      meta[64 * n + lane] = w;
+      // a V scale above all so far (rare): the next power of two from the largest
+      if (__ballot(lane >= 32 && (w & 0xffffu) > v_top)) {
+        uint32_t top = lane >= 32 ? w & 0x7fffu : 0u;
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const u4 w = *reinterpret_cast<const u4*>(meta + 64 * n + 16 * g + 4 * c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          km[n][4 * g + i] = w[i];
-          ksc[n][4 * g + i] = f16_bits_to_f32((uint16_t)w[i]);
-        }
+        for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+        top = __builtin_amdgcn_readfirstlane(top);
+        v_exp = (float)((int)(__builtin_bit_cast(uint32_t, f16_bits_to_f32((uint16_t)top)) >> 23) - 126);
+        v_top = top >> 10 ? top | 0x3ffu : 0xffffffffu >> __builtin_clz(top);
       }
+    }
+    // tokens of small pages that do not exist, a bit each (P32: all or none)
+    const uint32_t gone = P32 ? 0u : ~(uint32_t)__ballot(T.ok);
+    const bool masked = tk + 32 > low || (P32 ? !T.ok : gone != 0);
+    f4 sc[RT][2][NB];
 #pragma unroll
     for (int g = 0; g < 2; ++g)
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        const uint32_t zw = (meta[64 * n + 16 * g + r] >> 16) & 15u;
-        const uint32_t zz = zw * 0x00010001u;
+        const uint32_t zz = (meta[64 * n + 16 * g + r] >> 16) * 0x00010001u;
         const h2 z1 = zero1024(zz), z6 = zero64(zz);
 #pragma unroll
         for (int t = 0; t < RT; ++t) sc[t][g][n] = f4{0, 0, 0, 0};
-        constexpr int SB = NS / NB;
 #pragma unroll
         for (int j = 0; j < SB; ++j) {
           const uint32_t w = T.k[g][SB * n + j], w8 = w >> 8;
@@ -319,65 +331,43 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? 2 * W / 4 : W / 4) vo
                                                                  sc[t][g][n], 0, 0, 0);
         }
       }
-    // V: scales below 1 by a power of two that follows the largest so far
-    float vsc[NB][8];
-    uint32_t vm[NB][8];
-    float vmax = 0.0f;
+    // scores times their token's K scale
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const u4 w = *reinterpret_cast<const u4*>(meta + 64 * n + 32 + 16 * g + 4 * c);
+        const u4 w = *reinterpret_cast<const u4*>(meta + 64 * n + 16 * g + 4 * c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          vm[n][4 * g + i] = w[i];
-          vsc[n][4 * g + i] = f16_bits_to_f32((uint16_t)w[i]);
-          vmax = fmaxf(vmax, vsc[n][4 * g + i]);
+          const float s = f16_bits_to_f32((uint16_t)w[i]);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) sc[t][g][0][i] = n ? __builtin_fmaf(sc[t][g][n][i], s, sc[t][g][0][i]) : sc[t][g][0][i] * s;
         }
       }
-    vmax = max_over_rows16(vmax);
-    if (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(uint32_t, vmax)) >
-        __builtin_bit_cast(uint32_t, v_top)) {  // both positive: bits order as values
-      const uint32_t ex = min((__builtin_amdgcn_readfirstlane(__builtin_bit_cast(uint32_t, vmax)) >> 23) + 1, 200u);
-      const float n_top = __builtin_bit_cast(float, ex << 23);
-      const float n_down = __builtin_bit_cast(float, (254u - ex) << 23);
-      const float k = v_top * n_down;
-      v_top = n_top;
-      v_down = n_down;
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int e = 0; e < NE; ++e) acc[t][e] *= k;
-    }
+    u4 vm[NB][2];
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        vsc[n][i] *= v_down;
-        any_off |= (km[n][i] & kTokenOff) != 0;
-      }
-    const bool masked = tk + 32 > low || __ballot(any_off) != 0;
+      for (int g = 0; g < 2; ++g) vm[n][g] = *reinterpret_cast<const u4*>(meta + 64 * n + 32 + 16 * g + 4 * c);
     h8 pf[RT][NB];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       float s8[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s8[i] = sc[t][i / 4][0][i % 4] * ksc[0][i];
-        if constexpr (NB == 2) s8[i] += sc[t][i / 4][1][i % 4] * ksc[1][i];
-      }
+      for (int i = 0; i < 8; ++i) s8[i] = sc[t][i / 4][0][i % 4];
       if (masked) {
+        const int seen = P32 && !T.ok ? 0 : lim[t] - tk;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int64_t tok = tk + 16 * (i / 4) + 4 * c + i % 4;
-          if (tok >= lim[t] || (km[0][i] & kTokenOff)) s8[i] = kNegInf;
+          const int tok = 16 * (i / 4) + 4 * c + i % 4;
+          if (tok >= seen || (!P32 && (gone >> tok & 1))) s8[i] = kNegInf;
         }
       }
       float mx = s8[0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s8[i]);
-      mx = max_over_rows16(mx) * f[t];
-      if (__ballot(mx > m[t])) {
+      mx = __builtin_fmaf(max_over_rows16(mx), f[t], v_exp);
+      if (__ballot(mx > m[t] + kLag)) {
         const float mn = fmaxf(m[t], mx);
         const float al = m[t] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[t] - mn);
         m[t] = mn;
@@ -386,16 +376,13 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? 2 * W / 4 : W / 4) vo
         for (int e = 0; e < NE; ++e) acc[t][e] *= al;
       }
       const float ms = m[t] == kNegInf ? 0.0f : m[t];
-      float p[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s8[i], f[t], -ms));
-        l[t] += p[i];
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s8[i], f[t], -ms));
+        l[t] += p;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) pf[t][n][i] = (_Float16)(p * f16_bits_to_f32((uint16_t)vm[n][i / 4][i % 4]));
       }
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) pf[t][n][i] = (_Float16)(p[i] * vsc[n][i]);
     }
     // O^T += V^T P^T, 16 channels an MFMA
 #pragma unroll
@@ -403,27 +390,18 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? 2 * W / 4 : W / 4) vo
       h2 z1[4], z6[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t zz = __builtin_amdgcn_perm(vm[n][2 * i + 1], vm[n][2 * i], 0x07060302u) & 0x000F000Fu;
+        const uint32_t zz = __builtin_amdgcn_perm(vm[n][i / 2][2 * (i % 2) + 1], vm[n][i / 2][2 * (i % 2)], 0x07060302u);
         z1[i] = zero1024(zz);
         z6[i] = zero64(zz);
-      }
-      auto product = [&](int e, u4 d) {
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-          acc[t][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, d), pf[t][n], acc[t][e], 0, 0, 0);
-      };
-      uint32_t x[4], y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = __builtin_amdgcn_perm(T.v[2 * i + 1][n], T.v[2 * i][n], 0x05040100u);  // even channels of two tokens
-        if constexpr (D != 64) y[i] = __builtin_amdgcn_perm(T.v[2 * i + 1][n], T.v[2 * i][n], 0x07060302u);
       }
 #pragma unroll
       for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
         u4 d[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t w = half ? y[i] : x[i], w8 = w >> 8;
+          // even (odd) channels of two tokens
+          const uint32_t w = __builtin_amdgcn_perm(T.v[2 * i + 1][n], T.v[2 * i][n], half ? 0x07060302u : 0x05040100u);
+          const uint32_t w8 = w >> 8;
           d[0][i] = code_pair(w, z1[i]);
           d[1][i] = code_pair16(w, z6[i]);
           d[2][i] = code_pair(w8, z1[i]);
@@ -432,94 +410,86 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? 2 * W / 4 : W / 4) vo
         // MFMA e of a block: channel 8 m + e of row m (D = 64: channel
         // 8 (m / 2) + m % 2 + 2 e)
 #pragma unroll
-        for (int p = 0; p < 4; ++p) product(D == 64 ? p : 8 * n + 2 * p + half, d[p]);
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            const int e = D == 64 ? p : 8 * n + 2 * p + half;
+            acc[t][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, d[p]), pf[t][n], acc[t][e], 0, 0, 0);
+          }
       }
     }
   };
 
   Tile<D> ta, tb;
-  const int64_t stride = 32 * TW;
-  int64_t tk = t_begin + 32 * tg;
+  const int stride = 32 * TW;
+  int tk = t_begin + 32 * tg;
   if (tk < t_end) {
     load(ta, tk, page_entry(tk));
     int pg = page_entry(tk + stride);
     while (true) {
       // past the end the next tile repeats real rows and is not computed
-      load(tb, min(tk + stride, (t_end - 1) & ~(int64_t)31), pg);
+      load(tb, min(tk + stride, (t_end - 1) & ~31), pg);
       pg = page_entry(tk + 2 * stride);
       compute(ta, tk);
       tk += stride;
       if (tk >= t_end) break;
-      load(ta, min(tk + stride, (t_end - 1) & ~(int64_t)31), pg);
+      load(ta, min(tk + stride, (t_end - 1) & ~31), pg);
       pg = page_entry(tk + 2 * stride);
       compute(tb, tk);
       tk += stride;
       if (tk >= t_end) break;
     }
   }
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    l[t] = sum_over_rows16(l[t]);
-#pragma unroll
-    for (int e = 0; e < NE; ++e) acc[t][e] *= v_top;
-  }
 
-  // Waves of one head join through LDS: the largest maximum, every wave's sums
-  // scaled to it, added in wave order.  Slab: the 16 rows of one row tile and
-  // block, [channel][row] per wave.
+  // Waves of one head join through LDS: the largest reference point, every
+  // wave's sums scaled to it, added in wave order.  Slab: the 16 rows of one row
+  // tile and block, [row][channel] per wave.
   constexpr int DB = D < 128 ? D : 128, NEB = DB / 16;
   float* slab = reinterpret_cast<float*>(lds) + W * 64 * NB;
   float* stat = slab + W * 16 * DB;  // [wave][2][16]
-  for (int t = 0; t < RT; ++t) {
-    float mt = kNegInf, lt = 0.0f;
 #pragma unroll
-    for (int u = 0; u < RT; ++u)
-      if (u == t) mt = m[u], lt = l[u];
-    __syncthreads();
+  for (int t = 0; t < RT; ++t) {
+    if (t) __syncthreads();
+    const float lt = sum_over_rows16(l[t]);
     if (c == 0) {
-      stat[wave * 32 + r] = mt;
+      stat[wave * 32 + r] = m[t];
       stat[wave * 32 + 16 + r] = lt;
     }
     __syncthreads();
     float M = kNegInf;
-    for (int g = 0; g < TW; ++g) M = fmaxf(M, stat[(wave % HW + HW * g) * 32 + r]);
+    for (int g = 0; g < TW; ++g) M = fmaxf(M, stat[(hw + HW * g) * 32 + r]);
     // a wave whose sum is 0 saw nothing (a NaN sum stays one)
-    const float k = lt == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(mt - M);
+    const float k = lt == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[t] - M);
+#pragma unroll
     for (int n = 0; n < NB; ++n) {
       if (n) __syncthreads();
 #pragma unroll
-      for (int u = 0; u < RT; ++u)
+      for (int e = 0; e < NEB; ++e)
 #pragma unroll
-        for (int nn = 0; nn < NB; ++nn)
-          if (u == t && nn == n) {
-#pragma unroll
-            for (int e = 0; e < NEB; ++e)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int mrow = 4 * c + i;
-                const int ch = D == 64 ? 8 * (mrow / 2) + mrow % 2 + 2 * e : 8 * mrow + e;
-                slab[wave * 16 * DB + r * DB + ch] = acc[u][NEB * nn + e][i] * k;
-              }
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int mrow = 4 * c + i;
+          const int ch = D == 64 ? 8 * (mrow / 2) + mrow % 2 + 2 * e : 8 * mrow + e;
+          slab[wave * 16 * DB + r * DB + ch] = acc[t][NEB * n + e][i] * k;
+        }
       __syncthreads();
-      // thread: two channels of one row and head
-      const int per_head = 16 * DB / 2;
-      for (int x = threadIdx.x; x < HW * per_head; x += 64 * W) {
-        const int hw = x / per_head, rest = x % per_head, rr = rest / (DB / 2), ch = 2 * (rest % (DB / 2));
-        const int64_t row = row0 + 16 * t + rr;
-        if (row > row1) continue;
+      // a thread: two channels of one row and head
+      constexpr uint32_t per_head = 16 * DB / 2;
+      for (uint32_t x = threadIdx.x; x < HW * per_head; x += 64 * W) {
+        const int hx = x / per_head, rr = x % per_head / (DB / 2), ch = 2 * (x % (DB / 2));
+        const uint32_t row = row0 + 16 * t + rr;
+        if ((int)row > row1) continue;
         float o0 = 0.0f, o1 = 0.0f, Mr = kNegInf, L = 0.0f;
-        for (int g = 0; g < TW; ++g) Mr = fmaxf(Mr, stat[(hw + HW * g) * 32 + rr]);
+        for (int g = 0; g < TW; ++g) Mr = fmaxf(Mr, stat[(hx + HW * g) * 32 + rr]);
         for (int g = 0; g < TW; ++g) {
-          const int wv = hw + HW * g;
+          const int wv = hx + HW * g;
           const float lw = stat[wv * 32 + 16 + rr];
           if (lw == 0.0f) continue;
           o0 += slab[wv * 16 * DB + rr * DB + ch];
           o1 += slab[wv * 16 * DB + rr * DB + ch + 1];
           L += lw * __builtin_amdgcn_exp2f(stat[wv * 32 + rr] - Mr);
         }
-        const int64_t hq = (int64_t)(hg * HW + hw) * G + row % G;
-        const int64_t at = (q0 + row / G) * a.Hq + hq;
+        const uint32_t qi = row / (uint32_t)G;
+        const int64_t at = (int64_t)(q0 + qi) * a.Hq + (hg * HW + hx) * G + (row - qi * G);
         if (whole) {
           const float inv = L == 0.0f ? 0.0f : 1.0f / L;
           const uint32_t lo = a.dtype == 1 ? f32_to_bf16_bits(o0 * inv) : f32_to_f16_bits(o0 * inv);
@@ -530,53 +500,81 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? 2 * W / 4 : W / 4) vo
         } else {
           const int64_t nrow = a.T * a.Hq;
           float* ws = static_cast<float*>(a.workspace);
-          float* part = ws + 2 * nrow * KS + ((int64_t)split * nrow + at) * D + 128 * n + ch;
+          float* part = ws + 2 * nrow * KS + (split * nrow + at) * D + 128 * n + ch;
           *reinterpret_cast<float2*>(part) = make_float2(o0, o1);
-          if (ch == 0 && n == 0) *reinterpret_cast<float2*>(ws + 2 * ((int64_t)split * nrow + at)) = make_float2(Mr, L);
+          if (ch == 0 && n == 0) *reinterpret_cast<float2*>(ws + 2 * (split * nrow + at)) = make_float2(Mr, L);
         }
       }
     }
   }
 }
 
-// Joins the partial results of the sequences that were split: one wave per
-// query row, D / 64 channels a lane, splits in order.
+// Joins the partial results of the sequences that were split: a workgroup of
+// four waves per query row.  The weights of up to 256 splits at a time are made
+// by a thread each; then wave w adds splits w, w + 4, ..., whose loads do not wait
+// for one another, and the four sums meet in LDS.
 template <int D>
-__global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int64_t chunk, int KS) {
-  const int lane = threadIdx.x & 63;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t hq = id % a.Hq, qi = (id / a.Hq) % a.max_queries, b = id / a.Hq / a.max_queries;
-  if (b >= a.B) return;
-  int64_t q0 = b, nq = 1;
-  if (a.q_starts) {
-    q0 = max((int64_t)a.q_starts[b], (int64_t)0);
-    nq = min((int64_t)a.q_starts[b + 1], a.T) - q0;
-  }
-  const int64_t len = min((int64_t)a.lens[b], a.max_context);
-  if (qi >= nq || len <= chunk) return;
-  const int n = (int)((len + chunk - 1) / chunk);
-  const int64_t nrow = a.T * a.Hq, at = (q0 + qi) * a.Hq + hq;
-  const float* ws = static_cast<const float*>(a.workspace);
-  float M = kNegInf;
-  for (int s = 0; s < n; ++s) M = fmaxf(M, ws[2 * (s * nrow + at)]);
+__global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int chunk, int KS) {
   constexpr int C = D / 64;
+  __shared__ float wt[256], red[8], sum[4][D];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t id = blockIdx.x;
+  const int hq = id % (uint32_t)a.Hq;
+  id /= (uint32_t)a.Hq;
+  const int qi = id % (uint32_t)a.max_queries, b = id / (uint32_t)a.max_queries;
+  int q0 = b, nq = 1;
+  if (a.q_starts) {
+    q0 = max(a.q_starts[b], 0);
+    nq = (int)min((int64_t)a.q_starts[b + 1], a.T) - q0;
+  }
+  const int len = (int)min((int64_t)a.lens[b], a.max_context);
+  if (qi >= nq || len <= chunk) return;
+  const int n = (int)(((int64_t)len + chunk - 1) / chunk);
+  const int64_t nrow = a.T * a.Hq, at = (int64_t)(q0 + qi) * a.Hq + hq;
+  const float* ws = static_cast<const float*>(a.workspace);
+  const float2* stat = reinterpret_cast<const float2*>(ws) + at;
+  const float* part = ws + 2 * nrow * KS + at * D + lane * C;
+  float M = kNegInf;
+  for (int s = threadIdx.x; s < n; s += 256) M = fmaxf(M, stat[s * nrow].x);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) M = fmaxf(M, __shfl_xor(M, d));
+  if (lane == 0) red[wave] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   float o[C], L = 0.0f;
 #pragma unroll
   for (int i = 0; i < C; ++i) o[i] = 0.0f;
-  for (int s = 0; s < n; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(ws + 2 * (s * nrow + at));
-    if (ml.y == 0.0f) continue;
-    const float k = __builtin_amdgcn_exp2f(ml.x - M);
-    L += ml.y * k;
-    const float* part = ws + 2 * nrow * KS + (s * nrow + at) * D + lane * C;
+  for (int s0 = 0; s0 < n; s0 += 256) {
+    const int here = min(256, n - s0);
+    if (s0) __syncthreads();
+    if ((int)threadIdx.x < here) {
+      const float2 ml = stat[(s0 + threadIdx.x) * nrow];
+      const float k = ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - M);  // 0: the split saw nothing
+      wt[threadIdx.x] = k;
+      L += ml.y * k;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int s = wave; s < here; s += 4) {
+      const float k = wt[s];
+      const float* p = part + (s0 + s) * nrow * D;
 #pragma unroll
-    for (int i = 0; i < C; ++i) o[i] += part[i] * k;
+      for (int i = 0; i < C; ++i) o[i] += p[i] * k;
+    }
   }
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
-  for (int i = 0; i < C; ++i)
-    a.out[at * D + lane * C + i] = a.dtype == 1 ? f32_to_bf16_bits(o[i] * inv) : f32_to_f16_bits(o[i] * inv);
-  if (a.lse && lane == 0) a.lse[at] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
+  for (int d = 1; d < 64; d <<= 1) L += __shfl_xor(L, d);
+  if (lane == 0) red[4 + wave] = L;
+#pragma unroll
+  for (int i = 0; i < C; ++i) sum[wave][lane * C + i] = o[i];
+  __syncthreads();
+  L = red[4] + red[5] + red[6] + red[7];
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  for (int x = threadIdx.x; x < D; x += 256) {
+    const float v = (sum[0][x] + sum[1][x] + sum[2][x] + sum[3][x]) * inv;
+    a.out[at * D + x] = a.dtype == 1 ? f32_to_bf16_bits(v) : f32_to_f16_bits(v);
+  }
+  if (a.lse && threadIdx.x == 0) a.lse[at] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
 }
 
 template <int D>
@@ -592,11 +590,11 @@ hipError_t launch_main(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream)
   hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&kv_attn_kernel<D, RT, W, P32>), lds, raised);
   if (e != hipSuccess) return e;
   const int64_t grid = (int64_t)a.B * p.KS * (a.Hkv / p.HW) * p.rtiles;
-  kv_attn_kernel<D, RT, W, P32><<<(unsigned)grid, 64 * W, lds, stream>>>(a, p.HW, p.chunk, (int)p.KS, (int)p.rtiles);
+  kv_attn_kernel<D, RT, W, P32><<<(unsigned)grid, 64 * W, lds, stream>>>(a, p.HW, (int)p.chunk, (int)p.KS, (int)p.rtiles);
   e = hipGetLastError();
   if (e != hipSuccess || p.KS == 1) return e;
   const int64_t rows = (int64_t)a.B * a.max_queries * a.Hq;
-  kv_attn_join_kernel<D><<<(unsigned)((rows + 3) / 4), 256, 0, stream>>>(a, p.chunk, (int)p.KS);
+  kv_attn_join_kernel<D><<<(unsigned)rows, 256, 0, stream>>>(a, (int)p.chunk, (int)p.KS);
   return hipGetLastError();
 }
 
