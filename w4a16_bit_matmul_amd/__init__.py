@@ -502,46 +502,60 @@ def wq_kv_dequant(cache: KVCache, T: int, slot: torch.Tensor | None = None, out_
 # outputs and workspaces on the stream they run on.
 
 class _on:
-    """The device of a tensor and the stream of a call, current inside the with block."""
+    """Makes the device of a call's tensors and its stream current within the
+    block (nothing to do where they already are); gives the raw stream."""
+    __slots__ = ("raw", "guard")
 
-    def __init__(self, t: torch.Tensor, stream):
-        if t.device.type != "cuda":
-            raise ValueError(f"tensors must be on the GPU (got {t.device})")
-        self.device = t.device
-        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
-        if self.stream.device != t.device:
-            raise ValueError(f"the stream belongs to {self.stream.device}, the tensors are on {t.device}")
+    def __init__(self, device: torch.device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on the GPU (got {device})")
+        self.guard = None
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+            if torch.cuda.current_device() != device.index:
+                self.guard = torch.cuda.stream(stream)
+        else:
+            if stream.device != device:
+                raise ValueError(f"the stream belongs to {stream.device}, the tensors are on {device}")
+            self.guard = torch.cuda.stream(stream)  # sets the stream's device too
+        self.raw = stream.cuda_stream
 
     def __enter__(self):
-        self.guard = torch.cuda.stream(self.stream)  # sets the stream's device too
-        self.guard.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.raw
 
     def __exit__(self, *e):
-        return self.guard.__exit__(*e)
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+_DT16 = {torch.bfloat16: WQ_BF16, torch.float16: WQ_F16}
 
 
 def _heads(name: str, x: torch.Tensor, like: torch.Tensor | None = None, T: int | None = None) -> int:
     """x is [T][heads][D], heads and values contiguous; its stride between tokens."""
-    if x.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float16):
+    if x.dim() != 3 or x.dtype not in _DT16:
         raise ValueError(f"{name} must be a bfloat16 or float16 tensor [tokens][heads][D] "
                          f"(got {x.dtype}, shape {tuple(x.shape)})")
     n, h, d = x.shape
-    if (d > 1 and x.stride(2) != 1) or (h > 1 and x.stride(1) != d):
+    st, sh, sd = x.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError(f"{name}: the heads and values of a token must be contiguous (strides {x.stride()})")
     if like is not None and (x.dtype != like.dtype or x.device != like.device or d != like.shape[2]):
         raise ValueError(f"{name} is {x.dtype} on {x.device} with D={d}, expected {like.dtype} on {like.device} with "
                          f"D={like.shape[2]}")
     if T is not None and n != T:
         raise ValueError(f"{name} has {n} tokens, expected {T}")
-    return x.stride(0) if n > 1 else h * d
+    return st if n > 1 else h * d
 
 
-def _dev_array(name: str, t: torch.Tensor, dtype, shape, like: torch.Tensor) -> torch.Tensor:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != like.device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device} "
+def _dev_array(name: str, t: torch.Tensor, dtype, shape, device: torch.device) -> int:
+    """The address of a contiguous tensor of exactly that type and shape on that device."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device} "
                          f"(got {t.dtype}, shape {tuple(t.shape)}, on {t.device})")
-    return t
+    return t.data_ptr()
 
 
 def wq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor, *,
@@ -556,41 +570,45 @@ def wq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, sin: to
     Returns (q_out, k_out)."""
     qs, ks = _heads("q", q), _heads("k", k, q, q.shape[0])
     T, Hq, D = q.shape
+    Hkv, dev, dt = k.shape[1], q.device, q.dtype
     P, half = cos.shape
-    _dev_array("cos", cos, torch.float32, (P, half), q)
-    _dev_array("sin", sin, torch.float32, (P, half), q)
-    _dev_array("positions", positions, torch.int32, (T,), q)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _dev_array(name, w, q.dtype, (D,), q)
-    with _on(q, stream) as s:
-        outs, strides = [], []
-        for name, x, o in (("q_out", q, q_out), ("k_out", k, k_out)):
-            if o is None:
-                o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            strides.append(_heads(name, o, q, T))
-            if o.shape[1] != x.shape[1]:
-                raise ValueError(f"{name} has {o.shape[1]} heads, expected {x.shape[1]}")
-            outs.append(o)
-        _check(lib().wq_qk_norm_rope(_ptr(q), _ptr(k), _DT[q.dtype], T, Hq, k.shape[1], D, qs, ks, _ptr(q_weight),
-                                     _ptr(k_weight), eps, _ptr(positions), _ptr(cos), _ptr(sin), P, 2 * half,
-                                     int(interleaved), _ptr(outs[0]), _ptr(outs[1]), strides[0], strides[1], s),
-               "wq_qk_norm_rope")
-    return outs[0], outs[1]
+    c, n, p = (_dev_array("cos", cos, torch.float32, (P, half), dev), _dev_array("sin", sin, torch.float32, (P, half), dev),
+               _dev_array("positions", positions, torch.int32, (T,), dev))
+    qw = None if q_weight is None else _dev_array("q_weight", q_weight, dt, (D,), dev)
+    kw = None if k_weight is None else _dev_array("k_weight", k_weight, dt, (D,), dev)
+    qos, kos = Hq * D, Hkv * D
+    if q_out is not None:
+        qos = _heads("q_out", q_out, q, T)
+        if q_out.shape[1] != Hq:
+            raise ValueError(f"q_out has {q_out.shape[1]} heads, expected {Hq}")
+    if k_out is not None:
+        kos = _heads("k_out", k_out, q, T)
+        if k_out.shape[1] != Hkv:
+            raise ValueError(f"k_out has {k_out.shape[1]} heads, expected {Hkv}")
+    with _on(dev, stream) as s:
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+        if k_out is None:
+            k_out = torch.empty((T, Hkv, D), dtype=dt, device=dev)
+        st = (_lib or lib()).wq_qk_norm_rope(q.data_ptr(), k.data_ptr(), _DT16[dt], T, Hq, Hkv, D, qs, ks, qw, kw, eps, p, c, n,
+                                             P, 2 * half, 1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), qos,
+                                             kos, s)
+    _check(st, "wq_qk_norm_rope")
+    return q_out, k_out
 
 
-def _attn_out(q: torch.Tensor, out, lse):
+def _attn_out(shape, dtype, device, out, lse):
     """The output and the optional lse tensor (lse: False, True or a tensor)."""
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty(shape, dtype=dtype, device=device)
     else:
-        _dev_array("out", out, q.dtype, q.shape, q)
+        _dev_array("out", out, dtype, shape, device)
     if lse is True:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=device)
     elif lse is False or lse is None:
         lse = None
     else:
-        _dev_array("lse", lse, torch.float32, q.shape[:2], q)
+        _dev_array("lse", lse, torch.float32, shape[:2], device)
     return out, lse
 
 
@@ -608,13 +626,14 @@ def wq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_s
         raise ValueError(f"k has {Hkv} heads, v {v.shape[1]}")
     if seq_starts.dim() != 1 or seq_starts.numel() < 1:
         raise ValueError("seq_starts must hold B + 1 token numbers")
-    B = seq_starts.numel() - 1
-    _dev_array("seq_starts", seq_starts, torch.int32, (B + 1,), q)
-    with _on(q, stream) as s:
-        out, lse = _attn_out(q, out, lse)
-        _check(lib().wq_prompt_attention(_ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], T, Hq, Hkv, D, qs, ks, vs, B,
-                                         _ptr(seq_starts), D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse),
-                                         s), "wq_prompt_attention")
+    B, dev, dt = seq_starts.numel() - 1, q.device, q.dtype
+    starts = _dev_array("seq_starts", seq_starts, torch.int32, (B + 1,), dev)
+    with _on(dev, stream) as s:
+        out, lse = _attn_out((T, Hq, D), dt, dev, out, lse)
+        st = (_lib or lib()).wq_prompt_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), _DT16[dt], T, Hq, Hkv, D, qs, ks, vs,
+                                                 B, starts, D ** -0.5 if scale is None else scale, out.data_ptr(),
+                                                 None if lse is None else lse.data_ptr(), s)
+    _check(st, "wq_prompt_attention")
     return out if lse is None else (out, lse)
 
 
@@ -653,37 +672,36 @@ def wq_kv_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, block_t
     if (v_cache.S, v_cache.hd) != (S, hd) or hd % D != 0:
         raise ValueError(f"caches of {S} x {hd} and {v_cache.S} x {v_cache.hd} values, heads of {D}")
     Hkv = hd // D
+    dev, dt, nb = q.device, q.dtype, hd // 128
+    kv = []
     for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _dev_array(name + ".codes", c.codes, torch.uint8, (S, hd // 2), q)
-        _dev_array(name + ".s", c.s, torch.float16, (S, hd // 128), q)
-        _dev_array(name + ".zpacked", c.zpacked, torch.uint8, (S, (hd // 128 + 1) // 2), q)
+        kv += (_dev_array(name + ".codes", c.codes, torch.uint8, (S, hd // 2), dev),
+               _dev_array(name + ".s", c.s, torch.float16, (S, nb), dev),
+               _dev_array(name + ".zpacked", c.zpacked, torch.uint8, (S, (nb + 1) // 2), dev))
     if block_table.dim() != 2:
         raise ValueError("block_table must be [sequences][pages]")
     B, width = block_table.shape
-    _dev_array("block_table", block_table, torch.int32, (B, width), q)
-    _dev_array("context_lens", context_lens, torch.int32, (B,), q)
+    table = _dev_array("block_table", block_table, torch.int32, (B, width), dev)
+    lens = _dev_array("context_lens", context_lens, torch.int32, (B,), dev)
     if q_starts is not None:
-        _dev_array("q_starts", q_starts, torch.int32, (B + 1,), q)
-        if max_queries is None:
-            max_queries = T
-        max_queries = min(max_queries, T)
+        starts = _dev_array("q_starts", q_starts, torch.int32, (B + 1,), dev)
+        max_queries = T if max_queries is None else min(max_queries, T)
     else:
-        max_queries = min(T, 1)
+        starts, max_queries = None, min(T, 1)
     if max_context is None:
         max_context = width * page_size
-    with _on(q, stream) as s:
-        out, lse = _attn_out(q, out, lse)
+    L = _lib or lib()
+    with _on(dev, stream) as s:
+        out, lse = _attn_out((T, Hq, D), dt, dev, out, lse)
         if workspace is None:
-            need = lib().wq_kv_attention_workspace_bytes(T, Hq, Hkv, D, B, page_size, max_context, max_queries)
+            need = L.wq_kv_attention_workspace_bytes(T, Hq, Hkv, D, B, page_size, max_context, max_queries)
             if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _check(lib().wq_kv_attention(_ptr(q), _DT[q.dtype], T, Hq, Hkv, D, qs, _ptr(k_cache.codes), _ptr(k_cache.s),
-                                     _ptr(k_cache.zpacked), _ptr(v_cache.codes), _ptr(v_cache.s), _ptr(v_cache.zpacked),
-                                     S, B, _ptr(block_table), width, page_size, _ptr(context_lens), max_context,
-                                     _ptr(q_starts), max_queries, D ** -0.5 if scale is None else scale, _ptr(out),
-                                     _ptr(lse), _ptr(workspace),
-                                     0 if workspace is None else workspace.numel() * workspace.element_size(), s),
-               "wq_kv_attention")
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        st = L.wq_kv_attention(q.data_ptr(), _DT16[dt], T, Hq, Hkv, D, qs, *kv, S, B, table, width, page_size, lens,
+                               max_context, starts, max_queries, D ** -0.5 if scale is None else scale, out.data_ptr(),
+                               None if lse is None else lse.data_ptr(), ws, wsb, s)
+    _check(st, "wq_kv_attention")
     return out if lse is None else (out, lse)
 
 
