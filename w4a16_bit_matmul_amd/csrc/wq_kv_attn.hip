@@ -47,36 +47,100 @@ constexpr float kNegInf = -__builtin_inff();
 // (fp16 weights stay below 2^9, the fp32 sums far below their limits), so that it
 // rarely moves.
 constexpr float kLag = 8.0f;
+constexpr int kMaxFlat = 256;  // sequences that a wave scans for its share
 
 struct KvPlan {
-  int HW;          // KV heads of a workgroup (its W / HW waves per head take different tiles)
-  int RT;          // 16-row tiles of a wave
-  int W;           // waves of a workgroup
-  int64_t rtiles;  // workgroups along the query rows of one KV head
-  int64_t chunk;   // tokens of a split
-  int64_t KS;      // splits of max_context
+  int HW;           // KV heads of a workgroup (its W / HW waves per head take different tiles)
+  int RT;           // 16-row tiles of a wave
+  int W;            // waves of a workgroup
+  int rtiles;       // units along the query rows of one KV head
+  int urows;        // query rows of a unit that a call can use
+  int64_t grid;     // workgroups
+  bool flat;        // shared out in equal runs of steps; else one unit a workgroup
 };
 
-// Tokens read past a chunk are never attended: a chunk is whole tiles of 32.
+// A unit is HW heads of one sequence and one tile of query rows; its steps are
+// the runs of 32 W / HW tokens that its waves take together.
 KvPlan plan_kv(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries) {
   KvPlan p;
   const int64_t G = Hq / Hkv, rows = max_queries * G;
   p.RT = rows <= 16 ? 1 : 2;
   p.W = 8;
-  p.rtiles = (rows + 16 * p.RT - 1) / (16 * p.RT);
-  p.HW = Hkv % 8 == 0 ? 8 : Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
+  p.rtiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
+  p.urows = (int)(rows < 16 * p.RT ? rows : 16 * p.RT);
+  p.HW = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
   if (max_context <= 2048) p.HW = 1;
-  const int64_t TW = p.W / p.HW;
-  const int64_t base = (int64_t)B * (Hkv / p.HW) * p.rtiles;
-  const int64_t want = (1024 + base - 1) / base;
-  const int64_t unit = 32 * TW;
-  int64_t chunk = (max_context + want - 1) / want;
-  chunk = (chunk + unit - 1) / unit * unit;
-  if (chunk < 2 * unit) chunk = 2 * unit;
-  p.chunk = chunk;
-  p.KS = (max_context + chunk - 1) / chunk;
-  if (p.KS < 1) p.KS = 1;
+  const int64_t units = (int64_t)B * (Hkv / p.HW) * p.rtiles;
+  const int64_t steps = (max_context + 32 * (p.W / p.HW) - 1) / (32 * (p.W / p.HW));
+  const int64_t want = 512;
+  // runs of at least four steps, so that joining them stays cheap
+  const int64_t n = units * steps / 4 < want ? units * steps / 4 : want;
+  p.flat = n > units && B <= kMaxFlat && units * steps < (int64_t(1) << 31);
+  p.grid = p.flat ? n : units;
   return p;
+}
+
+// Equal shares of the steps of all units.  The shares follow from the lengths
+// alone, which only the device knows: each wave scans them.
+struct Shares {
+  uint32_t total, n;  // steps of all units, workgroups that share them
+  uint32_t* lds;      // [2][kMaxFlat]: steps before each sequence's units, steps of one of its units
+};
+
+__device__ __forceinline__ int queries_of(const KvAttnArgs& a, int b, int* q0) {
+  if (!a.q_starts) {
+    *q0 = b;
+    return 1;
+  }
+  *q0 = max(a.q_starts[b], 0);
+  return (int)max((int64_t)0, min(min((int64_t)a.q_starts[b + 1], a.T) - *q0, a.max_queries));
+}
+__device__ __forceinline__ int length_of(const KvAttnArgs& a, int b) {
+  return (int)max((int64_t)0, min((int64_t)a.lens[b], a.max_context));
+}
+
+// Units of sequence b and steps of each (one at least: a row that sees nothing
+// is written too).
+__device__ __forceinline__ uint32_t units_of(int nq, int G, int HG, int row_tile) {
+  return (uint32_t)HG * ((uint32_t)(nq * G + row_tile - 1) / (uint32_t)row_tile);
+}
+__device__ __forceinline__ uint32_t steps_of(int len, int step) {
+  return max((uint32_t)(len + step - 1) / (uint32_t)step, 1u);
+}
+
+// Every wave scans all of it and writes the same words, so none waits for
+// another.  A share is at least four steps while there are that many.
+__device__ __forceinline__ Shares scan_shares(const KvAttnArgs& a, uint32_t wgs, int HG, int row_tile, int step,
+                                              int lane, uint32_t* lds) {
+  Shares s;
+  s.total = 0;
+  s.lds = lds;
+  const int G = a.Hq / a.Hkv;
+  for (int w = 0; w < a.B; w += 64) {
+    const int b = w + lane;
+    uint32_t cost = 0, steps = 1;
+    if (b < a.B) {
+      int q0;
+      const int nq = queries_of(a, b, &q0);
+      steps = steps_of(length_of(a, b), step);
+      cost = units_of(nq, G, HG, row_tile) * steps;
+    }
+    uint32_t run = cost;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t up = (uint32_t)__shfl_up((int)run, d);
+      run += lane >= d ? up : 0u;
+    }
+    lds[w + lane] = s.total + run - cost;
+    lds[kMaxFlat + w + lane] = steps;
+    s.total += (uint32_t)__builtin_amdgcn_readlane((int)run, 63);
+  }
+  s.n = max(min(wgs, (s.total + 3) / 4), 1u);
+  return s;
+}
+// First step of share i of n.
+__device__ __forceinline__ uint32_t share_start(uint32_t total, uint32_t i, uint32_t n) {
+  return (uint32_t)((uint64_t)total * i / n);
 }
 
 __device__ __forceinline__ float max_over_rows16(float v) {  // over the lanes l, l ^ 16, l ^ 32, l ^ 48
@@ -97,12 +161,21 @@ __device__ __forceinline__ float sum_over_rows16(float v) {
 }
 
 // Two fp16 pairs (c - z) of the nibbles 0, 4 and 1, 5 of a word: (1024 + c) and
-// (64 + c) by OR-ing an exponent in (wq_device.h), less the same of z.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, h2 z1024) {
-  return as_u32(as_h2((w & 0x000F000Fu) | 0x64006400u) - z1024);
+// (64 + c) by OR-ing an exponent in (wq_device.h), less the same of z.  The
+// exponents come in vector registers (`magic`): v_and_or_b32 takes one scalar
+// operand and no literal.
+struct Magic {
+  uint32_t e10 = 0x64006400u, e6 = 0x54005400u;
+  __device__ __forceinline__ Magic() {
+    asm("" : "+v"(e10));
+    asm("" : "+v"(e6));
+  }
+};
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, h2 z1024, const Magic& g) {
+  return as_u32(as_h2((w & 0x000F000Fu) | g.e10) - z1024);
 }
-__device__ __forceinline__ uint32_t code_pair16(uint32_t w, h2 z64) {
-  return as_u32(as_h2((w & 0x00F000F0u) | 0x54005400u) - z64);
+__device__ __forceinline__ uint32_t code_pair16(uint32_t w, h2 z64, const Magic& g) {
+  return as_u32(as_h2((w & 0x00F000F0u) | g.e6) - z64);
 }
 __device__ __forceinline__ h2 zero1024(uint32_t zz) { return as_h2(zz | 0x64006400u); }
 __device__ __forceinline__ h2 zero64(uint32_t zz) { return as_h2((zz << 4) | 0x54005400u); }
@@ -120,9 +193,8 @@ struct Tile {
 };
 
 template <int D, int RT, int W, bool P32>
-__global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? W / 2 : W / 4) void kv_attn_kernel(KvAttnArgs a, int HW,
-                                                                                             int chunk, int KS,
-                                                                                             int rtiles) {
+__global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? W / 2 : W / 4) void kv_attn_kernel(KvAttnArgs a, int HW, int rtiles,
+                                                                                             int urows, bool flat) {
   constexpr int NB = Tile<D>::NB;
   constexpr int NS = D / 32;  // MFMA steps of a score
   constexpr int SB = NS / NB;
@@ -130,33 +202,63 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? W / 2 : W / 4) void k
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4, ml = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int TW = W / HW, tg = wave / HW, hw = wave - tg * HW;
-  const uint32_t HG = a.Hkv / HW;
-  uint32_t id = blockIdx.x;
-  const int rt0 = id % (uint32_t)rtiles;
-  id /= (uint32_t)rtiles;
-  const int hg = id % HG;
-  id /= HG;
-  const int split = id % (uint32_t)KS;
-  const int b = id / (uint32_t)KS;
-  const int h = hg * HW + hw;
-  const int G = a.Hq / a.Hkv;
+  const int TW = W / HW, tg = wave / HW, hw = wave - tg * HW, step = 32 * TW;
+  const int HG = a.Hkv / HW, G = a.Hq / a.Hkv;
+  const uint32_t rowb = (uint32_t)a.Hkv * (D / 2);  // code bytes of a cache row
+  const uint32_t nbt = (uint32_t)a.Hkv * D / 128, zb = (nbt + 1) / 2;
+  const int lg = 31 - __builtin_clz(a.page);
+  const int pages = (int)(a.S >> lg);
+  uint32_t* meta = lds + wave * (64 * NB);
+  const Magic magic;
 
-  int q0 = b, nq = 1;
-  if (a.q_starts) {
-    q0 = max(a.q_starts[b], 0);
-    nq = (int)min(min((int64_t)a.q_starts[b + 1], a.T) - q0, a.max_queries);
+  // this workgroup's steps, counted over all units
+  uint32_t at = 0, at_end = 1;
+  uint32_t* share_lds = lds + W * 64 * NB;
+  if (flat) {
+    const Shares sh = scan_shares(a, gridDim.x, HG, 16 * RT, step, lane, share_lds);
+    if (blockIdx.x >= sh.n) return;
+    at = share_start(sh.total, blockIdx.x, sh.n);
+    at_end = share_start(sh.total, blockIdx.x + 1, sh.n);
   }
-  const int len = (int)min((int64_t)a.lens[b], a.max_context);
+  for (int seg = 0; at < at_end; ++seg) {
+  int b, rt0, hg, s0 = 0, s1 = 0;
+  bool whole = true;  // all of a unit's steps are here
+  if (flat) {
+    // the last sequence that starts at or before `at` and is not empty
+    b = 0;
+    for (int w = 0; w < a.B; w += 64) {
+      const uint64_t le = __ballot(w + lane < a.B && share_lds[w + lane] <= at);
+      if (le) b = w + 63 - __builtin_clzll(le);
+    }
+    const uint32_t before = __builtin_amdgcn_readfirstlane(share_lds[b]);
+    const uint32_t steps = __builtin_amdgcn_readfirstlane(share_lds[kMaxFlat + b]);
+    const uint32_t unit = (at - before) / steps;
+    rt0 = (int)(unit / (uint32_t)HG);
+    hg = (int)(unit % (uint32_t)HG);
+    s0 = (int)(at - before - unit * steps);
+    s1 = (int)min(steps, (uint32_t)s0 + (at_end - at));
+    whole = s0 == 0 && s1 == (int)steps;
+    at += s1 - s0;
+  } else {
+    uint32_t id = blockIdx.x;
+    hg = (int)(id % (uint32_t)HG);
+    id /= (uint32_t)HG;
+    rt0 = (int)(id % (uint32_t)rtiles);
+    b = (int)(id / (uint32_t)rtiles);
+    at = 1;
+  }
+  int q0;
+  const int nq = queries_of(a, b, &q0);
+  const int len = length_of(a, b);
+  if (!flat) s1 = (int)steps_of(len, step);
   const int row0 = rt0 * (16 * RT), rows = nq * G;
   if (row0 >= rows) return;
-  if (split > 0 && split * (int64_t)chunk >= len) return;
-  const bool whole = len <= chunk;  // the sequence is not split
+  const int h = hg * HW + hw;
   const int row1 = min(row0 + 16 * RT, rows) - 1;
   // of these rows' tokens: what the last row sees ends the walk, what the first
   // sees ends the tiles that need no mask
-  const int t_begin = split * chunk;
-  const int t_end = min(min(t_begin + chunk, len), len - nq + (int)((uint32_t)row1 / (uint32_t)G) + 1);
+  const int t_begin = s0 * step;
+  const int t_end = min((int)min((int64_t)s1 * step, (int64_t)len), len - nq + (int)((uint32_t)row1 / (uint32_t)G) + 1);
   const int low = min(t_end, len - nq + (int)((uint32_t)row0 / (uint32_t)G) + 1);
 
   // the wave's queries, as the B operand of the scores: lane (r, c) channels
@@ -219,14 +321,9 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? W / 2 : W / 4) void k
   uint32_t v_top = 0;
   float v_exp = -25.0f;
 
-  const uint32_t rowb = (uint32_t)a.Hkv * (D / 2);  // code bytes of a cache row
-  const uint32_t nbt = (uint32_t)a.Hkv * D / 128, zb = (nbt + 1) / 2;
-  const uint32_t blk = (uint32_t)h * D / 128;       // first block of the head
+  const uint32_t blk = (uint32_t)h * D / 128;  // first block of the head
   const int zshift = D == 256 ? 0 : (blk & 1) * 4;
-  const int lg = 31 - __builtin_clz(a.page);
-  const int pages = (int)(a.S >> lg);
   const int32_t* table = a.table + (int64_t)b * a.table_width;
-  uint32_t* meta = lds + wave * (64 * NB);
   const uint8_t* kc = a.k_codes + (uint32_t)h * (D / 2);
   const uint8_t* vc = a.v_codes + (uint32_t)h * (D / 2);
   const uint16_t* sp = (lane < 32 ? a.k_s : a.v_s) + blk + (P32 ? ml * nbt : 0);
@@ -324,7 +421,7 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? W / 2 : W / 4) void k
 #pragma unroll
         for (int j = 0; j < SB; ++j) {
           const uint32_t w = T.k[g][SB * n + j], w8 = w >> 8;
-          const u4 d = {code_pair(w, z1), code_pair16(w, z6), code_pair(w8, z1), code_pair16(w8, z6)};
+          const u4 d = {code_pair(w, z1, magic), code_pair16(w, z6, magic), code_pair(w8, z1, magic), code_pair16(w8, z6, magic)};
 #pragma unroll
           for (int t = 0; t < RT; ++t)
             sc[t][g][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, d), qf[t][SB * n + j],
@@ -402,10 +499,10 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? W / 2 : W / 4) void k
           // even (odd) channels of two tokens
           const uint32_t w = __builtin_amdgcn_perm(T.v[2 * i + 1][n], T.v[2 * i][n], half ? 0x07060302u : 0x05040100u);
           const uint32_t w8 = w >> 8;
-          d[0][i] = code_pair(w, z1[i]);
-          d[1][i] = code_pair16(w, z6[i]);
-          d[2][i] = code_pair(w8, z1[i]);
-          d[3][i] = code_pair16(w8, z6[i]);
+          d[0][i] = code_pair(w, z1[i], magic);
+          d[1][i] = code_pair16(w, z6[i], magic);
+          d[2][i] = code_pair(w8, z1[i], magic);
+          d[3][i] = code_pair16(w8, z6[i], magic);
         }
         // MFMA e of a block: channel 8 m + e of row m (D = 64: channel
         // 8 (m / 2) + m % 2 + 2 e)
@@ -421,22 +518,21 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? W / 2 : W / 4) void k
   };
 
   Tile<D> ta, tb;
-  const int stride = 32 * TW;
   int tk = t_begin + 32 * tg;
   if (tk < t_end) {
     load(ta, tk, page_entry(tk));
-    int pg = page_entry(tk + stride);
+    int pg = page_entry(tk + step);
     while (true) {
       // past the end the next tile repeats real rows and is not computed
-      load(tb, min(tk + stride, (t_end - 1) & ~31), pg);
-      pg = page_entry(tk + 2 * stride);
+      load(tb, min(tk + step, (t_end - 1) & ~31), pg);
+      pg = page_entry(tk + 2 * step);
       compute(ta, tk);
-      tk += stride;
+      tk += step;
       if (tk >= t_end) break;
-      load(ta, min(tk + stride, (t_end - 1) & ~31), pg);
-      pg = page_entry(tk + 2 * stride);
+      load(ta, min(tk + step, (t_end - 1) & ~31), pg);
+      pg = page_entry(tk + 2 * step);
       compute(tb, tk);
-      tk += stride;
+      tk += step;
       if (tk >= t_end) break;
     }
   }
@@ -445,11 +541,11 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? W / 2 : W / 4) void k
   // wave's sums scaled to it, added in wave order.  Slab: the 16 rows of one row
   // tile and block, [row][channel] per wave.
   constexpr int DB = D < 128 ? D : 128, NEB = DB / 16;
-  float* slab = reinterpret_cast<float*>(lds) + W * 64 * NB;
+  float* slab = reinterpret_cast<float*>(lds) + W * 64 * NB + 2 * kMaxFlat;
   float* stat = slab + W * 16 * DB;  // [wave][2][16]
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    if (t) __syncthreads();
+    if (t || seg) __syncthreads();
     const float lt = sum_over_rows16(l[t]);
     if (c == 0) {
       stat[wave * 32 + r] = m[t];
@@ -489,53 +585,62 @@ __global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? W / 2 : W / 4) void k
           L += lw * __builtin_amdgcn_exp2f(stat[wv * 32 + rr] - Mr);
         }
         const uint32_t qi = row / (uint32_t)G;
-        const int64_t at = (int64_t)(q0 + qi) * a.Hq + (hg * HW + hx) * G + (row - qi * G);
+        const int64_t orow = (int64_t)(q0 + qi) * a.Hq + (hg * HW + hx) * G + (row - qi * G);
         if (whole) {
           const float inv = L == 0.0f ? 0.0f : 1.0f / L;
           const uint32_t lo = a.dtype == 1 ? f32_to_bf16_bits(o0 * inv) : f32_to_f16_bits(o0 * inv);
           const uint32_t hi = a.dtype == 1 ? f32_to_bf16_bits(o1 * inv) : f32_to_f16_bits(o1 * inv);
-          *reinterpret_cast<uint32_t*>(a.out + at * D + 128 * n + ch) = lo | (hi << 16);
+          *reinterpret_cast<uint32_t*>(a.out + orow * D + 128 * n + ch) = lo | (hi << 16);
           if (a.lse && ch == 0 && n == 0)
-            a.lse[at] = L == 0.0f ? kNegInf : (Mr + __builtin_log2f(L)) * 0.6931471805599453f;
+            a.lse[orow] = L == 0.0f ? kNegInf : (Mr + __builtin_log2f(L)) * 0.6931471805599453f;
         } else {
-          const int64_t nrow = a.T * a.Hq;
+          // partial result: a workgroup has two at most, of its first and its last unit
+          const int64_t slot = ((int64_t)(2 * blockIdx.x + (seg > 0)) * HW + hx) * urows + (row - row0);
           float* ws = static_cast<float*>(a.workspace);
-          float* part = ws + 2 * nrow * KS + (split * nrow + at) * D + 128 * n + ch;
-          *reinterpret_cast<float2*>(part) = make_float2(o0, o1);
-          if (ch == 0 && n == 0) *reinterpret_cast<float2*>(ws + 2 * (split * nrow + at)) = make_float2(Mr, L);
+          float2* stats = reinterpret_cast<float2*>(ws + (int64_t)2 * gridDim.x * HW * urows * D);
+          *reinterpret_cast<float2*>(ws + slot * D + 128 * n + ch) = make_float2(o0, o1);
+          if (ch == 0 && n == 0) stats[slot] = make_float2(Mr, L);
         }
       }
     }
   }
+  }
 }
 
-// Joins the partial results of the sequences that were split: a workgroup of
-// four waves per query row.  The weights of up to 256 splits at a time are made
-// by a thread each; then wave w adds splits w, w + 4, ..., whose loads do not wait
-// for one another, and the four sums meet in LDS.
-template <int D>
-__global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int chunk, int KS) {
+// Joins the partial results of the units that several workgroups shared: a
+// workgroup of four waves per query row.  It finds the shares as they did; the
+// weights of up to 256 pieces at a time are made by a thread each; then wave w
+// adds pieces w, w + 4, ..., whose loads do not wait for one another, and the four
+// sums meet in LDS.
+template <int D, int RT>
+__global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int HW, int step, int urows, uint32_t wgs) {
   constexpr int C = D / 64;
   __shared__ float wt[256], red[8], sum[4][D];
+  __shared__ uint32_t shares[2 * kMaxFlat];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int HG = a.Hkv / HW, G = a.Hq / a.Hkv;
   uint32_t id = blockIdx.x;
   const int hq = id % (uint32_t)a.Hq;
   id /= (uint32_t)a.Hq;
   const int qi = id % (uint32_t)a.max_queries, b = id / (uint32_t)a.max_queries;
-  int q0 = b, nq = 1;
-  if (a.q_starts) {
-    q0 = max(a.q_starts[b], 0);
-    nq = (int)min((int64_t)a.q_starts[b + 1], a.T) - q0;
-  }
-  const int len = (int)min((int64_t)a.lens[b], a.max_context);
-  if (qi >= nq || len <= chunk) return;
-  const int n = (int)(((int64_t)len + chunk - 1) / chunk);
-  const int64_t nrow = a.T * a.Hq, at = (int64_t)(q0 + qi) * a.Hq + hq;
+  int q0;
+  if (qi >= queries_of(a, b, &q0)) return;
+  const Shares sh = scan_shares(a, wgs, HG, 16 * RT, step, lane, shares);
+  const uint32_t before = shares[b], steps = shares[kMaxFlat + b];
+  const int kvh = hq / G, row = qi * G + hq % G, row0 = row / (16 * RT) * (16 * RT);
+  const uint32_t u0 = before + (uint32_t)(row0 / (16 * RT) * HG + kvh / HW) * steps, u1 = u0 + steps;
+  // the workgroups of its first and last step
+  const uint32_t w0 = (uint32_t)(((uint64_t)(u0 + 1) * sh.n - 1) / sh.total);
+  const uint32_t w1 = (uint32_t)(((uint64_t)u1 * sh.n - 1) / sh.total);
+  if (w0 == w1) return;  // one workgroup had all of it
+  const int n = (int)(w1 - w0) + 1;
+  const int late = share_start(sh.total, w0, sh.n) < u0;  // for w0 it was the last unit, for the others the first
   const float* ws = static_cast<const float*>(a.workspace);
-  const float2* stat = reinterpret_cast<const float2*>(ws) + at;
-  const float* part = ws + 2 * nrow * KS + at * D + lane * C;
+  const float2* stats = reinterpret_cast<const float2*>(ws + (int64_t)2 * wgs * HW * urows * D);
+  const int in_slot = kvh % HW * urows + (row - row0);
+  auto slot = [&](int s) -> int64_t { return (int64_t)(2 * (w0 + s) + (s == 0 ? late : 0)) * HW * urows + in_slot; };
   float M = kNegInf;
-  for (int s = threadIdx.x; s < n; s += 256) M = fmaxf(M, stat[s * nrow].x);
+  for (int s = threadIdx.x; s < n; s += 256) M = fmaxf(M, stats[slot(s)].x);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) M = fmaxf(M, __shfl_xor(M, d));
   if (lane == 0) red[wave] = M;
@@ -548,8 +653,8 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int chu
     const int here = min(256, n - s0);
     if (s0) __syncthreads();
     if ((int)threadIdx.x < here) {
-      const float2 ml = stat[(s0 + threadIdx.x) * nrow];
-      const float k = ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - M);  // 0: the split saw nothing
+      const float2 ml = stats[slot(s0 + threadIdx.x)];
+      const float k = ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - M);  // 0: the piece saw nothing
       wt[threadIdx.x] = k;
       L += ml.y * k;
     }
@@ -557,7 +662,7 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int chu
 #pragma unroll 4
     for (int s = wave; s < here; s += 4) {
       const float k = wt[s];
-      const float* p = part + (s0 + s) * nrow * D;
+      const float* p = ws + slot(s0 + s) * D + lane * C;
 #pragma unroll
       for (int i = 0; i < C; ++i) o[i] += p[i] * k;
     }
@@ -570,17 +675,18 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int chu
   __syncthreads();
   L = red[4] + red[5] + red[6] + red[7];
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const int64_t orow = (int64_t)(q0 + qi) * a.Hq + hq;
   for (int x = threadIdx.x; x < D; x += 256) {
     const float v = (sum[0][x] + sum[1][x] + sum[2][x] + sum[3][x]) * inv;
-    a.out[at * D + x] = a.dtype == 1 ? f32_to_bf16_bits(v) : f32_to_f16_bits(v);
+    a.out[orow * D + x] = a.dtype == 1 ? f32_to_bf16_bits(v) : f32_to_f16_bits(v);
   }
-  if (a.lse && threadIdx.x == 0) a.lse[at] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
+  if (a.lse && threadIdx.x == 0) a.lse[orow] = L == 0.0f ? kNegInf : (M + __builtin_log2f(L)) * 0.6931471805599453f;
 }
 
 template <int D>
 size_t lds_bytes(int W) {
   constexpr int DB = D < 128 ? D : 128;
-  return (size_t)W * (64 * Tile<D>::NB + 16 * DB + 32) * 4;
+  return ((size_t)W * (64 * Tile<D>::NB + 16 * DB + 32) + 2 * kMaxFlat) * 4;
 }
 
 template <int D, int RT, int W, bool P32>
@@ -589,12 +695,11 @@ hipError_t launch_main(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream)
   const size_t lds = lds_bytes<D>(W);
   hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&kv_attn_kernel<D, RT, W, P32>), lds, raised);
   if (e != hipSuccess) return e;
-  const int64_t grid = (int64_t)a.B * p.KS * (a.Hkv / p.HW) * p.rtiles;
-  kv_attn_kernel<D, RT, W, P32><<<(unsigned)grid, 64 * W, lds, stream>>>(a, p.HW, (int)p.chunk, (int)p.KS, (int)p.rtiles);
+  kv_attn_kernel<D, RT, W, P32><<<(unsigned)p.grid, 64 * W, lds, stream>>>(a, p.HW, p.rtiles, p.urows, p.flat);
   e = hipGetLastError();
-  if (e != hipSuccess || p.KS == 1) return e;
+  if (e != hipSuccess || !p.flat) return e;
   const int64_t rows = (int64_t)a.B * a.max_queries * a.Hq;
-  kv_attn_join_kernel<D><<<(unsigned)rows, 256, 0, stream>>>(a, (int)p.chunk, (int)p.KS);
+  kv_attn_join_kernel<D, RT><<<(unsigned)rows, 256, 0, stream>>>(a, p.HW, 32 * (W / p.HW), p.urows, (uint32_t)p.grid);
   return hipGetLastError();
 }
 
@@ -613,15 +718,14 @@ hipError_t launch_rt(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream) {
 size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context,
                                int64_t max_queries) {
   const KvPlan p = plan_kv(T, B, Hq, Hkv, D, page, max_context, max_queries);
-  return p.KS == 1 ? 0 : (size_t)p.KS * T * Hq * (D + 2) * 4;
+  return p.flat ? (size_t)2 * p.grid * p.HW * p.urows * (D + 2) * 4 : 0;
 }
 
 int describe_kv_attn(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries,
                      char* buf, size_t len) {
   const KvPlan p = plan_kv(T, B, Hq, Hkv, D, page, max_context, max_queries);
-  return snprintf(buf, len, "kv_attn_kernel<D=%d, RT=%d, W=%d, P32=%d> grid=%lld block=%d heads=%d chunk=%lld splits=%lld",
-                  D, p.RT, p.W, page % 32 == 0 ? 1 : 0, (long long)(B * p.KS * (Hkv / p.HW) * p.rtiles), 64 * p.W, p.HW,
-                  (long long)p.chunk, (long long)p.KS);
+  return snprintf(buf, len, "kv_attn_kernel<D=%d, RT=%d, W=%d, P32=%d> grid=%lld block=%d heads=%d %s", D, p.RT, p.W,
+                  page % 32 == 0 ? 1 : 0, (long long)p.grid, 64 * p.W, p.HW, p.flat ? "shared steps" : "whole units");
 }
 
 hipError_t launch_kv_attn(const KvAttnArgs& a, hipStream_t stream) {
