@@ -576,10 +576,11 @@ int wq_prompt_attention(const void* q, const void* k, const void* v, int dtype, 
  * one rounding at the end.  A query that sees no token gets zeros (lse: -inf).
  * out [T][Hq][D] contiguous, 16-byte aligned; lse as above (or NULL); rows of T
  * outside every sequence keep what they held.  scale finite and positive.
- *   workspace  wq_kv_attention_workspace_bytes bytes, 256-byte aligned, for
- * the partial results of contexts split across workgroups; its content needs
- * no initialisation and is not used after the call's work, so calls ordered on
- * one stream may share it, concurrent ones (graphs included) may not.
+ *   workspace  wq_kv_attention_workspace_bytes bytes, 256-byte aligned, needed
+ * where a sequence's tokens are shared out to several workgroups; its content
+ * needs no initialisation and is not used after the call's work, so calls
+ * ordered on one stream may share it, concurrent ones (graphs replayed at the
+ * same time included) may not.
  * WQ_EWORKSPACE when missing or too small.  Preconditions: finite scales and
  * block contents in attended rows. */
 int wq_kv_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D, int64_t q_stride,
