@@ -99,21 +99,22 @@ def test_cache_refusals():
 
 
 def test_cache_plans_and_their_workspace():
-    """Few sequences and heads with long contexts are cut into pieces (whose
-    results need a workspace, within the launch's counters); many, or short ones,
-    are a workgroup each."""
-    for T, Hq, Hkv, D, nb, page, ctx, nq, cut in [
+    """Long contexts of few sequences and heads are shared out equally (with a
+    workspace for the results of the units that several workgroups hold); many,
+    or short ones, are a workgroup each."""
+    for T, Hq, Hkv, D, nb, page, ctx, nq, shared in [
             (1, 64, 8, 128, 1, 16, 1, 1, False), (1, 64, 8, 128, 1, 16, 200, 1, False), (64, 64, 8, 128, 64, 64, 8192, 1, True),
             (1, 8, 1, 256, 1, 256, 131072, 1, True), (16, 8, 8, 64, 4, 8, 5000, 4, True), (512, 64, 8, 128, 1, 64, 16384, 512, False),
             (1, 6, 3, 256, 1, 1, 10 ** 6, 1, True), (600, 8, 8, 128, 600, 16, 8192, 1, False), (257, 1, 1, 128, 257, 16, 65536, 1, False)]:
         d = wq.wq_kv_attention_plan(T, Hq, Hkv, D, nb, page, ctx, nq)
-        grid, heads, rt = (int(re.search(n + r"=(\d+)", d).group(1)) for n in ("grid", "heads", "RT"))
+        grid, heads, rt = (int(re.search(n + r"=(\d+)", d).group(1)) for n in ("grid", "HP", "RT"))
         rows = nq * Hq // Hkv
+        assert Hkv % heads == 0 and heads * D in (128, 256), d
         units = nb * (Hkv // heads) * (-(-rows // (16 * rt)))
         need = wq.wq_kv_attention_workspace_bytes(T, Hq, Hkv, D, nb, page, ctx, nq)
-        assert (d.split()[-1] == "pieces") == cut == (need > 0), d
-        assert units < grid <= 1024 if cut else grid == units, d
-        assert need == (4096 + grid * heads * min(rows, 16 * rt) * (D + 2) * 4 if cut else 0), d
+        assert (d.split()[-1] == "shares") == shared == (need > 0), d
+        assert grid <= 512 if shared else grid == units, d
+        assert need == (2 * grid * heads * min(rows, 16 * rt) * (D + 2) * 4 if shared else 0), d
 
 
 def test_binding_rejects_before_any_call():

@@ -633,7 +633,7 @@ size_t wq_kv_attention_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int64_
                                        int64_t max_context, int64_t max_queries) {
   if (check_kv_attn(WQ_BF16, T, Hq, Hkv, D, B, page_size, max_context, max_queries)) return 0;
   if (T == 0 || B == 0 || max_queries == 0) return 0;
-  return wq::kv_attn_workspace_bytes(T, (int)B, Hq, Hkv, D, page_size, max_context, max_queries);
+  return wq::kv_attn_workspace_bytes((int)B, Hq, Hkv, D, max_context, max_queries);
 }
 
 int wq_kv_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size, int64_t max_context,
@@ -643,7 +643,7 @@ int wq_kv_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_
   const int st = check_kv_attn(WQ_BF16, T, Hq, Hkv, D, B, page_size, max_context, max_queries);
   if (st) return st;
   if (T == 0 || B == 0 || max_queries == 0) return WQ_OK;
-  wq::describe_kv_attn(T, (int)B, Hq, Hkv, D, page_size, max_context, max_queries, buf, buf_len);
+  wq::describe_kv_attn((int)B, Hq, Hkv, D, page_size, max_context, max_queries, buf, buf_len);
   return WQ_OK;
 }
 
@@ -669,7 +669,7 @@ int wq_kv_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D,
       !aligned(lse, 4))
     return WQ_EALIGN;
   const size_t need =
-      wq::kv_attn_workspace_bytes(T, (int)B, Hq, Hkv, D, page_size, max_context, max_queries);
+      wq::kv_attn_workspace_bytes((int)B, Hq, Hkv, D, max_context, max_queries);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return WQ_EWORKSPACE;
     if (!aligned(workspace, 256)) return WQ_EALIGN;

@@ -118,10 +118,9 @@ struct KvAttnArgs {
   float* lse;
   void* workspace;
 };
-size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context,
-                               int64_t max_queries);
-int describe_kv_attn(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries,
-                     char* buf, size_t len);
+size_t kv_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_queries);
+int describe_kv_attn(int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries, char* buf,
+                     size_t len);
 hipError_t launch_kv_attn(const KvAttnArgs& a, hipStream_t stream);
 
 // Causal attention over packed prompts (wq_prompt_attn.hip).

@@ -30,11 +30,14 @@
 // pair of tokens turns them into words of one channel's token pairs.
 //
 // Reading is the bound: 2 (D/2 + 2.5 D/128) bytes a token and KV head.  A wave
-// walks 32-token tiles of one KV head, the next tile's codes in flight while it
-// computes; a workgroup's waves take neighbouring KV heads of the same tokens or
-// different tiles of one head and join in LDS.  Where sequences and heads are too
-// few to fill the GPU their walks are cut into pieces, whose fp32 results the last
-// workgroup of each to arrive joins.
+// walks 32-token tiles, the next tile's codes in flight while it computes.  It takes as many
+// neighbouring KV heads as fill a 128-byte line (two of 128 values): what a CU
+// can have in flight is bounded by the lines of its 32 KB cache, and half-used
+// lines halve it (one head a wave read 4.4 TB/s where two read 5.0).  The waves of
+// a workgroup take different tiles of the same heads and join in LDS.  Where
+// sequences and heads are too few to fill the GPU evenly, all steps of all units
+// are shared out equally; units that end up in several workgroups leave fp32
+// results which a second kernel joins.
 #include <stdio.h>
 
 #include "wq_device.h"
@@ -50,40 +53,41 @@ constexpr float kNegInf = -__builtin_inff();
 // (fp16 weights stay below 2^9, the fp32 sums far below their limits), so that it
 // rarely moves.
 constexpr float kLag = 8.0f;
-constexpr int kMaxShared = 256;  // sequences that a wave scans for its piece
+constexpr int kShares = 512;     // workgroups that steps are shared out to
+constexpr int kMaxShared = 256;  // sequences that a wave scans for its share
+constexpr int kMinSteps = 4;     // steps of a share, so that joining stays cheap
 constexpr int kMeta = 160;       // words of a wave's scales and zero-points of a tile and block
-constexpr int kMinSteps = 4;     // steps of a piece, so that joining stays cheap
-constexpr int kCounters = 1024;  // pieces that a launch can have
+
+constexpr int kWaves = 4;
 
 struct KvPlan {
-  int HW;        // KV heads of a workgroup (its W / HW waves per head take different tiles)
-  int RT;        // 16-row tiles of a wave
-  int W;         // waves of a workgroup
+  int HP;        // KV heads of a wave
+  int RT;        // 16-row tiles of a head
   int rtiles;    // units along the query rows of one KV head
-  int urows;     // query rows of a unit that a call can use
-  int share;     // workgroups that the steps of all units are shared out to (0: one unit a workgroup)
+  int urows;     // query rows of a unit and head that a call can use
+  bool flat;     // the steps of all units are shared out equally (else one unit a workgroup)
   int64_t grid;  // workgroups launched
 };
 
-// A unit is HW heads of one sequence and one tile of query rows; its steps are
-// the runs of 32 W / HW tokens that its waves take together.  With fewer units
-// than the GPU holds workgroups they are cut into pieces of equal length (on the
-// device, where the lengths are).
-KvPlan plan_kv(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries) {
+// A unit is HP heads of one sequence and one tile of query rows; its steps are
+// the runs of 32 kWaves tokens that a workgroup's waves take together.
+KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_queries) {
   KvPlan p;
   const int64_t G = Hq / Hkv, rows = max_queries * G;
-  p.RT = rows <= 16 ? 1 : 2;
-  p.W = 8;
+  // more than 16 rows: two tiles share the decoded codes (D = 256: no registers for them)
+  p.RT = rows <= 16 || D == 256 ? 1 : 2;
   p.rtiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
   p.urows = (int)(rows < 16 * p.RT ? rows : 16 * p.RT);
-  p.HW = Hkv % 2 == 0 ? 2 : 1;
-  const int64_t want = 512;
-  if ((int64_t)B * (Hkv / p.HW) * p.rtiles < want / 4) p.HW = 1;
-  const int64_t units = (int64_t)B * (Hkv / p.HW) * p.rtiles;
-  const int64_t steps = (max_context + 32 * (p.W / p.HW) - 1) / (32 * (p.W / p.HW));
-  const bool cut = units < want && steps >= 2 * kMinSteps && B <= kMaxShared;
-  p.share = cut ? (int)want : 0;
-  p.grid = cut ? units + want : units;
+  const int64_t steps = (max_context + 32 * kWaves - 1) / (32 * kWaves);
+  // two heads of 128 to a wave once that fills the GPU (below, twice the waves
+  // count more)
+  p.HP = D == 64 ? 2 : 1;
+  if (D == 128 && p.RT == 1 && Hkv % 2 == 0 && (int64_t)B * (Hkv / 2) * p.rtiles * steps >= 2 * kShares) p.HP = 2;
+  const int64_t units = (int64_t)B * (Hkv / p.HP) * p.rtiles;
+  // two workgroups a CU
+  const int64_t n = units * steps / kMinSteps < kShares ? units * steps / kMinSteps : kShares;
+  p.flat = units < 2 * kShares && n > units / 2 && steps >= 2 * kMinSteps && B <= kMaxShared;
+  p.grid = p.flat ? n : units;
   return p;
 }
 
@@ -108,59 +112,55 @@ __device__ __forceinline__ uint32_t steps_of(int len, int step) {
   return max((uint32_t)(len + step - 1) / (uint32_t)step, 1u);
 }
 
-// The piece of workgroup `id` when the units are cut, found by every wave for
-// itself from the lengths.
-struct Piece {
-  int b, rt, hg;   // its unit
-  int k, n;        // piece k of the unit's n
-  uint32_t first;  // piece 0 of the unit (pieces of a unit are HG apart)
+// Equal shares of the steps of all units: with n workgroups and total = q n + r
+// steps the first r take q + 1, the others q.  They follow from the lengths alone,
+// which only the device knows: every wave scans all of them and writes the same
+// words to LDS, so none waits for another.
+struct Shares {
+  uint32_t n, q, r;
 };
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v, int lane) {  // inclusive
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t up = (uint32_t)__shfl_up((int)v, d);
-    v += lane >= d ? up : 0u;
-  }
-  return v;
-}
-__device__ __forceinline__ bool find_piece(const KvAttnArgs& a, uint32_t id, uint32_t share, int G, int HG, int row_tile,
-                                           int step, int lane, Piece* p) {
-  uint32_t units[kMaxShared / 64], steps[kMaxShared / 64], total = 0;
-#pragma unroll
-  for (int w = 0; w < kMaxShared / 64; ++w) {
-    units[w] = steps[w] = 0;
-    const int b = 64 * w + lane;
+struct ShareLds {  // of every sequence
+  uint32_t before[kMaxShared];  // steps before its units
+  uint32_t steps[kMaxShared];   // steps of each of them
+  int32_t len[kMaxShared], q0[kMaxShared], nq[kMaxShared];
+};
+__device__ __forceinline__ Shares scan_shares(const KvAttnArgs& a, uint32_t wgs, int HG, int row_tile, int step, int lane,
+                                              ShareLds* lds) {
+  uint32_t total = 0;
+  const int G = a.Hq / a.Hkv;
+  for (int w = 0; w < a.B; w += 64) {
+    const int b = w + lane;
+    uint32_t cost = 0, steps = 1;
+    int q0 = 0, nq = 0, len = 0;
     if (b < a.B) {
-      int q0;
-      units[w] = units_of(queries_of(a, b, &q0), G, HG, row_tile);
-      steps[w] = steps_of(length_of(a, b), step);
+      nq = queries_of(a, b, &q0);
+      len = length_of(a, b);
+      steps = steps_of(len, step);
+      cost = units_of(nq, G, HG, row_tile) * steps;
     }
-    if (64 * w < a.B) total += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(units[w] * steps[w], lane), 63);
-  }
-  const uint32_t size = max((total + share - 1) / share, (uint32_t)kMinSteps);  // steps of a piece
-  uint32_t before = 0;
+    uint32_t run = cost;
 #pragma unroll
-  for (int w = 0; w < kMaxShared / 64; ++w) {
-    if (64 * w >= a.B) break;
-    const uint32_t n = max((steps[w] + size - 1) / size, 1u);
-    const uint32_t incl = wave_scan(units[w] * n, lane);
-    const uint64_t past = __ballot(before + incl > id);
-    if (past) {
-      const int i = __builtin_ctzll(past);
-      const uint32_t ni = (uint32_t)__builtin_amdgcn_readlane((int)n, i);
-      const uint32_t start = before + (uint32_t)__builtin_amdgcn_readlane((int)(incl - units[w] * n), i);
-      const uint32_t x = id - start, y = x / (uint32_t)HG, rt = y / ni;
-      p->b = 64 * w + i;
-      p->hg = (int)(x - y * HG);
-      p->rt = (int)rt;
-      p->k = (int)(y - rt * ni);
-      p->n = (int)ni;
-      p->first = start + rt * ni * HG + p->hg;
-      return true;
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t up = (uint32_t)__shfl_up((int)run, d);
+      run += lane >= d ? up : 0u;
     }
-    before += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
+    lds->before[b] = total + run - cost;
+    lds->steps[b] = steps;
+    lds->len[b] = len;
+    lds->q0[b] = q0;
+    lds->nq[b] = nq;
+    total += (uint32_t)__builtin_amdgcn_readlane((int)run, 63);
   }
-  return false;
+  Shares s;
+  s.n = max(min(wgs, (total + kMinSteps - 1) / kMinSteps), 1u);
+  s.q = total / s.n;
+  s.r = total - s.q * s.n;
+  return s;
+}
+__device__ __forceinline__ uint32_t share_start(const Shares& s, uint32_t i) { return s.q * i + min(i, s.r); }
+__device__ __forceinline__ uint32_t share_of(const Shares& s, uint32_t at) {  // the share that holds a step
+  const uint32_t long_end = (s.q + 1) * s.r;
+  return at < long_end ? at / (s.q + 1) : s.r + (at - long_end) / s.q;
 }
 
 __device__ __forceinline__ float max_over_rows16(float v) {  // over the lanes l, l ^ 16, l ^ 32, l ^ 48
@@ -180,15 +180,6 @@ __device__ __forceinline__ float sum_over_rows16(float v) {
   return __builtin_bit_cast(float, (uint32_t)b[0]) + __builtin_bit_cast(float, (uint32_t)b[1]);
 }
 
-// Two floats of a piece's result, coherent across the chiplets' caches.
-__device__ __forceinline__ void store_agent(float* p, float x, float y) {
-  const uint64_t v = __builtin_bit_cast(uint32_t, x) | (uint64_t)__builtin_bit_cast(uint32_t, y) << 32;
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float2 load_agent(const float* p) {
-  const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return make_float2(__builtin_bit_cast(float, (uint32_t)v), __builtin_bit_cast(float, (uint32_t)(v >> 32)));
-}
 __device__ __forceinline__ void store_pair(const KvAttnArgs& a, int64_t at, float x, float y) {
   const uint32_t lo = a.dtype == 1 ? f32_to_bf16_bits(x) : f32_to_f16_bits(x);
   const uint32_t hi = a.dtype == 1 ? f32_to_bf16_bits(y) : f32_to_f16_bits(y);
@@ -215,547 +206,650 @@ __device__ __forceinline__ u4 code_pairs(uint32_t w, uint32_t z10, uint32_t z6, 
             as_u32(as_h2((w8 & 0x000F000Fu) | g.e10) - as_h2(z10)), as_u32(as_h2((w8 & 0x00F000F0u) | g.e6) - as_h2(z6))};
 }
 
-// One 32-token tile of one KV head as loaded, untouched.
-template <int D>
+// What a wave covers of a cache row, and one 32-token tile of it as loaded.
+template <int D, int HP>
 struct Tile {
-  static constexpr int NB = D == 256 ? 2 : 1;   // cache blocks of a head
-  static constexpr int KL = D / 64;             // 16-byte loads of a lane that cover the tile's K codes
+  static constexpr int NB = HP * D / 128;         // cache blocks
+  static constexpr int kChunks = HP * D / 32;     // 16-byte chunks of K codes of a token
+  static constexpr int kTok = 64 / kChunks;       // tokens of one 16-byte load a lane
+  static constexpr int KL = 32 / kTok;            // such loads
+  static constexpr int NV = D == 64 ? HP : NB;    // V words (D = 64: half words) of a lane and token
   u4 k[KL];
-  uint32_t v[8][NB];  // (D = 64: half words)
-  uint32_t s[NB];     // lanes 0..31: K scale of token l, lanes 32..63: V scale of token l - 32
-  uint32_t z;         // the zero-point byte beside it
-  bool ok;            // the tile's page (small pages: the page of the lane's token) exists
+  uint32_t v[8][NV];
+  uint32_t s;  // scales of the blocks (16 bits each): lanes 0..31 K's of token l, lanes 32..63 V's of token l - 32
+  uint32_t z;  // the zero-point byte beside them
+  bool ok;     // the tile's page (small pages: the page of the lane's token) exists
 };
 
-// K codes of a tile pass through LDS: they are loaded as whole 64-byte rows (four
-// lanes a token) and read as operands (16 tokens of one chunk).  Chunk j of token
-// t sits at k_place, so that those 16 fall in different banks.
-template <int D>
+// K codes of a tile pass through LDS: they are loaded as whole rows (4 or 8 lanes
+// a token) and read as operands (16 tokens of one chunk).  Chunk j of token t sits
+// at k_place, so that those 16 fall in different banks.
+template <int CHUNKS>
 __device__ __forceinline__ int k_place(int t, int j) {
-  return D == 64 ? j ^ (t >> 3 & 1) : D == 128 ? j ^ (t >> 2 & 3) : j ^ (t >> 1 & 7);
+  return CHUNKS == 4 ? j ^ (t >> 2 & 3) : j ^ (t >> 1 & 7);
 }
-// Words of LDS a wave walks with: scales and zero-points, K codes.
+// Words of LDS: a wave's scales, zero-points and K codes of a tile; over them, at
+// the end, its results of one row tile and block; then the waves' statistics and
+// the shares.
+template <int D, int HP>
+constexpr int kWalk = kMeta * Tile<D, HP>::NB + 128 * Tile<D, HP>::kChunks;
 template <int D>
-constexpr int kWave = kMeta * Tile<D>::NB + 4 * D;
+constexpr int kSlabRow = (D < 128 ? D : 128) + 4;  // padded: rows in different banks
+template <int D>
+constexpr int kSlab = 16 * kSlabRow<D>;
+template <int D, int HP>
+constexpr int kPerWave = kWalk<D, HP> > kSlab<D> ? kWalk<D, HP> : kSlab<D>;
+template <int D, int HP>
+constexpr int lds_words = kWaves * (kPerWave<D, HP> + 32) + sizeof(ShareLds) / 4;
 
-template <int D, int RT, int W, bool P32>
-__global__ __launch_bounds__(64 * W, RT == 1 && D <= 128 ? W / 2 : W / 4) void kv_attn_kernel(KvAttnArgs a, int HW, int rtiles,
-                                                                                             int urows, int share) {
-  constexpr int NB = Tile<D>::NB;
-  constexpr int NS = D / 32;  // MFMA steps of a score
-  constexpr int SB = NS / NB;
-  constexpr int NE = D / 16;  // MFMAs of an output tile: 16 channels each
-  constexpr int KL = Tile<D>::KL, kChunks = D / 32, kTok = 64 / kChunks;  // 16-byte chunks of a token, tokens of a load
+template <int D, int HP, int RT, bool P32>
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, int rtiles, int urows, bool flat) {
+  using T = Tile<D, HP>;
+  constexpr int NB = T::NB, X = HP * RT;  // blocks, row tiles of a wave (tile x: head x / RT)
+  constexpr int NH = D == 256 ? 2 : 1;    // blocks of a head
+  constexpr int NS = D / 32;              // MFMA steps of a score
+  constexpr int NE = D / 16;              // MFMAs of an output tile: 16 channels each
+  constexpr int kStep = 32 * kWaves;
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4, ml = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int TW = W / HW, tg = wave / HW, hw = wave - tg * HW, step = 32 * TW;
-  const int HG = a.Hkv / HW, G = a.Hq / a.Hkv;
+  const int HG = a.Hkv / HP, G = a.Hq / a.Hkv;
   const uint32_t rowb = (uint32_t)a.Hkv * (D / 2);  // code bytes of a cache row
   const uint32_t nbt = (uint32_t)a.Hkv * D / 128, zb = (nbt + 1) / 2;
   const int lg = 31 - __builtin_clz(a.page);
   const int pages = (int)(a.S >> lg);
-  float* meta = reinterpret_cast<float*>(lds) + wave * kWave<D>;
+  float* meta = reinterpret_cast<float*>(lds) + wave * kWalk<D, HP>;
   u4* kd = reinterpret_cast<u4*>(meta + kMeta * NB);
-
+  float* slab = reinterpret_cast<float*>(lds);
+  float* stat = slab + kWaves * kPerWave<D, HP>;  // [wave][2][16]
+  ShareLds* shares = reinterpret_cast<ShareLds*>(lds + kWaves * (kPerWave<D, HP> + 32));
   const Magic magic;
 
-  Piece u;
-  if (share) {
-    if (!find_piece(a, blockIdx.x, share, G, HG, 16 * RT, step, lane, &u)) return;
-  } else {
-    const uint32_t x = blockIdx.x / (uint32_t)HG;
-    u.hg = (int)(blockIdx.x - x * HG);
-    u.b = (int)(x / (uint32_t)rtiles);
-    u.rt = (int)(x - u.b * rtiles);
-    u.k = 0;
-    u.n = 1;
-    u.first = blockIdx.x;
-  }
-  const int b = u.b, hg = u.hg;
-  int q0;
-  const int nq = queries_of(a, b, &q0);
-  const int len = length_of(a, b);
-  const int row0 = u.rt * (16 * RT), rows = nq * G;
-  if (row0 >= rows) return;
-  const uint32_t steps = steps_of(len, step);
-  const int s0 = (int)((uint64_t)steps * u.k / (uint32_t)u.n), s1 = (int)((uint64_t)steps * (u.k + 1) / (uint32_t)u.n);
-  const int h = hg * HW + hw;
-  const int row1 = min(row0 + 16 * RT, rows) - 1;
-  // of these rows' tokens: what the last row sees ends the walk, what the first
-  // sees ends the tiles that need no mask
-  const int t_begin = s0 * step;
-  const int t_end = min((int)min((int64_t)s1 * step, (int64_t)len), len - nq + (int)((uint32_t)row1 / (uint32_t)G) + 1);
-  const int low = min(t_end, len - nq + (int)((uint32_t)row0 / (uint32_t)G) + 1);
+  // Workgroups go round the eight chiplets in turn; consecutive numbers here lie
+  // on one, so that the heads of a sequence share its L2 (their scales lie in the
+  // same lines).
+  const uint32_t xcd = blockIdx.x % 8;
+  const uint32_t wg = xcd * (gridDim.x / 8) + min(xcd, gridDim.x % 8) + blockIdx.x / 8;
 
-  // the wave's queries, as the B operand of the scores: lane (r, c) channels
-  // 32 c + 8 j (D = 64: 16 c + 8 j) of each block, brought into fp16's range by
-  // the power of two that takes the row's largest value into [1, 2)
-  h8 qf[RT][NS];
-  float f[RT];   // score of a row in units of log2: raw * f
-  int lim[RT];   // tokens the row sees, of those of this walk
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const uint32_t row = min(row0 + 16 * t + r, rows - 1);  // rows past the end repeat the last, not stored
-    const uint32_t qi = row / (uint32_t)G;
-    lim[t] = min(t_end, len - nq + (int)qi + 1);
-    const uint16_t* qp = a.q + (int64_t)(q0 + qi) * a.q_stride + (int64_t)(h * G + (int)(row - qi * G)) * D;
-    u4 raw[NS];
-#pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      const int ch = D == 64 ? 16 * c + 8 * j : 128 * (j / 4) + 32 * c + 8 * (j % 4);
-      raw[j] = *reinterpret_cast<const u4*>(qp + ch);
-    }
-    float x[NS][8], top_q = 0.0f;
-    if (a.dtype == 1) {
-#pragma unroll
-      for (int j = 0; j < NS; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          x[j][e] = __builtin_bit_cast(float, e % 2 ? raw[j][e / 2] & 0xffff0000u : raw[j][e / 2] << 16);
+  // this workgroup's steps, counted over all units
+  uint32_t at = 0, at_end = 1;
+  Shares sh{1, 1, 0};
+  if (flat) {
+    sh = scan_shares(a, gridDim.x, HG, 16 * RT, kStep, lane, shares);
+    if (wg >= sh.n) return;
+    at = share_start(sh, wg);
+    at_end = share_start(sh, wg + 1);
+  }
+  for (int seg = 0; at < at_end; ++seg) {
+    int b, rt, hg, s0 = 0, s1;
+    uint32_t u0 = 0, steps = 1;  // first step and steps of the unit
+    if (flat) {
+      // the last sequence whose units start at or before `at` (an empty one has
+      // the start of the next)
+      b = 0;
+      for (int w = 0; w < a.B; w += 64) {
+        const uint64_t le = __ballot(w + lane < a.B && shares->before[w + lane] <= at);
+        if (le) b = w + 63 - __builtin_clzll(le);
+      }
+      const uint32_t before = __builtin_amdgcn_readfirstlane(shares->before[b]);
+      steps = __builtin_amdgcn_readfirstlane(shares->steps[b]);
+      const uint32_t unit = (at - before) / steps;
+      rt = (int)(unit / (uint32_t)HG);
+      hg = (int)(unit - (uint32_t)rt * HG);
+      u0 = before + unit * steps;
+      s0 = (int)(at - u0);
+      s1 = (int)min(steps, (uint32_t)s0 + (at_end - at));
+      at += s1 - s0;
     } else {
-#pragma unroll
-      for (int j = 0; j < NS; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[j][e] = (float)__builtin_bit_cast(h8, raw[j])[e];
+      const uint32_t x = wg / (uint32_t)HG;
+      hg = (int)(wg - x * HG);
+      b = (int)(x / (uint32_t)rtiles);
+      rt = (int)(x - (uint32_t)b * rtiles);
+      at = 1;
     }
-#pragma unroll
-    for (int j = 0; j < NS; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top_q = fmaxf(top_q, fabsf(x[j][e]));
-    top_q = max_over_rows16(top_q);
-    int ex = (int)(__builtin_bit_cast(uint32_t, top_q) >> 23) - 127;
-    ex = min(max(ex, -126), 126);  // zeros, subnormals and infinities: the nearest power
-    const float down = __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23);
-    const float up = __builtin_bit_cast(float, (uint32_t)(127 + ex) << 23);
-    f[t] = a.scale * 1.4426950408889634f * up;
-#pragma unroll
-    for (int j = 0; j < NS; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) qf[t][j][e] = (_Float16)(x[j][e] * down);
-  }
+    int q0, nq, len;
+    if (flat) {
+      q0 = __builtin_amdgcn_readfirstlane(shares->q0[b]);
+      nq = __builtin_amdgcn_readfirstlane(shares->nq[b]);
+      len = __builtin_amdgcn_readfirstlane(shares->len[b]);
+    } else {
+      nq = queries_of(a, b, &q0);
+      len = length_of(a, b);
+      s1 = (int)(steps = steps_of(len, kStep));
+    }
+    const bool whole = s0 == 0 && s1 == (int)steps;
+    const int row0 = rt * (16 * RT), rows = nq * G;
+    if (row0 >= rows) return;
+    const int row1 = min(row0 + 16 * RT, rows) - 1;
+    // of these rows' tokens: what the last row sees ends the walk, what the first
+    // sees ends the tiles that need no mask
+    const int t_begin = s0 * kStep;
+    const int t_end = min((int)min((int64_t)s1 * kStep, (int64_t)len), len - nq + (int)((uint32_t)row1 / (uint32_t)G) + 1);
+    const int low = min(t_end, len - nq + (int)((uint32_t)row0 / (uint32_t)G) + 1);
 
-  f4 acc[RT][NE];
-  float m[RT], l[RT];  // weights are 2^(score - m); m follows the largest score + v_exp
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    m[t] = kNegInf;
-    l[t] = 0.0f;
-#pragma unroll
-    for (int e = 0; e < NE; ++e) acc[t][e] = f4{0, 0, 0, 0};
-  }
-  // V scales so far are at most v_top (fp16 bits) < 2^v_exp
-  uint32_t v_top = 0;
-  float v_exp = -25.0f;
+    const uint32_t blk = (uint32_t)hg * HP * D / 128;  // first block of the wave's heads
+    const int32_t* table = a.table + (int64_t)b * a.table_width;
+    const uint8_t* kc = a.k_codes + (uint32_t)hg * (HP * D / 2);
+    const uint8_t* vc = a.v_codes + (uint32_t)hg * (HP * D / 2);
+    int ln = lane;  // per-lane offsets are made here for each unit, not kept through the loop over units
+    asm volatile("" : "+v"(ln));
+    const uint16_t* sp = (ln < 32 ? a.k_s : a.v_s) + blk + (P32 ? (ln & 31) * nbt : 0);
+    const uint8_t* zp = (ln < 32 ? a.k_zp : a.v_zp) + blk / 2 + (P32 ? (ln & 31) * zb : 0);
+    const uint32_t k_at = 16 * (ln % T::kChunks) + (P32 ? ln / T::kChunks * rowb : 0);
+    const uint32_t v_at = (D == 64 ? 2 : 4) * (ln & 15) + (P32 ? 4 * (ln >> 4) * rowb : 0);
 
-  const uint32_t blk = (uint32_t)h * D / 128;  // first block of the head
-  const int zshift = D == 256 ? 0 : (blk & 1) * 4;
-  const int32_t* table = a.table + (int64_t)b * a.table_width;
-  const uint8_t* kc = a.k_codes + (uint32_t)h * (D / 2);
-  const uint8_t* vc = a.v_codes + (uint32_t)h * (D / 2);
-  const uint16_t* sp = (lane < 32 ? a.k_s : a.v_s) + blk + (P32 ? ml * nbt : 0);
-  const uint8_t* zp = (lane < 32 ? a.k_zp : a.v_zp) + blk / 2 + (P32 ? ml * zb : 0);
-  const uint32_t k_at = 16 * (lane % kChunks) + (P32 ? lane / kChunks * rowb : 0);
-  const uint32_t v_at = (D == 64 ? 2 : 4) * r + (P32 ? 4 * c * rowb : 0);
-
-  // page entries of a tile: one of the whole tile (P32) or one of lane ml's token
-  auto page_entry = [&](int tk) -> int {
-    if constexpr (P32) return table[min(tk, t_end - 1) >> lg];
-    return table[min(tk + ml, t_end - 1) >> lg];
-  };
-  // row of the tile's first token (P32) or of lane ml's token
-  auto rows_of = [&](int tk, int pg, bool* ok) -> int {
-    *ok = pg >= 0 && pg < pages;
-    return *ok ? (pg << lg) + ((P32 ? tk : tk + ml) & (a.page - 1)) : 0;  // none: the first rows of the cache
-  };
-  auto load_k = [&](Tile<D>& T, int row) {
+    // page entries of a tile: one of the whole tile (P32) or one of lane ml's token
+    auto page_entry = [&](int tk) -> int {
+      if constexpr (P32) return table[min(tk, t_end - 1) >> lg];
+      return table[min(tk + ml, t_end - 1) >> lg];
+    };
+    // row of the tile's first token (P32) or of lane ml's token
+    auto rows_of = [&](int tk, int pg, bool* ok) -> int {
+      *ok = pg >= 0 && pg < pages;
+      return *ok ? (pg << lg) + ((P32 ? tk : tk + ml) & (a.page - 1)) : 0;  // none: the first rows of the cache
+    };
+    auto load_k = [&](T& t, int row) {
+      const uint16_t* s = sp + (int64_t)row * nbt;
+      if constexpr (NB == 2) __builtin_memcpy(&t.s, s, 4);
+      else t.s = *s;
+      t.z = (zp + (int64_t)row * zb)[0];
+      uint32_t off = k_at;  // a lane's offset from a scalar address (not folded into a 64-bit one outside the loop)
+      asm volatile("" : "+v"(off));
 #pragma unroll
-    for (int n = 0; n < NB; ++n) T.s[n] = (sp + (int64_t)row * nbt)[n];
-    T.z = (zp + (int64_t)row * zb)[0];
-    uint32_t at = k_at;  // a lane's offset from a scalar address (not folded into a 64-bit one outside the loop)
-    asm volatile("" : "+v"(at));
-#pragma unroll
-    for (int i = 0; i < KL; ++i) {
-      const uint8_t* p = kc + (int64_t)(P32 ? row + kTok * i : __shfl(row, kTok * i + lane / kChunks)) * rowb;
-      if constexpr (P32) asm volatile("" : "+s"(p));
-      T.k[i] = *reinterpret_cast<const u4*>(p + at);
-    }
-  };
-  auto load_v = [&](Tile<D>& T, int row) {
-    uint32_t at = v_at;
-    asm volatile("" : "+v"(at));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = 16 * (i / 4) + i % 4;
-      const uint8_t* p = vc + (int64_t)(P32 ? row + t : __shfl(row, t + 4 * c)) * rowb;
-      if constexpr (P32) asm volatile("" : "+s"(p));  // the tile's rows: a scalar address
-      p += at;
-      if constexpr (D == 64) {
-        T.v[i][0] = *reinterpret_cast<const uint16_t*>(p);
-      } else {
-#pragma unroll
-        for (int n = 0; n < NB; ++n) T.v[i][n] = *reinterpret_cast<const uint32_t*>(p + 64 * n);
+      for (int i = 0; i < T::KL; ++i) {
+        const uint8_t* p = kc + (int64_t)(P32 ? row + T::kTok * i : __shfl(row, T::kTok * i + lane / T::kChunks)) * rowb;
+        if constexpr (P32) asm volatile("" : "+s"(p));
+        t.k[i] = *reinterpret_cast<const u4*>(p + off);
       }
-    }
-  };
-
-  // Works on tile tk; K and V of the next tile (rows `row`) replace this one's as
-  // soon as they are decoded.
-  auto compute = [&](Tile<D>& T, int tk, int row, bool next_ok) {
-    const bool ok = T.ok;
-    // scales and zero-points through LDS to the lanes that need them, in the form
-    // they need; a token that is not attended has 0 for all, whatever its cache
-    // row holds
-    const bool off = !ok || tk + ml >= t_end;
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const uint32_t z = off ? 0u : (D == 256 ? T.z >> (4 * n) : T.z >> zshift) & 15u;
-      const uint32_t sb = off ? 0u : T.s[n];
-      const float sv = f16_bits_to_f32((uint16_t)sb);
-      float* mn = meta + kMeta * n;
-      mn[lane] = sv;  // K's, then V's
-      const uint32_t z10 = z | 0x6400u, z6 = (z << 4) | 0x5400u;  // 1024 + z, 64 + z
-      if (lane < 32) {
-        *reinterpret_cast<u2*>(mn + 64 + 2 * ml) = u2{z10 * 0x00010001u, z6 * 0x00010001u};
-      } else {
-        reinterpret_cast<uint16_t*>(mn + 128)[ml] = (uint16_t)z10;
-        reinterpret_cast<uint16_t*>(mn + 144)[ml] = (uint16_t)z6;
-      }
-      // a V scale above all so far (rare): the next power of two from the largest
-      if (__ballot(lane >= 32 && sb > v_top)) {
-        uint32_t top = lane >= 32 ? sb & 0x7fffu : 0u;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-        top = __builtin_amdgcn_readfirstlane(top);
-        v_exp = (float)((int)(__builtin_bit_cast(uint32_t, f16_bits_to_f32((uint16_t)top)) >> 23) - 126);
-        v_top = top >> 10 ? top | 0x3ffu : 0xffffffffu >> __builtin_clz(top);
-      }
-    }
-    // tokens of small pages that do not exist, a bit each (P32: all or none)
-    const uint32_t gone = P32 ? 0u : ~(uint32_t)__ballot(ok);
-    const bool masked = tk + 32 > low || (P32 ? !ok : gone != 0);
-#pragma unroll
-    for (int i = 0; i < KL; ++i) {
-      const int t = kTok * i + lane / kChunks;
-      kd[t * kChunks + k_place<D>(t, lane % kChunks)] = T.k[i];
-    }
-    f4 sc[RT][2][NB];
-#pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        const int t16 = 16 * g + r;
-        uint32_t kw[SB];
-        if constexpr (D == 64) {
-          const u2 w = reinterpret_cast<const u2*>(kd + t16 * kChunks + k_place<D>(t16, c / 2))[c % 2];
-          kw[0] = w[0];
-          kw[1] = w[1];
-        } else {
-          const u4 w = kd[t16 * kChunks + k_place<D>(t16, 4 * n + c)];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) kw[j] = w[j];
-        }
-        const u2 z = *reinterpret_cast<const u2*>(meta + kMeta * n + 64 + 2 * (16 * g + r));
-#pragma unroll
-        for (int t = 0; t < RT; ++t) sc[t][g][n] = f4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < SB; ++j) {
-          const u4 d = code_pairs(kw[j], z[0], z[1], magic);
-#pragma unroll
-          for (int t = 0; t < RT; ++t)
-            sc[t][g][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, d), qf[t][SB * n + j],
-                                                                 sc[t][g][n], 0, 0, 0);
-        }
-      }
-    __builtin_amdgcn_sched_barrier(0);
-    load_k(T, row);
-    T.ok = next_ok;
-    // scores times their token's scale
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      f4 ks[NB];
-#pragma unroll
-      for (int n = 0; n < NB; ++n) ks[n] = *reinterpret_cast<const f4*>(meta + kMeta * n + 16 * g + 4 * c);
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sc[t][g][0][i] *= ks[0][i];
-          if constexpr (NB == 2) sc[t][g][0][i] = __builtin_fmaf(sc[t][g][1][i], ks[1][i], sc[t][g][0][i]);
-        }
-    }
-    f4 vs[NB][2];
-    u2 vz10[NB][2], vz6[NB][2];
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        vs[n][g] = *reinterpret_cast<const f4*>(meta + kMeta * n + 32 + 16 * g + 4 * c);
-        vz10[n][g] = *reinterpret_cast<const u2*>(meta + kMeta * n + 128 + 8 * g + 2 * c);
-        vz6[n][g] = *reinterpret_cast<const u2*>(meta + kMeta * n + 144 + 8 * g + 2 * c);
-      }
-    h8 pf[RT][NB];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      float s8[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s8[i] = sc[t][i / 4][0][i % 4];
-      if (masked) {
-        const int seen = P32 && !ok ? 0 : lim[t] - tk;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int tok = 16 * (i / 4) + 4 * c + i % 4;
-          if (tok >= seen || (!P32 && (gone >> tok & 1))) s8[i] = kNegInf;
-        }
-      }
-      float mx = s8[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s8[i]);
-      mx = __builtin_fmaf(max_over_rows16(mx), f[t], v_exp);
-      if (__ballot(mx > m[t] + kLag)) {
-        const float mn = fmaxf(m[t], mx);
-        const float al = m[t] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[t] - mn);
-        m[t] = mn;
-        l[t] *= al;
-#pragma unroll
-        for (int e = 0; e < NE; ++e) acc[t][e] *= al;
-      }
-      const float ms = m[t] == kNegInf ? 0.0f : m[t];
+    };
+    auto load_v = [&](T& t, int row) {
+      uint32_t off = v_at;
+      asm volatile("" : "+v"(off));
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s8[i], f[t], -ms));
-        l[t] += p;
+        const int tok = 16 * (i / 4) + i % 4;
+        const uint8_t* p = vc + (int64_t)(P32 ? row + tok : __shfl(row, tok + 4 * c)) * rowb;
+        if constexpr (P32) asm volatile("" : "+s"(p));
+        p += off;
 #pragma unroll
-        for (int n = 0; n < NB; ++n) pf[t][n][i] = (_Float16)(p * vs[n][i / 4][i % 4]);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    // O^T += V^T P^T, 16 channels an MFMA
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      // 1024 + z and 64 + z of the token pairs
-      const u4 z10 = {vz10[n][0][0], vz10[n][0][1], vz10[n][1][0], vz10[n][1][1]};
-      const u4 z6 = {vz6[n][0][0], vz6[n][0][1], vz6[n][1][0], vz6[n][1][1]};
-#pragma unroll
-      for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
-        u4 d[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // even (odd) channels of two tokens
-          const u4 x = code_pairs(
-              __builtin_amdgcn_perm(T.v[2 * i + 1][n], T.v[2 * i][n], half ? 0x07060302u : 0x05040100u), z10[i],
-              z6[i], magic);
-#pragma unroll
-          for (int p = 0; p < 4; ++p) d[p][i] = x[p];
+        for (int n = 0; n < T::NV; ++n) {
+          if constexpr (D == 64) t.v[i][n] = *reinterpret_cast<const uint16_t*>(p + 32 * n);
+          else t.v[i][n] = *reinterpret_cast<const uint32_t*>(p + 64 * n);
         }
-        // MFMA e of a block: channel 8 m + e of row m (D = 64: channel
-        // 8 (m / 2) + m % 2 + 2 e)
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            const int e = D == 64 ? p : 8 * n + 2 * p + half;
-            acc[t][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, d[p]), pf[t][n], acc[t][e], 0, 0, 0);
-          }
       }
-    }
-  };
+    };
 
-  Tile<D> tile;
-  int tk = t_begin + 32 * tg;
-  if (tk < t_end) {
-    int row = rows_of(tk, page_entry(tk), &tile.ok);
-    load_k(tile, row);
-    load_v(tile, row);
-    int pg = page_entry(tk + step);
-    do {
-      // past the end the next tile repeats real rows and is not used
-      bool ok;
-      row = rows_of(min(tk + step, (t_end - 1) & ~31), pg, &ok);
-      pg = page_entry(tk + 2 * step);
-      compute(tile, tk, row, ok);
+    T tile;
+    int tk = t_begin + 32 * wave, row = 0, pg = 0;
+    if (tk < t_end) {
+      row = rows_of(tk, page_entry(tk), &tile.ok);
+      load_k(tile, row);
       load_v(tile, row);
-      tk += step;
-    } while (tk < t_end);
-  }
-
-  // Waves of one head join through LDS: the largest reference point, every
-  // wave's sums scaled to it, added in wave order.  Slab: the 16 rows of one row
-  // tile and block, [row][channel] per wave.
-  constexpr int DB = D < 128 ? D : 128, NEB = DB / 16;
-  // indices made here, not kept in registers through the walk
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));
-  const int re = tid & 15, ce = (tid & 63) >> 4;
-  // pieces' results: [piece][head of the unit][row], (reference point, sum) and sums
-  float* stats = static_cast<float*>(a.workspace) + kCounters;
-  float* part = stats + (int64_t)2 * gridDim.x * HW * urows;
-  float* slab = reinterpret_cast<float*>(lds);  // over what the waves walked with (they meet before it is written)
-  float* stat = slab + W * (kWave<D> > 16 * DB ? kWave<D> : 16 * DB);  // [wave][2][16]
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    if (t) __syncthreads();
-    const float lt = sum_over_rows16(l[t]);
-    if (ce == 0) {
-      stat[wave * 32 + re] = m[t];
-      stat[wave * 32 + 16 + re] = lt;
+      pg = page_entry(tk + kStep);
     }
-    __syncthreads();
-    float M = kNegInf;
-    for (int g = 0; g < TW; ++g) M = fmaxf(M, stat[(hw + HW * g) * 32 + re]);
-    // a wave whose sum is 0 saw nothing (a NaN sum stays one)
-    const float k = lt == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[t] - M);
+
+    // the wave's queries, as the B operand of the scores: lane (r, c) channels
+    // 32 c + 8 j (D = 64: 16 c + 8 j) of each block, brought into fp16's range by
+    // the power of two that takes the row's largest value into [1, 2)
+    h8 qf[X][NS];
+    float f[X];   // score of a row in units of log2: raw * f
+    int lim[RT];  // tokens the row sees, of those of this walk
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      if (n) __syncthreads();
+    for (int x = 0; x < X; ++x) {
+      const int t = x % RT;
+      const uint32_t qrow = min(row0 + 16 * t + r, rows - 1);  // rows past the end repeat the last, not stored
+      const uint32_t qi = qrow / (uint32_t)G;
+      lim[t] = min(t_end, len - nq + (int)qi + 1);
+      const int head = (hg * HP + x / RT) * G + (int)(qrow - qi * G);
+      const uint16_t* qp = a.q + (int64_t)(q0 + qi) * a.q_stride + (int64_t)head * D;
+      u4 raw[NS];
 #pragma unroll
-      for (int e = 0; e < NEB; ++e)
+      for (int j = 0; j < NS; ++j) {
+        const int ch = D == 64 ? 16 * c + 8 * j : 128 * (j / 4) + 32 * c + 8 * (j % 4);
+        raw[j] = *reinterpret_cast<const u4*>(qp + ch);
+      }
+      float y[NS][8], top_q = 0.0f;
+      if (a.dtype == 1) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            y[j][e] = __builtin_bit_cast(float, e % 2 ? raw[j][e / 2] & 0xffff0000u : raw[j][e / 2] << 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[j][e] = (float)__builtin_bit_cast(h8, raw[j])[e];
+      }
+#pragma unroll
+      for (int j = 0; j < NS; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top_q = fmaxf(top_q, fabsf(y[j][e]));
+      top_q = max_over_rows16(top_q);
+      int ex = (int)(__builtin_bit_cast(uint32_t, top_q) >> 23) - 127;
+      ex = min(max(ex, -126), 126);  // zeros, subnormals and infinities: the nearest power
+      const float down = __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23);
+      const float up = __builtin_bit_cast(float, (uint32_t)(127 + ex) << 23);
+      f[x] = a.scale * 1.4426950408889634f * up;
+#pragma unroll
+      for (int j = 0; j < NS; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) qf[x][j][e] = (_Float16)(y[j][e] * down);
+    }
+
+    f4 acc[X][NE];
+    float m[X], l[X];  // weights are 2^(score - m); m follows the largest score + v_exp
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      m[x] = kNegInf;
+      l[x] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) acc[x][e] = f4{0, 0, 0, 0};
+    }
+    // V scales so far are at most v_top (fp16 bits) < 2^v_exp, for each block (a
+    // head of two: for both)
+    constexpr int NT = NB / NH;
+    uint32_t v_top[NT];
+    float v_exp[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) v_top[n] = 0, v_exp[n] = -25.0f;
+
+    // Works on tile tk; K and V of the next tile (rows `row`) replace this one's as
+    // soon as they are decoded.
+    auto compute = [&](int next, bool next_ok) {
+      const bool ok = tile.ok;
+      // scales and zero-points through LDS to the lanes that need them, in the
+      // form they need; a token that is not attended has 0 for all, whatever its
+      // cache row holds
+      const bool off = !ok || tk + ml >= t_end;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const int zshift = NB == 2 ? 4 * n : (int)(blk & 1) * 4;
+        const uint32_t z = off ? 0u : (tile.z >> zshift) & 15u;
+        const uint32_t sb = off ? 0u : (tile.s >> (16 * n)) & 0xffffu;
+        const float sv = f16_bits_to_f32((uint16_t)sb);
+        float* mn = meta + kMeta * n;
+        mn[lane] = sv;  // K's, then V's
+        const uint32_t z10 = z | 0x6400u, z6 = (z << 4) | 0x5400u;  // 1024 + z, 64 + z
+        if (lane < 32) {
+          *reinterpret_cast<u2*>(mn + 64 + 2 * ml) = u2{z10 * 0x00010001u, z6 * 0x00010001u};
+        } else {
+          reinterpret_cast<uint16_t*>(mn + 128)[ml] = (uint16_t)z10;
+          reinterpret_cast<uint16_t*>(mn + 144)[ml] = (uint16_t)z6;
+        }
+        // a V scale above all so far (rare): the next power of two from the largest
+        if (__ballot(lane >= 32 && sb > v_top[n / NH])) {
+          uint32_t top = lane >= 32 ? sb & 0x7fffu : 0u;
+#pragma unroll
+          for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+          top = __builtin_amdgcn_readfirstlane(top);
+          v_exp[n / NH] = (float)((int)(__builtin_bit_cast(uint32_t, f16_bits_to_f32((uint16_t)top)) >> 23) - 126);
+          v_top[n / NH] = top >> 10 ? top | 0x3ffu : 0xffffffffu >> __builtin_clz(top);
+        }
+      }
+      // tokens of small pages that do not exist, a bit each (P32: all or none)
+      const uint32_t gone = P32 ? 0u : ~(uint32_t)__ballot(ok);
+      const bool masked = tk + 32 > low || (P32 ? !ok : gone != 0);
+#pragma unroll
+      for (int i = 0; i < T::KL; ++i) {
+        const int t = T::kTok * i + lane / T::kChunks;
+        kd[t * T::kChunks + k_place<T::kChunks>(t, lane % T::kChunks)] = tile.k[i];
+      }
+      f4 sc[X][2][NH];
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int p = 0; p < HP; ++p)
+#pragma unroll
+          for (int n = 0; n < NH; ++n) {
+            const int t16 = 16 * g + r, blkn = D == 64 ? p / 2 : p + n;
+            uint32_t kw[NS / NH];
+            if constexpr (D == 64) {
+              const u2 w = reinterpret_cast<const u2*>(kd + t16 * T::kChunks + k_place<T::kChunks>(t16, 2 * p + c / 2))[c % 2];
+              kw[0] = w[0];
+              kw[1] = w[1];
+            } else {
+              const u4 w = kd[t16 * T::kChunks + k_place<T::kChunks>(t16, 4 * (p + n) + c)];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) kw[j] = w[j];
+            }
+            const u2 z = *reinterpret_cast<const u2*>(meta + kMeta * blkn + 64 + 2 * t16);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) sc[p * RT + t][g][n] = f4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < NS / NH; ++j) {
+              const u4 d = code_pairs(kw[j], z[0], z[1], magic);
+#pragma unroll
+              for (int t = 0; t < RT; ++t)
+                sc[p * RT + t][g][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                    __builtin_bit_cast(h8, d), qf[p * RT + t][NS / NH * n + j], sc[p * RT + t][g][n], 0, 0, 0);
+            }
+          }
+      __builtin_amdgcn_sched_barrier(0);
+      load_k(tile, next);
+      tile.ok = next_ok;
+      // scores times their token's scale
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int p = 0; p < HP; ++p)
+#pragma unroll
+          for (int n = 0; n < NH; ++n) {
+            const f4 ks = *reinterpret_cast<const f4*>(meta + kMeta * (D == 64 ? p / 2 : p + n) + 16 * g + 4 * c);
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                f4& v = sc[p * RT + t][g][0];
+                v[i] = n == 0 ? v[i] * ks[i] : __builtin_fmaf(sc[p * RT + t][g][n][i], ks[i], v[i]);
+              }
+          }
+      // heads in turn: softmax of their row tiles, then O^T += V^T P^T
+#pragma unroll
+      for (int p = 0; p < HP; ++p) {
+        f4 vs[NH][2];
+#pragma unroll
+        for (int n = 0; n < NH; ++n)
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            vs[n][g] = *reinterpret_cast<const f4*>(meta + kMeta * (D == 64 ? p / 2 : p + n) + 32 + 16 * g + 4 * c);
+        h8 pf[RT][NH];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          const int x = p * RT + t;
+          float s8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s8[i] = sc[x][i / 4][0][i % 4];
+          if (masked) {
+            const int seen = P32 && !ok ? 0 : lim[t] - tk;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int tok = 16 * (i / 4) + 4 * c + i % 4;
+              if (tok >= seen || (!P32 && (gone >> tok & 1))) s8[i] = kNegInf;
+            }
+          }
+          float mx = s8[0];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s8[i]);
+          mx = __builtin_fmaf(max_over_rows16(mx), f[x], v_exp[D == 64 ? p / 2 : p / NH]);
+          if (__ballot(mx > m[x] + kLag)) {
+            const float mn = fmaxf(m[x], mx);
+            const float al = m[x] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[x] - mn);
+            m[x] = mn;
+            l[x] *= al;
+#pragma unroll
+            for (int e = 0; e < NE; ++e) acc[x][e] *= al;
+          }
+          const float ms = m[x] == kNegInf ? 0.0f : m[x];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s8[i], f[x], -ms));
+            l[x] += w;
+#pragma unroll
+            for (int n = 0; n < NH; ++n) pf[t][n][i] = (_Float16)(w * vs[n][i / 4][i % 4]);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+          // 1024 + z and 64 + z of the token pairs
+          const float* mn = meta + kMeta * (D == 64 ? p / 2 : p + n) + 128;
+          uint32_t z10[4], z6[4];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const u2 w10 = *reinterpret_cast<const u2*>(mn + 8 * g + 2 * c);
+            const u2 w6 = *reinterpret_cast<const u2*>(mn + 16 + 8 * g + 2 * c);
+            z10[2 * g] = w10[0], z10[2 * g + 1] = w10[1], z6[2 * g] = w6[0], z6[2 * g + 1] = w6[1];
+          }
+#pragma unroll
+          for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
+            u4 d[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // even (odd) channels of two tokens
+              const u4 y = code_pairs(__builtin_amdgcn_perm(tile.v[2 * i + 1][p + n], tile.v[2 * i][p + n],
+                                                            half ? 0x07060302u : 0x05040100u),
+                                      z10[i], z6[i], magic);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) d[e][i] = y[e];
+            }
+            // MFMA e of a block: channel 8 m + e of row m (D = 64: channel
+            // 8 (m / 2) + m % 2 + 2 e)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int t = 0; t < RT; ++t) {
+                const int e = D == 64 ? k : 8 * n + 2 * k + half;
+                acc[p * RT + t][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, d[k]), pf[t][n],
+                                                                           acc[p * RT + t][e], 0, 0, 0);
+              }
+          }
+        }
+      }
+    };
+
+    if (tk < t_end) {
+      do {
+        // past the end the next tile repeats real rows and is not used
+        bool ok;
+        row = rows_of(min(tk + kStep, (t_end - 1) & ~31), pg, &ok);
+        pg = page_entry(tk + 2 * kStep);
+        compute(row, ok);
+        load_v(tile, row);
+        tk += kStep;
+      } while (tk < t_end);
+    }
+
+    // The waves join through LDS: the largest reference point, every wave's sums
+    // scaled to it, added in wave order.  Slab: the 16 rows of one row tile and
+    // block, [row][channel] per wave, over what the waves walked with (they meet
+    // before it is written).  A unit that is split leaves its sums, reference
+    // points and sums of weights in the workspace: two slots a workgroup, of its
+    // first and of its last unit.
+    constexpr int DB = D < 128 ? D : 128;
+    float* stats = static_cast<float*>(a.workspace);
+    float* part = stats + (int64_t)4 * gridDim.x * HP * urows;
+    int tid = threadIdx.x;  // indices made here, not kept in registers through the walk
+    asm volatile("" : "+v"(tid));
+    const int re = tid & 15, ce = (tid & 63) >> 4;
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      if (x) __syncthreads();
+      const float lt = sum_over_rows16(l[x]);
+      if (ce == 0) {
+        stat[wave * 32 + re] = m[x];
+        stat[wave * 32 + 16 + re] = lt;
+      }
+      __syncthreads();
+      float M = kNegInf;
+#pragma unroll
+      for (int g = 0; g < kWaves; ++g) M = fmaxf(M, stat[g * 32 + re]);
+      // a wave whose sum is 0 saw nothing (a NaN sum stays one)
+      const float k = lt == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[x] - M);
+#pragma unroll
+      for (int n = 0; n < NH; ++n) {
+        if (n) __syncthreads();
+        float* mine = slab + wave * kSlab<D> + re * kSlabRow<D>;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int mrow = 4 * ce + i;
-          const int ch = D == 64 ? 8 * (mrow / 2) + mrow % 2 + 2 * e : 8 * mrow + e;
-          slab[wave * 16 * DB + re * DB + ch] = acc[t][NEB * n + e][i] * k;
+          if constexpr (D == 64) {
+            // rows 2 j, 2 j + 1 of the product are the even and odd channels of eight
+            if (i % 2 == 0) {
+              float* at8 = mine + 8 * (2 * ce + i / 2);
+              *reinterpret_cast<f4*>(at8) = f4{acc[x][0][i], acc[x][0][i + 1], acc[x][1][i], acc[x][1][i + 1]} * k;
+              *reinterpret_cast<f4*>(at8 + 4) = f4{acc[x][2][i], acc[x][2][i + 1], acc[x][3][i], acc[x][3][i + 1]} * k;
+            }
+          } else {
+            float* at8 = mine + 8 * (4 * ce + i);
+            const int e = 8 * n;
+            *reinterpret_cast<f4*>(at8) = f4{acc[x][e][i], acc[x][e + 1][i], acc[x][e + 2][i], acc[x][e + 3][i]} * k;
+            *reinterpret_cast<f4*>(at8 + 4) = f4{acc[x][e + 4][i], acc[x][e + 5][i], acc[x][e + 6][i], acc[x][e + 7][i]} * k;
+          }
         }
-      __syncthreads();
-      // a thread: two channels of one row and head
-      constexpr uint32_t per_head = 16 * DB / 2;
-      for (uint32_t x = tid; x < HW * per_head; x += 64 * W) {
-        const int hx = x / per_head, rr = x % per_head / (DB / 2), ch = 2 * (x % (DB / 2));
-        const uint32_t row = row0 + 16 * t + rr;
-        if ((int)row > row1) continue;
-        float o0 = 0.0f, o1 = 0.0f, Mr = kNegInf, L = 0.0f;
-        for (int g = 0; g < TW; ++g) Mr = fmaxf(Mr, stat[(hx + HW * g) * 32 + rr]);
-        for (int g = 0; g < TW; ++g) {
-          const int wv = hx + HW * g;
-          const float lw = stat[wv * 32 + 16 + rr];
-          if (lw == 0.0f) continue;
-          o0 += slab[wv * 16 * DB + rr * DB + ch];
-          o1 += slab[wv * 16 * DB + rr * DB + ch + 1];
-          L += lw * __builtin_amdgcn_exp2f(stat[wv * 32 + rr] - Mr);
-        }
-        const uint32_t qi = row / (uint32_t)G;
-        const int64_t orow = (int64_t)(q0 + qi) * a.Hq + (hg * HW + hx) * G + (row - qi * G);
-        if (u.n == 1) {
-          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-          store_pair(a, orow * D + 128 * n + ch, o0 * inv, o1 * inv);
-          if (a.lse && ch == 0 && n == 0) a.lse[orow] = lse_of(Mr, L);
-        } else {
-          const int64_t slot = ((int64_t)blockIdx.x * HW + hx) * urows + (row - row0);
-          store_agent(part + slot * D + 128 * n + ch, o0, o1);
-          if (ch == 0 && n == 0) store_agent(stats + 2 * slot, Mr, L);
+        __syncthreads();
+        // a thread: two channels of one row
+        for (uint32_t y = tid; y < 16 * DB / 2; y += 64 * kWaves) {
+          const int rr = y / (DB / 2), ch = 2 * (y % (DB / 2));
+          const uint32_t qrow = row0 + 16 * (x % RT) + rr;
+          if ((int)qrow > row1) continue;
+          float o0 = 0.0f, o1 = 0.0f, Mr = kNegInf, L = 0.0f;
+#pragma unroll
+          for (int g = 0; g < kWaves; ++g) Mr = fmaxf(Mr, stat[g * 32 + rr]);
+#pragma unroll
+          for (int g = 0; g < kWaves; ++g) {
+            const float lw = stat[g * 32 + 16 + rr];
+            const float2 v = *reinterpret_cast<const float2*>(slab + g * kSlab<D> + rr * kSlabRow<D> + ch);
+            o0 += v.x;
+            o1 += v.y;
+            L += lw == 0.0f ? 0.0f : lw * __builtin_amdgcn_exp2f(stat[g * 32 + rr] - Mr);
+          }
+          const uint32_t qi = qrow / (uint32_t)G;
+          if (whole) {
+            const int64_t orow = (int64_t)(q0 + qi) * a.Hq + (hg * HP + x / RT) * G + (qrow - qi * G);
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            store_pair(a, orow * D + 128 * n + ch, o0 * inv, o1 * inv);
+            if (a.lse && ch == 0 && n == 0) a.lse[orow] = lse_of(Mr, L);
+          } else {
+            const int64_t slot = ((int64_t)(2 * wg + (seg > 0)) * HP + x / RT) * urows + (qrow - row0);
+            *reinterpret_cast<float2*>(part + slot * D + 128 * n + ch) = make_float2(o0, o1);
+            if (ch == 0 && n == 0) *reinterpret_cast<float2*>(stats + 2 * slot) = make_float2(Mr, L);
+          }
         }
       }
     }
+    __syncthreads();  // the next unit's walk is over this one's LDS
   }
-  if (u.n == 1) return;
+}
 
-  // The last workgroup of a unit to arrive joins its pieces, in order: a wave a
-  // row, D / 64 channels a lane, whose loads do not wait for one another.
-  unsigned* counter = static_cast<unsigned*>(a.workspace) + u.first;
-  if (!split_arrive(counter, u.n)) return;
-  constexpr int C = D / 64;
-  const int vrows = row1 - row0 + 1, ln = tid & 63;
-  const int64_t hop = (int64_t)HG * HW * urows;  // from a piece's rows to the next one's
-  for (int x = wave; x < HW * vrows; x += W) {
-    const int hx = x / vrows, rr = x - hx * vrows;
-    const int64_t slot = ((int64_t)u.first * HW + hx) * urows + rr;
-    const float* st = stats + 2 * slot;
-    float M = kNegInf;
-    for (int k = ln; k < u.n; k += 64) M = fmaxf(M, load_agent(st + 2 * k * hop).x);
+// Joins the results of the units that several workgroups held, WPR waves a query
+// row (the pieces of a row in turn), four waves a workgroup.  It finds the
+// shares as they did.  D / 64 channels a lane, the loads of kBatch pieces in flight
+// together.
+template <int D, int HP, int RT, int WPR>
+__global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int urows, uint32_t wgs, int64_t nrows) {
+  constexpr int C = D / 64, kBatch = D == 256 ? 8 : 16;
+  __shared__ ShareLds shares;
+  __shared__ float red[4][2], sum[4][D];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, part_of = wave % WPR;
+  const int HG = a.Hkv / HP, G = a.Hq / a.Hkv;
+  const Shares sh = scan_shares(a, wgs, HG, 16 * RT, 32 * kWaves, lane, &shares);
+  uint32_t id = min((int64_t)blockIdx.x * (4 / WPR) + wave / WPR, nrows - 1);
+  const int hq = id % (uint32_t)a.Hq;
+  id /= (uint32_t)a.Hq;
+  const int b = id / (uint32_t)a.max_queries, qi = id - b * (uint32_t)a.max_queries;
+  int q0, n = 1, late = 0;
+  uint32_t w0 = 0;
+  const int kvh = hq / G, row = qi * G + hq % G, row0 = row / (16 * RT) * (16 * RT);
+  q0 = shares.q0[b];
+  if (qi < shares.nq[b]) {
+    const uint32_t steps = shares.steps[b];
+    const uint32_t u0 = shares.before[b] + (uint32_t)(row0 / (16 * RT) * HG + kvh / HP) * steps;
+    w0 = share_of(sh, u0);
+    n = (int)(share_of(sh, u0 + steps - 1) - w0) + 1;
+    late = share_start(sh, w0) < u0;  // for w0 it was the last unit, for the others the first
+  }
+  // n == 1: one workgroup had all of the unit (or there is no such query)
+  const float* stats = static_cast<const float*>(a.workspace);
+  const float* part = stats + (int64_t)4 * wgs * HP * urows;
+  auto slot = [&](int k) -> int64_t {
+    return ((int64_t)(2 * (w0 + k) + (k == 0 ? late : 0)) * HP + kvh % HP) * urows + (row - row0);
+  };
+  float M = kNegInf, o[C], L = 0.0f;
+#pragma unroll
+  for (int i = 0; i < C; ++i) o[i] = 0.0f;
+  if (n > 1) {
+    for (int k = lane; k < n; k += 64) M = fmaxf(M, stats[2 * slot(k)]);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) M = fmaxf(M, __shfl_xor(M, d));
-    float o[C], L = 0.0f;
+    for (int k0 = part_of; k0 < n; k0 += WPR * kBatch) {
+      float2 ml[kBatch];
+      float v[kBatch][C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = 0.0f;
-    constexpr int U = D == 256 ? 8 : 16;  // pieces whose loads are in flight together
-    for (int k0 = 0; k0 < u.n; k0 += U) {
-      float2 ml[U], v[U][(C + 1) / 2];
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t sl = slot(min(k0 + WPR * j, n - 1));  // past the end: the last again, not added
+        ml[j] = *reinterpret_cast<const float2*>(stats + 2 * sl);
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int64_t at = slot + min(k0 + j, u.n - 1) * hop;  // past the end: the last again, not added
-        ml[j] = load_agent(stats + 2 * at);
-        const float* p = part + at * D + ln * C;
-        if constexpr (C == 1) {
-          v[j][0] = make_float2(split_load(p), 0.0f);
-        } else {
-#pragma unroll
-          for (int i = 0; i < C / 2; ++i) v[j][i] = load_agent(p + 2 * i);
-        }
+        for (int i = 0; i < C; ++i) v[j][i] = part[sl * D + lane * C + i];
       }
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
+      for (int j = 0; j < kBatch; ++j) {
         // 0: the piece saw nothing, or is past the end
-        const float w = ml[j].y == 0.0f || k0 + j >= u.n ? 0.0f : __builtin_amdgcn_exp2f(ml[j].x - M);
+        const float w = ml[j].y == 0.0f || k0 + WPR * j >= n ? 0.0f : __builtin_amdgcn_exp2f(ml[j].x - M);
         L += ml[j].y * w;
 #pragma unroll
-        for (int i = 0; i < C; ++i) o[i] += (i % 2 ? v[j][i / 2].y : v[j][i / 2].x) * w;
+        for (int i = 0; i < C; ++i) o[i] += v[j][i] * w;
       }
     }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    const uint32_t row = row0 + rr, qi = row / (uint32_t)G;
-    const int64_t orow = (int64_t)(q0 + qi) * a.Hq + (hg * HW + hx) * G + (row - qi * G);
-    if constexpr (C == 1) {
-      a.out[orow * D + ln] = a.dtype == 1 ? f32_to_bf16_bits(o[0] * inv) : f32_to_f16_bits(o[0] * inv);
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; i += 2) store_pair(a, orow * D + ln * C + i, o[i] * inv, o[i + 1] * inv);
-    }
-    if (a.lse && ln == 0) a.lse[orow] = lse_of(M, L);
   }
+  if constexpr (WPR > 1) {
+    if (lane == 0) red[wave][0] = L;
+#pragma unroll
+    for (int i = 0; i < C; ++i) sum[wave][lane * C + i] = o[i];
+    __syncthreads();
+    if (part_of != 0 || n == 1) return;
+    L = red[0][0] + red[1][0] + red[2][0] + red[3][0];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int ch = lane * C + i;
+      o[i] = sum[0][ch] + sum[1][ch] + sum[2][ch] + sum[3][ch];
+    }
+  }
+  if (n == 1 || (int64_t)blockIdx.x * (4 / WPR) + wave / WPR >= nrows) return;
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const int64_t orow = (int64_t)(q0 + qi) * a.Hq + hq;
+  if constexpr (C == 1) {
+    a.out[orow * D + lane] = a.dtype == 1 ? f32_to_bf16_bits(o[0] * inv) : f32_to_f16_bits(o[0] * inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; i += 2) store_pair(a, orow * D + lane * C + i, o[i] * inv, o[i + 1] * inv);
+  }
+  if (a.lse && lane == 0) a.lse[orow] = lse_of(M, L);
 }
 
-// Arrival counters of the units that are cut.
-__global__ __launch_bounds__(256) void kv_attn_clear_kernel(unsigned* counters) {
-  for (int i = threadIdx.x; i < kCounters; i += 256) counters[i] = 0;
-}
-
-template <int D>
-size_t lds_bytes(int W) {
-  constexpr int DB = D < 128 ? D : 128;
-  return (size_t)W * ((kWave<D> > 16 * DB ? kWave<D> : 16 * DB) + 32) * 4;
-}
-
-template <int D, int RT, int W, bool P32>
+template <int D, int HP, int RT, bool P32>
 hipError_t launch_main(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream) {
   static std::atomic<uint64_t> raised{0};
-  const size_t lds = lds_bytes<D>(W);
-  hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&kv_attn_kernel<D, RT, W, P32>), lds, raised);
+  constexpr size_t lds = lds_words<D, HP> * 4;
+  const hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&kv_attn_kernel<D, HP, RT, P32>), lds, raised);
   if (e != hipSuccess) return e;
-  if (p.share) kv_attn_clear_kernel<<<1, 256, 0, stream>>>(static_cast<unsigned*>(a.workspace));
-  kv_attn_kernel<D, RT, W, P32><<<(unsigned)p.grid, 64 * W, lds, stream>>>(a, p.HW, p.rtiles, p.urows, p.share);
+  kv_attn_kernel<D, HP, RT, P32><<<(unsigned)p.grid, 64 * kWaves, lds, stream>>>(a, p.rtiles, p.urows, p.flat);
+  if (!p.flat) return hipGetLastError();
+  const int64_t rows = (int64_t)a.B * a.max_queries * a.Hq, units = (int64_t)a.B * (a.Hkv / HP) * p.rtiles;
+  // many pieces to a row: four waves share them
+  if (p.grid > 8 * units)
+    kv_attn_join_kernel<D, HP, RT, 4><<<(unsigned)rows, 256, 0, stream>>>(a, p.urows, (uint32_t)p.grid, rows);
+  else
+    kv_attn_join_kernel<D, HP, RT, 1><<<(unsigned)((rows + 3) / 4), 256, 0, stream>>>(a, p.urows, (uint32_t)p.grid, rows);
   return hipGetLastError();
 }
 
-template <int D, int RT, int W>
+template <int D, int HP, int RT>
 hipError_t launch_p(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream) {
-  return a.page % 32 == 0 ? launch_main<D, RT, W, true>(a, p, stream) : launch_main<D, RT, W, false>(a, p, stream);
-}
-
-template <int D>
-hipError_t launch_rt(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream) {
-  return p.RT == 1 ? launch_p<D, 1, 8>(a, p, stream) : launch_p<D, 2, 8>(a, p, stream);
+  return a.page % 32 == 0 ? launch_main<D, HP, RT, true>(a, p, stream) : launch_main<D, HP, RT, false>(a, p, stream);
 }
 
 }  // namespace
 
-size_t kv_attn_workspace_bytes(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context,
-                               int64_t max_queries) {
-  const KvPlan p = plan_kv(T, B, Hq, Hkv, D, page, max_context, max_queries);
-  return p.share ? (size_t)kCounters * 4 + (size_t)p.grid * p.HW * p.urows * (D + 2) * 4 : 0;
+size_t kv_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_queries) {
+  const KvPlan p = plan_kv(B, Hq, Hkv, D, max_context, max_queries);
+  return p.flat ? (size_t)2 * p.grid * p.HP * p.urows * (D + 2) * 4 : 0;
 }
 
-int describe_kv_attn(int64_t T, int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries,
-                     char* buf, size_t len) {
-  const KvPlan p = plan_kv(T, B, Hq, Hkv, D, page, max_context, max_queries);
-  return snprintf(buf, len, "kv_attn_kernel<D=%d, RT=%d, W=%d, P32=%d> grid=%lld block=%d heads=%d %s", D, p.RT, p.W,
-                  page % 32 == 0 ? 1 : 0, (long long)p.grid, 64 * p.W, p.HW, p.share ? "pieces" : "whole units");
+int describe_kv_attn(int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries, char* buf,
+                     size_t len) {
+  const KvPlan p = plan_kv(B, Hq, Hkv, D, max_context, max_queries);
+  return snprintf(buf, len, "kv_attn_kernel<D=%d, HP=%d, RT=%d, P32=%d> grid=%lld block=%d %s", D, p.HP, p.RT,
+                  page % 32 == 0 ? 1 : 0, (long long)p.grid, 64 * kWaves, p.flat ? "shares" : "whole units");
 }
 
 hipError_t launch_kv_attn(const KvAttnArgs& a, hipStream_t stream) {
-  const KvPlan p = plan_kv(a.T, a.B, a.Hq, a.Hkv, a.D, a.page, a.max_context, a.max_queries);
-  if (a.D == 64) return launch_rt<64>(a, p, stream);
-  if (a.D == 128) return launch_rt<128>(a, p, stream);
-  return launch_rt<256>(a, p, stream);
+  const KvPlan p = plan_kv(a.B, a.Hq, a.Hkv, a.D, a.max_context, a.max_queries);
+  if (a.D == 256) return launch_p<256, 1, 1>(a, p, stream);
+  if (a.D == 128) {
+    if (p.RT == 2) return launch_p<128, 1, 2>(a, p, stream);
+    return p.HP == 2 ? launch_p<128, 2, 1>(a, p, stream) : launch_p<128, 1, 1>(a, p, stream);
+  }
+  return p.RT == 2 ? launch_p<64, 2, 2>(a, p, stream) : launch_p<64, 2, 1>(a, p, stream);
 }
 
 }  // namespace wq
