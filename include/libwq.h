@@ -517,9 +517,9 @@ int wq_kv_dequant(const uint8_t* codes, const uint16_t* s_f16, const uint8_t* zp
  * query heads and Hkv key / value heads of D values (D = 64, 128 or 256), Hq a
  * multiple of Hkv; query head h reads KV head h / (Hq / Hkv).  Query, key and
  * value tensors are [T][heads][D] with the heads and values of a token
- * contiguous and a stride (in values, at least heads * D, a multiple of 8)
- * from token to token, so slices of one fused projection can be passed; they are 16-byte
- * aligned.  T == 0 (or B == 0) enqueues nothing.  Errors: WQ_EINVAL for a NULL
+ * contiguous and a stride (in values, at least heads * D, below 2^23, a
+ * multiple of 8) from token to token, so slices of one fused projection can be
+ * passed; they are 16-byte aligned.  T == 0 (or B == 0) enqueues nothing.  Errors: WQ_EINVAL for a NULL
  * pointer, a bad size, dtype, scale or eps; WQ_EUNSUPPORTED for a head size, head
  * count, rotation or page size outside the above and below; WQ_EALIGN for
  * misaligned pointers or strides.  All three are deterministic and can be

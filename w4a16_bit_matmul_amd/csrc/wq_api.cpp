@@ -562,7 +562,7 @@ int check_heads(int dtype, int64_t T, int Hq, int Hkv, int D) {
 }
 
 int check_rows(const void* p, int64_t stride, int64_t heads, int D) {
-  if (stride < heads * D || stride > (int64_t(1) << 40)) return WQ_EINVAL;
+  if (stride < heads * D || stride >= (int64_t(1) << 23)) return WQ_EINVAL;
   return !aligned(p, 16) || stride % 8 != 0 ? WQ_EALIGN : WQ_OK;
 }
 

@@ -55,7 +55,7 @@ constexpr float kNegInf = -__builtin_inff();
 constexpr float kLag = 8.0f;
 constexpr int kShares = 512;     // workgroups that steps are shared out to
 constexpr int kMaxShared = 256;  // sequences that a wave scans for its share
-constexpr int kMinSteps = 4;     // steps of a share, so that joining stays cheap
+constexpr int kMinSteps = 2;     // steps of a share, so that joining stays cheap
 constexpr int kMeta = 160;       // words of a wave's scales and zero-points of a tile and block
 
 constexpr int kWaves = 4;
@@ -265,11 +265,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
   ShareLds* shares = reinterpret_cast<ShareLds*>(lds + kWaves * (kPerWave<D, HP> + 32));
   const Magic magic;
 
-  // Workgroups go round the eight chiplets in turn; consecutive numbers here lie
-  // on one, so that the heads of a sequence share its L2 (their scales lie in the
-  // same lines).
-  const uint32_t xcd = blockIdx.x % 8;
-  const uint32_t wg = xcd * (gridDim.x / 8) + min(xcd, gridDim.x % 8) + blockIdx.x / 8;
+  const uint32_t wg = blockIdx.x;
 
   // this workgroup's steps, counted over all units
   uint32_t at = 0, at_end = 1;
@@ -758,9 +754,6 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int uro
 #pragma unroll
   for (int i = 0; i < C; ++i) o[i] = 0.0f;
   if (n > 1) {
-    for (int k = lane; k < n; k += 64) M = fmaxf(M, stats[2 * slot(k)]);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) M = fmaxf(M, __shfl_xor(M, d));
     for (int k0 = part_of; k0 < n; k0 += WPR * kBatch) {
       float2 ml[kBatch];
       float v[kBatch][C];
@@ -771,6 +764,14 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int uro
 #pragma unroll
         for (int i = 0; i < C; ++i) v[j][i] = part[sl * D + lane * C + i];
       }
+      float top = M;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) top = fmaxf(top, ml[j].x);
+      const float al = L == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(M - top);
+      M = top;
+      L *= al;
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] *= al;
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         // 0: the piece saw nothing, or is past the end
@@ -782,16 +783,24 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int uro
     }
   }
   if constexpr (WPR > 1) {
-    if (lane == 0) red[wave][0] = L;
+    if (lane == 0) {
+      red[wave][0] = M;
+      red[wave][1] = L;
+    }
 #pragma unroll
     for (int i = 0; i < C; ++i) sum[wave][lane * C + i] = o[i];
     __syncthreads();
     if (part_of != 0 || n == 1) return;
-    L = red[0][0] + red[1][0] + red[2][0] + red[3][0];
+    M = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
+    L = 0.0f;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int ch = lane * C + i;
-      o[i] = sum[0][ch] + sum[1][ch] + sum[2][ch] + sum[3][ch];
+    for (int i = 0; i < C; ++i) o[i] = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float w = red[g][1] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(red[g][0] - M);
+      L += red[g][1] * w;
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] += sum[g][lane * C + i] * w;
     }
   }
   if (n == 1 || (int64_t)blockIdx.x * (4 / WPR) + wave / WPR >= nrows) return;

@@ -118,7 +118,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* starts, int B, int64
 }
 
 template <int D, bool BF>
-__global__ __launch_bounds__(256, 2) void prompt_attn_kernel(PromptAttnArgs a, int64_t slots) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_attn_kernel(PromptAttnArgs a, int64_t slots) {
   constexpr int KT = D == 256 ? 32 : 64;    // keys of a tile
   constexpr int TB = KT / 32;               // 32-key MFMA blocks
   constexpr int NC = D / 8;                 // 16-byte chunks of a row
@@ -140,7 +140,8 @@ __global__ __launch_bounds__(256, 2) void prompt_attn_kernel(PromptAttnArgs a, i
   const int64_t row = min(Rw + r, n * G - 1);               // past the end: the last row again, not stored
   const int64_t qi = row / G;                               // the row's token; it sees keys 0..qi
   const int64_t head = (int64_t)kvh * G + row % G;
-  const int64_t first = min(Rw, n * G - 1) / G;             // fewest and most keys of the wave's rows
+  const int qi32 = (int)qi;
+  const int first = (int)(min(Rw, n * G - 1) / G);          // fewest keys of the wave's rows, less one
   const int64_t last = min(R0 + kRows, n * G) - 1;
   const int tiles = (int)((last / G) / KT) + 1;
 
@@ -162,20 +163,36 @@ __global__ __launch_bounds__(256, 2) void prompt_attn_kernel(PromptAttnArgs a, i
 
   const uint16_t* kp = a.k + q0 * a.k_stride + (int64_t)kvh * D;
   const uint16_t* vp = a.v + q0 * a.v_stride + (int64_t)kvh * D;
-  const int64_t wg_first = R0 / G;  // every row of the workgroup sees keys 0..wg_first
+  const int wg_first = (int)(R0 / G);  // every row of the workgroup sees keys 0..wg_first
+  const int keys = (int)n;
+  // the thread's 16 bytes of a tile's load x: token t0 + x (256 / NC), chunk j0, as
+  // 32-bit offsets from the tile's first key (strides are below 2^23 values)
+  const int t0 = threadIdx.x / NC, j0 = threadIdx.x % NC;
+  const uint32_t ks = (uint32_t)a.k_stride, vs = (uint32_t)a.v_stride;
+  uint32_t k_at = (t0 * ks + 8 * j0) * 2, v_at = (t0 * vs + 8 * j0) * 2;
   u4 kreg[LD], vreg[LD];
   uint32_t odd = 0;
   auto fetch = [&](int kt) {
+    const int key0 = kt * KT;
+    const char* kb = reinterpret_cast<const char*>(kp + (int64_t)key0 * a.k_stride);
+    const char* vb = reinterpret_cast<const char*>(vp + (int64_t)key0 * a.v_stride);
+    if (key0 + KT <= keys) {
 #pragma unroll
-    for (int x = 0; x < LD; ++x) {
-      const int p = x * 256 + threadIdx.x, t = p / NC, j = p % NC;
-      const int64_t tok = min((int64_t)kt * KT + t, n - 1);  // past the sequence: its last key again
-      kreg[x] = *reinterpret_cast<const u4*>(kp + tok * a.k_stride + 8 * j);
-      vreg[x] = *reinterpret_cast<const u4*>(vp + tok * a.v_stride + 8 * j);
+      for (int x = 0; x < LD; ++x) {
+        kreg[x] = *reinterpret_cast<const u4*>(kb + x * (512 / NC) * (int64_t)ks + k_at);
+        vreg[x] = *reinterpret_cast<const u4*>(vb + x * (512 / NC) * (int64_t)vs + v_at);
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < LD; ++x) {
+        const uint32_t t = min(t0 + x * (256 / NC), keys - 1 - key0);  // past the sequence: its last key again
+        kreg[x] = *reinterpret_cast<const u4*>(kb + (t * ks + 8 * j0) * 2);
+        vreg[x] = *reinterpret_cast<const u4*>(vb + (t * vs + 8 * j0) * 2);
+      }
     }
   };
   auto stage = [&](int kt, int buf) {
-    if ((int64_t)kt * KT + KT - 1 > wg_first) {
+    if (kt * KT + KT - 1 > wg_first) {
 #pragma unroll
       for (int x = 0; x < LD; ++x)
 #pragma unroll
@@ -212,20 +229,21 @@ __global__ __launch_bounds__(256, 2) void prompt_attn_kernel(PromptAttnArgs a, i
     const u2* vd = reinterpret_cast<const u2*>(kd + KT * NC);
     f16v s[TB];
 #pragma unroll
-    for (int tb = 0; tb < TB; ++tb) {
+    for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[tb][i] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NS; ++j) s[tb] = mfma32<BF>(kd[32 * tb * NC + kat[j]], qf[j], s[tb]);
-    }
-    const int64_t key0 = (int64_t)kt * KT;
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) s[tb] = mfma32<BF>(kd[32 * tb * NC + kat[j]], qf[j], s[tb]);
+    const int key0 = kt * KT;
     if (key0 + KT - 1 > first) {
-      const int seen = (int)min(qi - key0, (int64_t)KT);  // the row sees the tile's keys 0..seen
+      const int seen = qi32 - key0 - 4 * hf;  // the row sees the tile's keys 0..seen + 4 hf
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (32 * tb + 8 * (i / 4) + 4 * hf + i % 4 > seen) s[tb][i] = kNegInf;
+          if (32 * tb + 8 * (i / 4) + i % 4 > seen) s[tb][i] = kNegInf;
     }
     float mx = kNegInf;
 #pragma unroll
@@ -297,7 +315,7 @@ __global__ __launch_bounds__(256, 2) void prompt_attn_kernel(PromptAttnArgs a, i
   // key by key, to the stored rows that see the key
   if (__syncthreads_or(odd != 0) && threadIdx.x < D) {
     const int ch = threadIdx.x;
-    for (int64_t t = (wg_first + 1) / KT * KT; t <= last / G; ++t) {
+    for (int64_t t = (int64_t)(wg_first + 1) / KT * KT; t <= last / G; ++t) {
       const uint32_t v = vp[t * a.v_stride + ch];
       if (finite_halves<BF>(v) == 0xffffffffu) continue;
       for (int64_t x = max(t * G, R0); x <= last; ++x) {
