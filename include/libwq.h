@@ -519,11 +519,14 @@ int wq_kv_dequant(const uint8_t* codes, const uint16_t* s_f16, const uint8_t* zp
  * value tensors are [T][heads][D] with the heads and values of a token
  * contiguous and a stride (in values, at least heads * D, below 2^23, a
  * multiple of 8) from token to token, so slices of one fused projection can be
- * passed; they are 16-byte aligned.  T == 0 (or B == 0) enqueues nothing.  Errors: WQ_EINVAL for a NULL
- * pointer, a bad size, dtype, scale or eps; WQ_EUNSUPPORTED for a head size, head
- * count, rotation or page size outside the above and below; WQ_EALIGN for
- * misaligned pointers or strides.  All three are deterministic and can be
- * captured into graphs. */
+ * passed; they are 16-byte aligned.  T == 0 (or B == 0) enqueues nothing.
+ * Limits: 65536 heads, 2^24 sequences, contexts of 2^30 tokens, and 2^24
+ * workgroups of a call (of 8192 values in the norm, of 128 rows of a KV head in
+ * the prompt attention, of 16 in the cache attention).  Errors: WQ_EINVAL for a
+ * NULL pointer, a bad size, dtype, stride, scale or eps; WQ_EUNSUPPORTED for a
+ * head size, head count, rotation or page size outside the above and below and
+ * for more workgroups; WQ_EALIGN for misaligned pointers or strides.  All three
+ * are deterministic and can be captured into graphs. */
 
 /* Norm of every query and key head and the rotation of its position, in one
  * pass: for a head row x of token t,

@@ -117,6 +117,30 @@ def test_cache_plans_and_their_workspace():
         assert need == (2 * grid * heads * min(rows, 16 * rt) * (D + 2) * 4 if shared else 0), d
 
 
+def test_shares_are_counted_in_32_bits():
+    """Steps of 128 tokens of all units together: past 2^31 each unit is a
+    workgroup again."""
+    below = wq.wq_kv_attention_plan(1, 508, 254, 128, 1, 4096, 2 ** 30, 1)  # 127 units of 2^23 steps
+    at = wq.wq_kv_attention_plan(1, 512, 512, 128, 1, 4096, 2 ** 30, 1)  # 256 units
+    assert "HP=2" in below and "grid=512" in below and below.endswith("shares")
+    assert "HP=2" in at and "grid=256" in at and at.endswith("whole units")
+    assert wq.wq_kv_attention_workspace_bytes(1, 512, 512, 128, 1, 4096, 2 ** 30) == 0
+
+
+def test_limits_of_the_cache_attention():
+    plan = lambda *a: wq.lib().wq_kv_attention_plan(*a, ctypes.create_string_buffer(160), 160)
+    assert plan(1, 8, 2, 128, 1, 16, 2 ** 30, 1) == wq.WQ_OK and plan(1, 8, 2, 128, 1, 16, 2 ** 30 + 1, 1) == EINVAL
+    assert plan(2 ** 24 + 1, 8, 2, 128, 2 ** 24 + 1, 16, 64, 1) == EINVAL
+    # a grid holds 2^24 workgroups less one
+    assert plan(2 ** 23 - 1, 8, 2, 128, 2 ** 23 - 1, 16, 64, 1) == wq.WQ_OK and plan(2 ** 23, 8, 2, 128, 2 ** 23, 16, 64, 1) == EUNSUP
+    assert cache(T=2 ** 23, nseq=2 ** 23) == EUNSUP
+    assert plan(2 ** 31 - 1, 65536, 1, 128, 2 ** 24, 16, 64, 2 ** 31 - 1) == EUNSUP
+    assert prompt(T=2 ** 28, Hq=8, Hkv=8, qs=1024, ks=1024, vs=1024) == prompt(nseq=2 ** 23) == EUNSUP
+    assert rope(T=2 ** 28) == rope(T=2 ** 26, Hq=64, Hkv=8, qs=8192, ks=1024, qos=8192, kos=1024) == EUNSUP
+    # strides (in values) from 2^23 on
+    assert prompt(ks=2 ** 23) == prompt(qs=2 ** 23) == cache(qs=2 ** 23) == rope(kos=2 ** 23) == EINVAL
+
+
 def test_binding_rejects_before_any_call():
     x = torch.zeros((2, 4, 128), dtype=torch.float16)
     i = torch.zeros(3, dtype=torch.int32)

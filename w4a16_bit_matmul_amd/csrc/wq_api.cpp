@@ -552,6 +552,7 @@ int wq_gemm_nvfp4_plan(int64_t M, int64_t N, int64_t K, int path, char* buf, siz
 namespace {
 
 constexpr int64_t kMaxCount = int64_t(1) << 31;  // tokens, rows, table entries
+constexpr int64_t kMaxGrid = int64_t(1) << 24;   // workgroups of 256 threads: a grid holds less than 2^32 threads
 
 // Types, head counts and sizes the three operators share.
 int check_heads(int dtype, int64_t T, int Hq, int Hkv, int D) {
@@ -576,8 +577,9 @@ int check_kv_attn(int dtype, int64_t T, int Hq, int Hkv, int D, int64_t B, int p
   if (B < 0 || B > (1 << 24) || max_context < 0 || max_context > (1 << 30) || max_queries < 0 || max_queries > T)
     return WQ_EINVAL;
   if (((int64_t)Hkv * D) % 128 != 0 || page_size < 1 || (page_size & (page_size - 1)) != 0) return WQ_EUNSUPPORTED;
-  // grids stay below 2^31 workgroups
-  if (max_queries > 0 && B * max_queries > kMaxCount / Hq) return WQ_EUNSUPPORTED;
+  // workgroups of 16 rows of a KV head at least
+  const int64_t groups = (max_queries * (Hq / Hkv) + 15) / 16;
+  if (groups >= kMaxGrid || groups * B >= kMaxGrid / Hkv) return WQ_EUNSUPPORTED;
   return WQ_OK;
 }
 
@@ -600,8 +602,8 @@ int wq_qk_norm_rope(const void* q, const void* k, int dtype, int64_t T, int Hq, 
   if (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(positions, 4) || !aligned(q_weight, 8) ||
       !aligned(k_weight, 8))
     return WQ_EALIGN;
-  // at most 2^31 workgroups of eight rows
-  if (T > (int64_t(1) << 34) / (Hq + Hkv)) return WQ_EUNSUPPORTED;
+  // workgroups of 8192 values, four rows a lane
+  if (T > (kMaxGrid - 1) * 8192 / D / (Hq + Hkv)) return WQ_EUNSUPPORTED;
   const wq::QkNormRopeArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), T, q_stride, k_stride,
                              Hq, Hkv, D, rot, interleaved, dtype, static_cast<const uint16_t*>(q_weight),
                              static_cast<const uint16_t*>(k_weight), eps, positions, cos, sin, P,
@@ -621,8 +623,8 @@ int wq_prompt_attention(const void* q, const void* k, const void* v, int dtype, 
       (st = check_rows(v, v_stride, Hkv, D)))
     return st;
   if (!aligned(out, 16) || !aligned(seq_starts, 4) || !aligned(lse, 4)) return WQ_EALIGN;
-  // at most 2^31 workgroups of 128 rows
-  if (T * (Hq / Hkv) / 128 + B >= kMaxCount / Hkv) return WQ_EUNSUPPORTED;
+  // workgroups of 128 rows
+  if (T * (Hq / Hkv) / 128 + B >= kMaxGrid / Hkv) return WQ_EUNSUPPORTED;
   const wq::PromptAttnArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
                              static_cast<const uint16_t*>(v), T, q_stride, k_stride, v_stride, dtype, Hq, Hkv, D,
                              (int)B, seq_starts, scale, static_cast<uint16_t*>(out), lse};

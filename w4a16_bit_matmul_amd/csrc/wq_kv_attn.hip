@@ -86,7 +86,8 @@ KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_q
   const int64_t units = (int64_t)B * (Hkv / p.HP) * p.rtiles;
   // two workgroups a CU
   const int64_t n = units * steps / kMinSteps < kShares ? units * steps / kMinSteps : kShares;
-  p.flat = units < 2 * kShares && n > units / 2 && steps >= 2 * kMinSteps && B <= kMaxShared;
+  p.flat = units < 2 * kShares && n > units / 2 && steps >= 2 * kMinSteps && B <= kMaxShared &&
+           units * steps < (int64_t)1 << 31;  // steps are counted in 32 bits
   p.grid = p.flat ? n : units;
   return p;
 }
