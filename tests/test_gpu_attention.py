@@ -337,6 +337,32 @@ def test_cache_attention_several_tokens(lens, nq, Hq, Hkv, D, page, dtype):
     _check_rows(got, lse, want)
 
 
+@pytest.mark.parametrize("B,most,Hq,Hkv,D,page", [(66, 125, 8, 8, 128, 16), (37, 12, 160, 16, 128, 64), (64, 250, 4, 4, 64, 1), (86, 33, 18, 6, 64, 32),
+                                                  (171, 101, 3, 3, 128, 4)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_cache_attention_many_rows(B, most, Hq, Hkv, D, page, dtype):
+    """Many sequences with up to `most` queries each (the kernel for many rows):
+    none or one among them, more queries than tokens, pages that are gone, page
+    numbers behind the cache, lengths past max_context."""
+    say(f"cache many rows B={B} most={most} Hq={Hq} Hkv={Hkv} D={D} page={page} {dtype}")
+    rng = np.random.default_rng(B + D)
+    nq = [0, 1, most, most] + [int(x) for x in rng.integers(0, most + 1, B - 4)]
+    lens = [5, 1, most // 2, 300] + [int(x) for x in rng.integers(0, 170, B - 4)]
+    starts = [int(x) for x in 1 + np.concatenate([[0], np.cumsum(nq)])]
+    S = (sum(-(-n // page) for n in lens) + 3) * page
+    cache = Cache(B + D, S, Hkv, D)
+    table = _tables(B, lens, page, S)
+    for b in range(5, B, 3):  # a page in the middle, or all of them
+        gone = [lens[b] // 2 // page] if b % 2 else list(range(table.shape[1]))
+        table[b, gone] = [-1, S // page, 2 ** 31 - 1, -2 ** 31][b % 4]
+    q = ref.values(Hq, (starts[-1] + 2, Hq, D), dtype)
+    cut = min(250, table.shape[1] * page)
+    assert "kv_chunk_kernel" in wq.wq_kv_attention_plan(q.shape[0], Hq, Hkv, D, B, page, cut, most)
+    want, used = _cache_want(cache, q, table, page, lens, starts, D ** -0.5, max_context=cut)
+    got, lse = _run_cache(cache.to_dev(used), q.cuda(), table, page, lens, starts, max_context=cut, max_queries=most)
+    _check_rows(got, lse, want)
+
+
 @pytest.mark.parametrize("page", [16, 64])
 def test_cache_attention_missing_pages_and_bounds(page):
     """Pages outside the cache (evicted ones) are not attended, a sequence whose
@@ -413,6 +439,20 @@ def test_cache_attention_nan_query_stays_in_its_row():
     keep = torch.ones((2, 8), dtype=torch.bool)
     keep[0, 3] = keep[1, 0] = False
     ref.check(got[keep], want[0][keep], want[1][keep], "other rows")
+
+
+@pytest.mark.parametrize("nq,scale", [(3, 1e-20), (150, 1e-38), (3, 0.1)])
+def test_cache_attention_zero_queries_with_small_scales(nq, scale):
+    """Queries of zeros, whatever the scale: the mean of what they see."""
+    lens, Hq, Hkv, D, page = [170, 200], 4, 1, 128, 16
+    cache = Cache(5, 32 * page, Hkv, D)
+    table = _tables(5, lens, page, 32 * page)
+    table[0, 2] = -1
+    q = ref.values(3, (2 * nq, Hq, D), HF)
+    q[::2] = 0
+    want, used = _cache_want(cache, q, table, page, lens, [0, nq, 2 * nq], float(np.float32(scale)))
+    got, lse = _run_cache(cache.to_dev(used), q.cuda(), table, page, lens, [0, nq, 2 * nq], scale=scale)
+    _check_rows(got, lse, want)
 
 
 def test_cache_attention_rows_past_2_31_bytes():

@@ -29,6 +29,7 @@ PER_FILE = {
     "wq_noalloc.hip": [],
     "wq_rope.hip": [],
     "wq_kv_attn.hip": [],
+    "wq_kv_chunk.hip": [],
     "wq_prompt_attn.hip": [],
     "wq_api.cpp": [],
 }

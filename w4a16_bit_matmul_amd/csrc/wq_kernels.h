@@ -122,6 +122,10 @@ size_t kv_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int64_t max_contex
 int describe_kv_attn(int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries, char* buf,
                      size_t len);
 hipError_t launch_kv_attn(const KvAttnArgs& a, hipStream_t stream);
+// Its kernel for many rows (wq_kv_chunk.hip): workgroups of kChunkWaves waves, 32
+// rows of a KV head each.
+constexpr int kChunkWaves = 4;
+hipError_t launch_kv_chunk(const KvAttnArgs& a, int64_t grid, int rtiles, hipStream_t stream);
 
 // Causal attention over packed prompts (wq_prompt_attn.hip).
 struct PromptAttnArgs {

@@ -24,13 +24,14 @@
 // eight scores and two lane swaps, rescaling needs no exchange, and a lane's
 // scores of tokens {4c..4c+3, 16+4c..16+4c+3} of a 32-token tile are, in order,
 // its operand of the second product.  For V that product needs eight tokens of
-// one channel in a lane while a cache word holds eight channels of one token:
-// a lane reads the same word of its eight tokens, and since the even channels of
-// a word lie in its low half and the odd ones in its high half, one v_perm per
-// pair of tokens turns them into words of one channel's token pairs.
+// one channel in a lane while a cache word holds eight channels of one token, the
+// even ones in its low half and the odd ones in its high half: ds_read_b64_tr_b16
+// transposes half words as it reads them from LDS, so a lane gets words of the
+// same four channels of two tokens each.
 //
 // Reading is the bound: 2 (D/2 + 2.5 D/128) bytes a token and KV head.  A wave
-// walks 32-token tiles, the next tile's codes in flight while it computes.  It takes as many
+// walks 32-token tiles: codes come as whole rows, 16 bytes a lane, pass through
+// LDS, and the next tile's are in flight while it computes.  It takes as many
 // neighbouring KV heads as fill a 128-byte line (two of 128 values): what a CU
 // can have in flight is bounded by the lines of its 32 KB cache, and half-used
 // lines halve it (one head a wave read 4.4 TB/s where two read 5.0).  The waves of
@@ -40,22 +41,14 @@
 // results which a second kernel joins.
 #include <stdio.h>
 
-#include "wq_device.h"
-#include "wq_kernels.h"
+#include "wq_attn.h"
 
 namespace wq {
 namespace {
 
-typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-
-constexpr float kNegInf = -__builtin_inff();
-// A row's reference point may lag its largest weight by this many powers of two
-// (fp16 weights stay below 2^9, the fp32 sums far below their limits), so that it
-// rarely moves.
-constexpr float kLag = 8.0f;
 constexpr int kShares = 512;     // workgroups that steps are shared out to
 constexpr int kMaxShared = 256;  // sequences that a wave scans for its share
-constexpr int kMinSteps = 2;     // steps of a share, so that joining stays cheap
+constexpr int kMinSteps = 4;     // steps of a unit that is worth sharing out
 constexpr int kMeta = 160;       // words of a wave's scales and zero-points of a tile and block
 
 constexpr int kWaves = 4;
@@ -65,6 +58,7 @@ struct KvPlan {
   int RT;        // 16-row tiles of a head
   int rtiles;    // units along the query rows of one KV head
   int urows;     // query rows of a unit and head that a call can use
+  bool chunk;    // many rows: the kernel of wq_kv_chunk.hip, RT its 16-row tiles
   bool flat;     // the steps of all units are shared out equally (else one unit a workgroup)
   int64_t grid;  // workgroups launched
 };
@@ -74,6 +68,16 @@ struct KvPlan {
 KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_queries) {
   KvPlan p;
   const int64_t G = Hq / Hkv, rows = max_queries * G;
+  p.HP = 1;
+  p.RT = 2 * kChunkWaves;
+  p.rtiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
+  p.urows = 16 * p.RT;
+  p.grid = (int64_t)B * Hkv * p.rtiles;
+  p.flat = false;
+  // tiles of 128 rows once two workgroups a CU come of it (one a CU: 510 us where
+  // the kernel of 32 rows takes 455) and nearly all of their rows are used
+  p.chunk = D != 256 && p.grid >= kShares && 5 * ((rows + 31) / 32) >= 16 * p.rtiles;
+  if (p.chunk) return p;
   // more than 16 rows: two tiles share the decoded codes (D = 256: no registers for them)
   p.RT = rows <= 16 || D == 256 ? 1 : 2;
   p.rtiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
@@ -85,23 +89,11 @@ KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_q
   if (D == 128 && p.RT == 1 && Hkv % 2 == 0 && (int64_t)B * (Hkv / 2) * p.rtiles * steps >= 2 * kShares) p.HP = 2;
   const int64_t units = (int64_t)B * (Hkv / p.HP) * p.rtiles;
   // two workgroups a CU
-  const int64_t n = units * steps / kMinSteps < kShares ? units * steps / kMinSteps : kShares;
-  p.flat = units < 2 * kShares && n > units / 2 && steps >= 2 * kMinSteps && B <= kMaxShared &&
+  const int64_t n = units * steps < kShares ? units * steps : kShares;
+  p.flat = units < 2 * kShares && steps >= kMinSteps && B <= kMaxShared &&
            units * steps < (int64_t)1 << 31;  // steps are counted in 32 bits
   p.grid = p.flat ? n : units;
   return p;
-}
-
-__device__ __forceinline__ int queries_of(const KvAttnArgs& a, int b, int* q0) {
-  if (!a.q_starts) {
-    *q0 = b;
-    return 1;
-  }
-  *q0 = max(a.q_starts[b], 0);
-  return (int)max((int64_t)0, min(min((int64_t)a.q_starts[b + 1], a.T) - *q0, a.max_queries));
-}
-__device__ __forceinline__ int length_of(const KvAttnArgs& a, int b) {
-  return (int)max((int64_t)0, min((int64_t)a.lens[b], a.max_context));
 }
 
 // Units of sequence b and steps of each (one at least: a row that sees nothing
@@ -153,7 +145,7 @@ __device__ __forceinline__ Shares scan_shares(const KvAttnArgs& a, uint32_t wgs,
     total += (uint32_t)__builtin_amdgcn_readlane((int)run, 63);
   }
   Shares s;
-  s.n = max(min(wgs, (total + kMinSteps - 1) / kMinSteps), 1u);
+  s.n = max(min(wgs, total), 1u);
   s.q = total / s.n;
   s.r = total - s.q * s.n;
   return s;
@@ -164,76 +156,53 @@ __device__ __forceinline__ uint32_t share_of(const Shares& s, uint32_t at) {  //
   return at < long_end ? at / (s.q + 1) : s.r + (at - long_end) / s.q;
 }
 
-__device__ __forceinline__ float max_over_rows16(float v) {  // over the lanes l, l ^ 16, l ^ 32, l ^ 48
-  const uint32_t u = __builtin_bit_cast(uint32_t, v);
-  auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  v = fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
-  const uint32_t w = __builtin_bit_cast(uint32_t, v);
+// Over the lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ float max_over_rows16(float v) {
+  const uint32_t w = __builtin_bit_cast(uint32_t, max_over_halves(v));
   auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
   return fmaxf(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
 }
 __device__ __forceinline__ float sum_over_rows16(float v) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, v);
-  auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  v = __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
-  const uint32_t w = __builtin_bit_cast(uint32_t, v);
+  const uint32_t w = __builtin_bit_cast(uint32_t, sum_over_halves(v));
   auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
   return __builtin_bit_cast(float, (uint32_t)b[0]) + __builtin_bit_cast(float, (uint32_t)b[1]);
 }
 
 __device__ __forceinline__ void store_pair(const KvAttnArgs& a, int64_t at, float x, float y) {
-  const uint32_t lo = a.dtype == 1 ? f32_to_bf16_bits(x) : f32_to_f16_bits(x);
-  const uint32_t hi = a.dtype == 1 ? f32_to_bf16_bits(y) : f32_to_f16_bits(y);
-  *reinterpret_cast<uint32_t*>(a.out + at) = lo | (hi << 16);
-}
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.0f ? kNegInf : (m + __builtin_log2f(l)) * 0.6931471805599453f;
-}
-
-// The eight codes of a word less their zero-point(s) as four fp16 pairs, of
-// nibbles 0 and 4, 1 and 5, 2 and 6, 3 and 7: 1024 + c and 64 + c by OR-ing an
-// exponent in (wq_device.h), less the same of z.  The exponents come in vector
-// registers: v_and_or_b32 takes one scalar operand and no literal.
-struct Magic {
-  uint32_t e10 = 0x64006400u, e6 = 0x54005400u;
-  __device__ __forceinline__ Magic() {
-    asm("" : "+v"(e10));
-    asm("" : "+v"(e6));
-  }
-};
-__device__ __forceinline__ u4 code_pairs(uint32_t w, uint32_t z10, uint32_t z6, const Magic& g) {
-  const uint32_t w8 = w >> 8;
-  return u4{as_u32(as_h2((w & 0x000F000Fu) | g.e10) - as_h2(z10)), as_u32(as_h2((w & 0x00F000F0u) | g.e6) - as_h2(z6)),
-            as_u32(as_h2((w8 & 0x000F000Fu) | g.e10) - as_h2(z10)), as_u32(as_h2((w8 & 0x00F000F0u) | g.e6) - as_h2(z6))};
+  *reinterpret_cast<uint32_t*>(a.out + at) = pack_out(a.dtype, x, y);
 }
 
 // What a wave covers of a cache row, and one 32-token tile of it as loaded.
 template <int D, int HP>
 struct Tile {
   static constexpr int NB = HP * D / 128;         // cache blocks
-  static constexpr int kChunks = HP * D / 32;     // 16-byte chunks of K codes of a token
+  static constexpr int kChunks = HP * D / 32;     // 16-byte chunks of a token's codes
   static constexpr int kTok = 64 / kChunks;       // tokens of one 16-byte load a lane
   static constexpr int KL = 32 / kTok;            // such loads
-  static constexpr int NV = D == 64 ? HP : NB;    // V words (D = 64: half words) of a lane and token
-  u4 k[KL];
-  uint32_t v[8][NV];
+  u4 k[KL], v[KL];
   uint32_t s;  // scales of the blocks (16 bits each): lanes 0..31 K's of token l, lanes 32..63 V's of token l - 32
   uint32_t z;  // the zero-point byte beside them
   bool ok;     // the tile's page (small pages: the page of the lane's token) exists
 };
 
-// K codes of a tile pass through LDS: they are loaded as whole rows (4 or 8 lanes
-// a token) and read as operands (16 tokens of one chunk).  Chunk j of token t sits
-// at k_place, so that those 16 fall in different banks.
+// The codes of a tile pass through LDS: they are loaded as whole rows (4 or 8
+// lanes a token) and read as operands: K's 16 tokens of one chunk, V's 8 bytes of
+// a token a lane, four tokens of 64 channels, which the reading instruction
+// transposes.  Chunk j of token t sits where the lanes that read together fall in
+// different banks.
 template <int CHUNKS>
 __device__ __forceinline__ int k_place(int t, int j) {
   return CHUNKS == 4 ? j ^ (t >> 2 & 3) : j ^ (t >> 1 & 7);
 }
-// Words of LDS: a wave's scales, zero-points and K codes of a tile; over them, at
+template <int CHUNKS>
+__device__ __forceinline__ int v_place(int t, int j) {
+  return CHUNKS == 4 ? j ^ 2 * (t >> 2 & 1) : j ^ 2 * (t >> 1 & 3);
+}
+// Words of LDS: a wave's scales, zero-points and codes of a tile; over them, at
 // the end, its results of one row tile and block; then the waves' statistics and
 // the shares.
 template <int D, int HP>
-constexpr int kWalk = kMeta * Tile<D, HP>::NB + 128 * Tile<D, HP>::kChunks;
+constexpr int kWalk = kMeta * Tile<D, HP>::NB + 2 * 128 * Tile<D, HP>::kChunks;
 template <int D>
 constexpr int kSlabRow = (D < 128 ? D : 128) + 4;  // padded: rows in different banks
 template <int D>
@@ -261,6 +230,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
   const int pages = (int)(a.S >> lg);
   float* meta = reinterpret_cast<float*>(lds) + wave * kWalk<D, HP>;
   u4* kd = reinterpret_cast<u4*>(meta + kMeta * NB);
+  u4* vd = kd + 32 * T::kChunks;
   float* slab = reinterpret_cast<float*>(lds);
   float* stat = slab + kWaves * kPerWave<D, HP>;  // [wave][2][16]
   ShareLds* shares = reinterpret_cast<ShareLds*>(lds + kWaves * (kPerWave<D, HP> + 32));
@@ -332,8 +302,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
     asm volatile("" : "+v"(ln));
     const uint16_t* sp = (ln < 32 ? a.k_s : a.v_s) + blk + (P32 ? (ln & 31) * nbt : 0);
     const uint8_t* zp = (ln < 32 ? a.k_zp : a.v_zp) + blk / 2 + (P32 ? (ln & 31) * zb : 0);
-    const uint32_t k_at = 16 * (ln % T::kChunks) + (P32 ? ln / T::kChunks * rowb : 0);
-    const uint32_t v_at = (D == 64 ? 2 : 4) * (ln & 15) + (P32 ? 4 * (ln >> 4) * rowb : 0);
+    const uint32_t c_at = 16 * (ln % T::kChunks) + (P32 ? ln / T::kChunks * rowb : 0);
 
     // page entries of a tile: one of the whole tile (P32) or one of lane ml's token
     auto page_entry = [&](int tk) -> int {
@@ -345,43 +314,30 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
       *ok = pg >= 0 && pg < pages;
       return *ok ? (pg << lg) + ((P32 ? tk : tk + ml) & (a.page - 1)) : 0;  // none: the first rows of the cache
     };
-    auto load_k = [&](T& t, int row) {
+    auto load_codes = [&](u4 (&to)[T::KL], const uint8_t* from, int row) {
+      uint32_t off = c_at;  // a lane's offset from a scalar address (not folded into a 64-bit one outside the loop)
+      asm volatile("" : "+v"(off));
+#pragma unroll
+      for (int i = 0; i < T::KL; ++i) {
+        const uint8_t* p = from + (int64_t)(P32 ? row + T::kTok * i : __shfl(row, T::kTok * i + lane / T::kChunks)) * rowb;
+        if constexpr (P32) asm volatile("" : "+s"(p));
+        to[i] = *reinterpret_cast<const u4*>(p + off);
+      }
+    };
+    auto load = [&](T& t, int row) {
       const uint16_t* s = sp + (int64_t)row * nbt;
       if constexpr (NB == 2) __builtin_memcpy(&t.s, s, 4);
       else t.s = *s;
       t.z = (zp + (int64_t)row * zb)[0];
-      uint32_t off = k_at;  // a lane's offset from a scalar address (not folded into a 64-bit one outside the loop)
-      asm volatile("" : "+v"(off));
-#pragma unroll
-      for (int i = 0; i < T::KL; ++i) {
-        const uint8_t* p = kc + (int64_t)(P32 ? row + T::kTok * i : __shfl(row, T::kTok * i + lane / T::kChunks)) * rowb;
-        if constexpr (P32) asm volatile("" : "+s"(p));
-        t.k[i] = *reinterpret_cast<const u4*>(p + off);
-      }
-    };
-    auto load_v = [&](T& t, int row) {
-      uint32_t off = v_at;
-      asm volatile("" : "+v"(off));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int tok = 16 * (i / 4) + i % 4;
-        const uint8_t* p = vc + (int64_t)(P32 ? row + tok : __shfl(row, tok + 4 * c)) * rowb;
-        if constexpr (P32) asm volatile("" : "+s"(p));
-        p += off;
-#pragma unroll
-        for (int n = 0; n < T::NV; ++n) {
-          if constexpr (D == 64) t.v[i][n] = *reinterpret_cast<const uint16_t*>(p + 32 * n);
-          else t.v[i][n] = *reinterpret_cast<const uint32_t*>(p + 64 * n);
-        }
-      }
+      load_codes(t.k, kc, row);
+      load_codes(t.v, vc, row);
     };
 
     T tile;
     int tk = t_begin + 32 * wave, row = 0, pg = 0;
     if (tk < t_end) {
       row = rows_of(tk, page_entry(tk), &tile.ok);
-      load_k(tile, row);
-      load_v(tile, row);
+      load(tile, row);
       pg = page_entry(tk + kStep);
     }
 
@@ -406,36 +362,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
         raw[j] = *reinterpret_cast<const u4*>(qp + ch);
       }
       float y[NS][8], top_q = 0.0f;
-      if (a.dtype == 1) {
 #pragma unroll
-        for (int j = 0; j < NS; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            y[j][e] = __builtin_bit_cast(float, e % 2 ? raw[j][e / 2] & 0xffff0000u : raw[j][e / 2] << 16);
-      } else {
-#pragma unroll
-        for (int j = 0; j < NS; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[j][e] = (float)__builtin_bit_cast(h8, raw[j])[e];
-      }
+      for (int j = 0; j < NS; ++j) widen8(raw[j], a.dtype, y[j]);
 #pragma unroll
       for (int j = 0; j < NS; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) top_q = fmaxf(top_q, fabsf(y[j][e]));
-      top_q = max_over_rows16(top_q);
-      int ex = (int)(__builtin_bit_cast(uint32_t, top_q) >> 23) - 127;
-      ex = min(max(ex, -126), 126);  // zeros, subnormals and infinities: the nearest power
-      const float down = __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23);
-      const float up = __builtin_bit_cast(float, (uint32_t)(127 + ex) << 23);
-      f[x] = a.scale * 1.4426950408889634f * up;
+      const RowPower pw = row_power(max_over_rows16(top_q));
+      f[x] = score_factor(a.scale, pw.up);
 #pragma unroll
       for (int j = 0; j < NS; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) qf[x][j][e] = (_Float16)(y[j][e] * down);
+        for (int e = 0; e < 8; ++e) qf[x][j][e] = (_Float16)(y[j][e] * pw.down);
     }
 
     f4 acc[X][NE];
-    float m[X], l[X];  // weights are 2^(score - m); m follows the largest score + v_exp
+    float m[X], l[X];  // weights are 2^(score - m); m follows the largest score + v_top's power
 #pragma unroll
     for (int x = 0; x < X; ++x) {
       m[x] = kNegInf;
@@ -443,16 +385,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
 #pragma unroll
       for (int e = 0; e < NE; ++e) acc[x][e] = f4{0, 0, 0, 0};
     }
-    // V scales so far are at most v_top (fp16 bits) < 2^v_exp, for each block (a
-    // head of two: for both)
-    constexpr int NT = NB / NH;
-    uint32_t v_top[NT];
-    float v_exp[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) v_top[n] = 0, v_exp[n] = -25.0f;
+    ScaleTop v_top[NB / NH];  // of each block (a head of two: of both)
 
-    // Works on tile tk; K and V of the next tile (rows `row`) replace this one's as
-    // soon as they are decoded.
+    // Works on tile tk; the next tile (rows `next`) is loaded as soon as this one
+    // lies in LDS.
     auto compute = [&](int next, bool next_ok) {
       const bool ok = tile.ok;
       // scales and zero-points through LDS to the lanes that need them, in the
@@ -474,15 +410,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
           reinterpret_cast<uint16_t*>(mn + 128)[ml] = (uint16_t)z10;
           reinterpret_cast<uint16_t*>(mn + 144)[ml] = (uint16_t)z6;
         }
-        // a V scale above all so far (rare): the next power of two from the largest
-        if (__ballot(lane >= 32 && sb > v_top[n / NH])) {
-          uint32_t top = lane >= 32 ? sb & 0x7fffu : 0u;
-#pragma unroll
-          for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-          top = __builtin_amdgcn_readfirstlane(top);
-          v_exp[n / NH] = (float)((int)(__builtin_bit_cast(uint32_t, f16_bits_to_f32((uint16_t)top)) >> 23) - 126);
-          v_top[n / NH] = top >> 10 ? top | 0x3ffu : 0xffffffffu >> __builtin_clz(top);
-        }
+        raise_top(v_top[n / NH], lane >= 32 ? sb : 0u);
       }
       // tokens of small pages that do not exist, a bit each (P32: all or none)
       const uint32_t gone = P32 ? 0u : ~(uint32_t)__ballot(ok);
@@ -491,7 +419,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
       for (int i = 0; i < T::KL; ++i) {
         const int t = T::kTok * i + lane / T::kChunks;
         kd[t * T::kChunks + k_place<T::kChunks>(t, lane % T::kChunks)] = tile.k[i];
+        vd[t * T::kChunks + v_place<T::kChunks>(t, lane % T::kChunks)] = tile.v[i];
       }
+      __builtin_amdgcn_sched_barrier(0);
+      load(tile, next);
+      tile.ok = next_ok;
       f4 sc[X][2][NH];
 #pragma unroll
       for (int g = 0; g < 2; ++g)
@@ -522,9 +454,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
                     __builtin_bit_cast(h8, d), qf[p * RT + t][NS / NH * n + j], sc[p * RT + t][g][n], 0, 0, 0);
             }
           }
-      __builtin_amdgcn_sched_barrier(0);
-      load_k(tile, next);
-      tile.ok = next_ok;
       // scores times their token's scale
 #pragma unroll
       for (int g = 0; g < 2; ++g)
@@ -568,7 +497,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
           float mx = s8[0];
 #pragma unroll
           for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s8[i]);
-          mx = __builtin_fmaf(max_over_rows16(mx), f[x], v_exp[D == 64 ? p / 2 : p / NH]);
+          mx = __builtin_fmaf(max_over_rows16(mx), f[x], v_top[D == 64 ? p / 2 : p / NH].exp);
           if (__ballot(mx > m[x] + kLag)) {
             const float mn = fmaxf(m[x], mx);
             const float al = m[x] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[x] - mn);
@@ -599,24 +528,26 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
             z10[2 * g] = w10[0], z10[2 * g + 1] = w10[1], z6[2 * g] = w6[0], z6[2 * g + 1] = w6[1];
           }
 #pragma unroll
-          for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
+          for (int j = 0; j < (D == 64 ? 1 : 2); ++j) {
+            // 64 channels: lane m gets their half word m (four channels, every second
+            // of eight) of its eight tokens, in pairs
+            const int h = 2 * (n + p * NH) + j, q64 = D == 64 ? p : h, t4 = 4 * c + r / 4;
+            const u2* at64 = reinterpret_cast<const u2*>(vd + t4 * T::kChunks + v_place<T::kChunks>(t4, 2 * q64 + r % 4 / 2)) + r % 2;
+            const u2 y0 = read_transposed(at64), y1 = read_transposed(at64 + 2 * 16 * T::kChunks);
+            const uint32_t y[4] = {y0[0], y0[1], y1[0], y1[1]};
             u4 d[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              // even (odd) channels of two tokens
-              const u4 y = code_pairs(__builtin_amdgcn_perm(tile.v[2 * i + 1][p + n], tile.v[2 * i][p + n],
-                                                            half ? 0x07060302u : 0x05040100u),
-                                      z10[i], z6[i], magic);
+              const u4 w = code_pairs(y[i], z10[i], z6[i], magic);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) d[e][i] = y[e];
+              for (int e = 0; e < 4; ++e) d[e][i] = w[e];
             }
-            // MFMA e of a block: channel 8 m + e of row m (D = 64: channel
-            // 8 (m / 2) + m % 2 + 2 e)
+            // MFMA k of them: row m is channel 8 (m / 2) + m % 2 + 2 k
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
               for (int t = 0; t < RT; ++t) {
-                const int e = D == 64 ? k : 8 * n + 2 * k + half;
+                const int e = 8 * n + 4 * j + k;
                 acc[p * RT + t][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, d[k]), pf[t][n],
                                                                            acc[p * RT + t][e], 0, 0, 0);
               }
@@ -632,7 +563,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
         row = rows_of(min(tk + kStep, (t_end - 1) & ~31), pg, &ok);
         pg = page_entry(tk + 2 * kStep);
         compute(row, ok);
-        load_v(tile, row);
         tk += kStep;
       } while (tk < t_end);
     }
@@ -668,21 +598,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
         if (n) __syncthreads();
         float* mine = slab + wave * kSlab<D> + re * kSlabRow<D>;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (D == 64) {
-            // rows 2 j, 2 j + 1 of the product are the even and odd channels of eight
-            if (i % 2 == 0) {
-              float* at8 = mine + 8 * (2 * ce + i / 2);
-              *reinterpret_cast<f4*>(at8) = f4{acc[x][0][i], acc[x][0][i + 1], acc[x][1][i], acc[x][1][i + 1]} * k;
-              *reinterpret_cast<f4*>(at8 + 4) = f4{acc[x][2][i], acc[x][2][i + 1], acc[x][3][i], acc[x][3][i + 1]} * k;
-            }
-          } else {
-            float* at8 = mine + 8 * (4 * ce + i);
-            const int e = 8 * n;
-            *reinterpret_cast<f4*>(at8) = f4{acc[x][e][i], acc[x][e + 1][i], acc[x][e + 2][i], acc[x][e + 3][i]} * k;
-            *reinterpret_cast<f4*>(at8 + 4) = f4{acc[x][e + 4][i], acc[x][e + 5][i], acc[x][e + 6][i], acc[x][e + 7][i]} * k;
+        for (int j = 0; j < DB / 64; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            // rows 2 w, 2 w + 1 of the product are the even and odd channels of eight
+            const f4* v = &acc[x][8 * n + 4 * j];
+            float* at8 = mine + 64 * j + 8 * (2 * ce + i / 2);
+            *reinterpret_cast<f4*>(at8) = f4{v[0][i], v[0][i + 1], v[1][i], v[1][i + 1]} * k;
+            *reinterpret_cast<f4*>(at8 + 4) = f4{v[2][i], v[2][i + 1], v[3][i], v[3][i + 1]} * k;
           }
-        }
         __syncthreads();
         // a thread: two channels of one row
         for (uint32_t y = tid; y < 16 * DB / 2; y += 64 * kWaves) {
@@ -848,12 +772,16 @@ size_t kv_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int64_t max_contex
 int describe_kv_attn(int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries, char* buf,
                      size_t len) {
   const KvPlan p = plan_kv(B, Hq, Hkv, D, max_context, max_queries);
+  if (p.chunk)
+    return snprintf(buf, len, "kv_chunk_kernel<D=%d, HP=%d, RT=%d> grid=%lld block=%d whole units", D, p.HP,
+                    p.RT, (long long)p.grid, 64 * kChunkWaves);
   return snprintf(buf, len, "kv_attn_kernel<D=%d, HP=%d, RT=%d, P32=%d> grid=%lld block=%d %s", D, p.HP, p.RT,
                   page % 32 == 0 ? 1 : 0, (long long)p.grid, 64 * kWaves, p.flat ? "shares" : "whole units");
 }
 
 hipError_t launch_kv_attn(const KvAttnArgs& a, hipStream_t stream) {
   const KvPlan p = plan_kv(a.B, a.Hq, a.Hkv, a.D, a.max_context, a.max_queries);
+  if (p.chunk) return launch_kv_chunk(a, p.grid, p.rtiles, stream);
   if (a.D == 256) return launch_p<256, 1, 1>(a, p, stream);
   if (a.D == 128) {
     if (p.RT == 2) return launch_p<128, 1, 2>(a, p, stream);

@@ -30,21 +30,15 @@
 // tile slots from floor(start_b G / 128) + b on, at least as many as it has
 // tiles and increasing in b, so no host needs the lengths.  Later (longer) tiles
 // go first.
-#include "wq_device.h"
-#include "wq_kernels.h"
+#include "wq_attn.h"
 
 namespace wq {
 namespace {
 
-typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-typedef short s4 __attribute__((ext_vector_type(4)));
-typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 
-constexpr float kNegInf = -__builtin_inff();
 constexpr int kRows = 128;
-constexpr float kLag = 8.0f;
 
 template <bool BF>
 __device__ __forceinline__ f16v mfma32(u4 x, u4 y, f16v c) {
@@ -66,12 +60,6 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
   }
 }
 
-__device__ __forceinline__ float max_over_halves(float v) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, v);
-  auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
-}
-
 // Ones over each 16-bit half of a word that holds a finite value.
 template <bool BF>
 __device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
@@ -81,12 +69,6 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
 template <bool BF>
 __device__ __forceinline__ float to_f32(uint32_t h) {
   return BF ? __builtin_bit_cast(float, h << 16) : f16_bits_to_f32((uint16_t)h);
-}
-
-// Four 16-bit values of each lane of 16, transposed in blocks of 4 x 16: lane i
-// gets value i % 4 of lanes i / 4, i / 4 + 4, i / 4 + 8, i / 4 + 12.
-__device__ __forceinline__ u2 read_transposed(const u2* p) {
-  return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p));
 }
 
 template <int D>
@@ -292,11 +274,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_attn_kernel(Prom
     step(kt, 0);
     if (kt + 1 < tiles) step(kt + 1, 1);
   }
-  {
-    const uint32_t u = __builtin_bit_cast(uint32_t, l);
-    auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    l = __builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]);
-  }
+  l = sum_over_halves(l);
   if (Rw + r < n * G) {
     const float inv = 1.0f / l;
     const int64_t at = (q0 + qi) * a.Hq + head;
