@@ -275,19 +275,29 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_attn_kernel(Prom
     if (kt + 1 < tiles) step(kt + 1, 1);
   }
   l = sum_over_halves(l);
-  if (Rw + r < n * G) {
+  // The outputs leave through LDS as whole rows, 16 bytes a lane: a lane holds 8 bytes
+  // here and there of its row, and the cache takes a write of 16 bytes no faster than
+  // one of a line.
+  {
     const float inv = 1.0f / l;
-    const int64_t at = (q0 + qi) * a.Hq + head;
-    uint16_t* o = a.out + at * D;
+    const uint32_t at = (uint32_t)(qi * a.Hq + head);  // the row among the sequence's
+    if (a.lse && hf == 0 && Rw + r < n * G) a.lse[q0 * a.Hq + at] = (m + __builtin_log2f(l)) * 0.6931471805599453f;
+    u4* ob = tile + wave * (32 * NC);
+    constexpr int kTurn = NC < 16 ? NC - 1 : 15;
 #pragma unroll
     for (int d = 0; d < NB; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const u2 w = {pack_pair<BF>(acc[d][i] * inv, acc[d][i + 1] * inv),
-                      pack_pair<BF>(acc[d][i + 2] * inv, acc[d][i + 3] * inv)};
-        *reinterpret_cast<u2*>(o + 32 * d + 2 * i + 4 * hf) = w;
-      }
-    if (a.lse && hf == 0) a.lse[at] = (m + __builtin_log2f(l)) * 0.6931471805599453f;
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<u2*>(ob + r * NC + ((4 * d + i) ^ (r & kTurn)))[hf] =
+            u2{pack_pair<BF>(acc[d][4 * i] * inv, acc[d][4 * i + 1] * inv),
+               pack_pair<BF>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv)};
+#pragma unroll
+    for (int x = 0; x < NC / 2; ++x) {
+      const int rr = (64 * x + lane) / NC, j = lane % NC;
+      const u4 v = ob[rr * NC + (j ^ (rr & kTurn))];
+      const uint32_t to = (uint32_t)__shfl((int)at, rr);
+      if (Rw + rr < n * G) *reinterpret_cast<u4*>(a.out + (q0 * a.Hq + to) * D + 8 * j) = v;
+    }
   }
   // infinities and NaNs of the partly seen tiles: a thread per channel adds them,
   // key by key, to the stored rows that see the key
