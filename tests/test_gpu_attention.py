@@ -405,6 +405,48 @@ def test_cache_attention_long_contexts_are_split_and_joined(B, n, Hq, Hkv, D, pa
     assert torch.equal(got, again) and torch.equal(lse, lse2)  # the same bits
 
 
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("Hq,Hkv,D,nq,plan", [
+    (16, 8, 64, 1, "HP=4, RT=1, PK=4"), (8, 8, 64, 4, "HP=4, RT=1, PK=4"), (14, 2, 64, 1, "HP=2, RT=1, PK=2"), (40, 8, 64, 2, "HP=2, RT=1, PK=1"),
+    (48, 8, 64, 3, "HP=2, RT=2, PK=1"), (64, 8, 128, 1, "HP=2, RT=1, PK=2"), (12, 4, 128, 2, "HP=2, RT=1, PK=2"), (18, 2, 128, 1, "HP=2, RT=1, PK=1"),
+    (15, 5, 128, 5, "HP=1, RT=1, PK=1"), (24, 8, 128, 7, "HP=1, RT=2, PK=1"), (40, 4, 256, 3, "HP=1, RT=1, PK=1")])
+def test_cache_attention_kernels_of_long_contexts(Hq, Hkv, D, nq, plan, page):
+    """Room for a million tokens (which picks the kernel) with short and long
+    contexts in it: heads that share a wave or a tile of rows differ in their
+    scales by orders of magnitude."""
+    say(f"cache room for long contexts Hq={Hq} Hkv={Hkv} D={D} nq={nq} page={page}")
+    lens, width = [700, 0, 3, 1300, 129], 2 ** 20 // page
+    starts = [0, nq, nq, 2 * nq, 3 * nq, 4 * nq] if nq > 1 else list(range(6))
+    S = 2304
+    cache = Cache(D + nq, S, Hkv, D)
+    for i in range(2):
+        X = ref.values(D + i, (S, Hkv, D), torch.float32).numpy() * (10.0 ** (np.arange(Hkv) % 4 - 2.0))[None, :, None].astype(np.float32)
+        oracle.kv_quantize(np.ascontiguousarray(X.reshape(S, -1), np.float32), cache.host[i])
+        cache.val[i] = torch.from_numpy(oracle.kv_dequant(cache.host[i], S, Hkv * D)).view(S, Hkv, D).double()
+    table = _tables(D, lens, page, S, width=width)
+    table[3, 700 // page] = -1
+    q = ref.values(Hq, (starts[-1], Hq, D), HF)
+    assert plan in wq.wq_kv_attention_plan(q.shape[0], Hq, Hkv, D, 5, page, 2 ** 20, nq)
+    want, used = _cache_want(cache, q, table, page, lens, starts, D ** -0.5)
+    got, lse = _run_cache(cache.to_dev(used), q.cuda(), table, page, lens, None if nq == 1 else starts, max_queries=nq)
+    _check_rows(got, lse, want)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,room", [(8, 2, 128, 128), (8, 2, 128, 2 ** 18), (4, 4, 64, 2 ** 18), (3, 1, 256, 256)])
+def test_cache_attention_more_sequences_than_are_shared_out(Hq, Hkv, D, room):
+    """300 sequences: a workgroup for each and its heads, however long they may be."""
+    rng = np.random.default_rng(D)
+    lens = [int(x) for x in rng.integers(0, 100, 300)]
+    page, S = 32, 300 * 128
+    cache = Cache(D, S, Hkv, D)
+    table = _tables(D, lens, page, S, width=room // page)
+    q = ref.values(Hq, (300, Hq, D), BF)
+    assert wq.wq_kv_attention_plan(300, Hq, Hkv, D, 300, page, room, 1).endswith("whole units")
+    want, used = _cache_want(cache, q, table, page, lens, list(range(301)), D ** -0.5)
+    got, lse = _run_cache(cache.to_dev(used), q.cuda(), table, page, lens, None)
+    _check_rows(got, lse, want)
+
+
 @pytest.mark.parametrize("dtype,qs,ks,vs", [(BF, 1e30, 1e-3, 1e-4), (HF, 3e4, 1e-4, 1e-4), (BF, 1e-30, 1e3, 1e3), (HF, 1e-4, 1.0, 2e4),
                                             (BF, 1.0, 1.0, 1e-6), (HF, 1e4, 1e-3, 1e3)])
 def test_cache_attention_value_ranges(dtype, qs, ks, vs):

@@ -34,7 +34,12 @@
 // LDS, and the next tile's are in flight while it computes.  It takes as many
 // neighbouring KV heads as fill a 128-byte line (two of 128 values): what a CU
 // can have in flight is bounded by the lines of its 32 KB cache, and half-used
-// lines halve it (one head a wave read 4.4 TB/s where two read 5.0).  The waves of
+// lines halve it (one head a wave read 4.4 TB/s where two read 5.0).  Decoding and
+// the softmax come next, so heads with few rows (a decode step of 8 query heads a
+// KV head, say) share a tile's 16 columns: each head's product has zeros for the
+// others' columns, all of them add up in one accumulator, and one softmax serves
+// all (64 contexts of up to 8K: heads of 64 in groups of four 79 -> 63 us, heads
+// of 128 in groups of eight 113 -> 110).  The waves of
 // a workgroup take different tiles of the same heads and join in LDS.  Where
 // sequences and heads are too few to fill the GPU evenly, all steps of all units
 // are shared out equally; units that end up in several workgroups leave fp32
@@ -55,6 +60,7 @@ constexpr int kWaves = 4;
 
 struct KvPlan {
   int HP;        // KV heads of a wave
+  int PK;        // of them, heads that share a tile of 16 rows
   int RT;        // 16-row tiles of a head
   int rtiles;    // units along the query rows of one KV head
   int urows;     // query rows of a unit and head that a call can use
@@ -68,7 +74,7 @@ struct KvPlan {
 KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_queries) {
   KvPlan p;
   const int64_t G = Hq / Hkv, rows = max_queries * G;
-  p.HP = 1;
+  p.HP = p.PK = 1;
   p.RT = 2 * kChunkWaves;
   p.rtiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
   p.urows = 16 * p.RT;
@@ -83,10 +89,13 @@ KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_q
   p.rtiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
   p.urows = (int)(rows < 16 * p.RT ? rows : 16 * p.RT);
   const int64_t steps = (max_context + 32 * kWaves - 1) / (32 * kWaves);
-  // two heads of 128 to a wave once that fills the GPU (below, twice the waves
-  // count more)
+  // whole 128-byte lines to a wave (two heads of 128; four of 64, if their rows fit
+  // a tile together) once that fills the GPU (below, twice the waves count more)
   p.HP = D == 64 ? 2 : 1;
-  if (D == 128 && p.RT == 1 && Hkv % 2 == 0 && (int64_t)B * (Hkv / 2) * p.rtiles * steps >= 2 * kShares) p.HP = 2;
+  const int line = 256 / D;
+  if (p.RT == 1 && (D == 128 || rows <= 4) && Hkv % line == 0 && (int64_t)B * (Hkv / line) * p.rtiles * steps >= 2 * kShares)
+    p.HP = line;
+  p.PK = rows * p.HP <= 16 ? p.HP : 1;
   const int64_t units = (int64_t)B * (Hkv / p.HP) * p.rtiles;
   // two workgroups a CU
   const int64_t n = units * steps < kShares ? units * steps : kShares;
@@ -212,16 +221,19 @@ constexpr int kPerWave = kWalk<D, HP> > kSlab<D> ? kWalk<D, HP> : kSlab<D>;
 template <int D, int HP>
 constexpr int lds_words = kWaves * (kPerWave<D, HP> + 32) + sizeof(ShareLds) / 4;
 
-template <int D, int HP, int RT, bool P32>
+template <int D, int HP, int RT, int PK, bool P32>
 __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, int rtiles, int urows, bool flat) {
   using T = Tile<D, HP>;
-  constexpr int NB = T::NB, X = HP * RT;  // blocks, row tiles of a wave (tile x: head x / RT)
+  constexpr int NB = T::NB;
+  constexpr int X = HP / PK * RT;         // row tiles of a wave: tile x has rows of heads x / RT * PK + sub
+  constexpr int PR = 16 / PK;             // rows of a head in a tile
   constexpr int NH = D == 256 ? 2 : 1;    // blocks of a head
   constexpr int NS = D / 32;              // MFMA steps of a score
   constexpr int NE = D / 16;              // MFMAs of an output tile: 16 channels each
   constexpr int kStep = 32 * kWaves;
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4, ml = lane & 31;
+  const int sub = r / PR;  // (0 unless heads share a tile)
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int HG = a.Hkv / HP, G = a.Hq / a.Hkv;
   const uint32_t rowb = (uint32_t)a.Hkv * (D / 2);  // code bytes of a cache row
@@ -344,13 +356,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
     // the wave's queries, as the B operand of the scores: lane (r, c) channels
     // 32 c + 8 j (D = 64: 16 c + 8 j) of each block, brought into fp16's range by
     // the power of two that takes the row's largest value into [1, 2)
-    h8 qf[X][NS];
+    h8 qf[HP * RT][NS];
     float f[X];   // score of a row in units of log2: raw * f
     int lim[RT];  // tokens the row sees, of those of this walk
 #pragma unroll
-    for (int x = 0; x < X; ++x) {
+    for (int x = 0; x < HP * RT; ++x) {
       const int t = x % RT;
-      const uint32_t qrow = min(row0 + 16 * t + r, rows - 1);  // rows past the end repeat the last, not stored
+      const uint32_t qrow = min(row0 + 16 * t + r % PR, rows - 1);  // rows past the end repeat the last, not stored
       const uint32_t qi = qrow / (uint32_t)G;
       lim[t] = min(t_end, len - nq + (int)qi + 1);
       const int head = (hg * HP + x / RT) * G + (int)(qrow - qi * G);
@@ -369,11 +381,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
 #pragma unroll
         for (int e = 0; e < 8; ++e) top_q = fmaxf(top_q, fabsf(y[j][e]));
       const RowPower pw = row_power(max_over_rows16(top_q));
-      f[x] = score_factor(a.scale, pw.up);
+      // heads that share a tile: 0 in the columns of the others
+      const bool mine = PK == 1 || x % PK == sub;
+      if (mine) f[x / PK] = score_factor(a.scale, pw.up);
 #pragma unroll
       for (int j = 0; j < NS; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) qf[x][j][e] = (_Float16)(y[j][e] * pw.down);
+        for (int e = 0; e < 8; ++e) qf[x][j][e] = mine ? (_Float16)(y[j][e] * pw.down) : (_Float16)0.0f;
     }
 
     f4 acc[X][NE];
@@ -444,48 +458,41 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
             }
             const u2 z = *reinterpret_cast<const u2*>(meta + kMeta * blkn + 64 + 2 * t16);
 #pragma unroll
-            for (int t = 0; t < RT; ++t) sc[p * RT + t][g][n] = f4{0, 0, 0, 0};
+            for (int t = 0; t < RT; ++t)
+              if (p % PK == 0) sc[p / PK * RT + t][g][n] = f4{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < NS / NH; ++j) {
               const u4 d = code_pairs(kw[j], z[0], z[1], magic);
 #pragma unroll
               for (int t = 0; t < RT; ++t)
-                sc[p * RT + t][g][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    __builtin_bit_cast(h8, d), qf[p * RT + t][NS / NH * n + j], sc[p * RT + t][g][n], 0, 0, 0);
+                sc[p / PK * RT + t][g][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                    __builtin_bit_cast(h8, d), qf[p * RT + t][NS / NH * n + j], sc[p / PK * RT + t][g][n], 0, 0, 0);
             }
           }
-      // scores times their token's scale
+      // heads (those that share a tile together) in turn: softmax of their row tiles,
+      // then O^T += V^T P^T
 #pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int p = 0; p < HP; ++p)
-#pragma unroll
-          for (int n = 0; n < NH; ++n) {
-            const f4 ks = *reinterpret_cast<const f4*>(meta + kMeta * (D == 64 ? p / 2 : p + n) + 16 * g + 4 * c);
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                f4& v = sc[p * RT + t][g][0];
-                v[i] = n == 0 ? v[i] * ks[i] : __builtin_fmaf(sc[p * RT + t][g][n][i], ks[i], v[i]);
-              }
-          }
-      // heads in turn: softmax of their row tiles, then O^T += V^T P^T
-#pragma unroll
-      for (int p = 0; p < HP; ++p) {
-        f4 vs[NH][2];
-#pragma unroll
-        for (int n = 0; n < NH; ++n)
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-            vs[n][g] = *reinterpret_cast<const f4*>(meta + kMeta * (D == 64 ? p / 2 : p + n) + 32 + 16 * g + 4 * c);
+      for (int hp = 0; hp < HP / PK; ++hp) {
+        const float* mh = meta + kMeta * (D == 64 ? (hp * PK + sub) / 2 : hp * PK + sub);
+        float v_exp = v_top[D == 64 ? hp * PK / 2 : hp * PK].exp;
+        if (PK > 1 && NB > 1 && sub >= PK / 2) v_exp = v_top[NB - 1].exp;
         h8 pf[RT][NH];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          const int x = p * RT + t;
+          const int x = hp * RT + t;
           float s8[8];
+          // scores times their token's scale
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s8[i] = sc[x][i / 4][0][i % 4];
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+              const f4 ks = *reinterpret_cast<const f4*>(mh + kMeta * n + 16 * g + 4 * c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float& v = s8[4 * g + i];
+                v = n == 0 ? sc[x][g][n][i] * ks[i] : __builtin_fmaf(sc[x][g][n][i], ks[i], v);
+              }
+            }
           if (masked) {
             const int seen = P32 && !ok ? 0 : lim[t] - tk;
 #pragma unroll
@@ -497,7 +504,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
           float mx = s8[0];
 #pragma unroll
           for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s8[i]);
-          mx = __builtin_fmaf(max_over_rows16(mx), f[x], v_top[D == 64 ? p / 2 : p / NH].exp);
+          mx = __builtin_fmaf(max_over_rows16(mx), f[x], v_exp);
           if (__ballot(mx > m[x] + kLag)) {
             const float mn = fmaxf(m[x], mx);
             const float al = m[x] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[x] - mn);
@@ -508,49 +515,70 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
           }
           const float ms = m[x] == kNegInf ? 0.0f : m[x];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s8[i], f[x], -ms));
-            l[x] += w;
+          for (int g = 0; g < 2; ++g) {
+            f4 vs[NH];
 #pragma unroll
-            for (int n = 0; n < NH; ++n) pf[t][n][i] = (_Float16)(w * vs[n][i / 4][i % 4]);
+            for (int n = 0; n < NH; ++n) vs[n] = *reinterpret_cast<const f4*>(mh + kMeta * n + 32 + 16 * g + 4 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s8[4 * g + i], f[x], -ms));
+              l[x] += w;
+#pragma unroll
+              for (int n = 0; n < NH; ++n) pf[t][n][4 * g + i] = (_Float16)(w * vs[n][i]);
+            }
           }
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int n = 0; n < NH; ++n) {
-          // 1024 + z and 64 + z of the token pairs
-          const float* mn = meta + kMeta * (D == 64 ? p / 2 : p + n) + 128;
-          uint32_t z10[4], z6[4];
+        for (int y = 0; y < PK; ++y) {
+          const int p = hp * PK + y;
+          h8 pm[RT][NH];  // (a shared tile: the weights of this head's rows)
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const u2 w10 = *reinterpret_cast<const u2*>(mn + 8 * g + 2 * c);
-            const u2 w6 = *reinterpret_cast<const u2*>(mn + 16 + 8 * g + 2 * c);
-            z10[2 * g] = w10[0], z10[2 * g + 1] = w10[1], z6[2 * g] = w6[0], z6[2 * g + 1] = w6[1];
-          }
+          for (int t = 0; t < RT; ++t)
 #pragma unroll
-          for (int j = 0; j < (D == 64 ? 1 : 2); ++j) {
-            // 64 channels: lane m gets their half word m (four channels, every second
-            // of eight) of its eight tokens, in pairs
-            const int h = 2 * (n + p * NH) + j, q64 = D == 64 ? p : h, t4 = 4 * c + r / 4;
-            const u2* at64 = reinterpret_cast<const u2*>(vd + t4 * T::kChunks + v_place<T::kChunks>(t4, 2 * q64 + r % 4 / 2)) + r % 2;
-            const u2 y0 = read_transposed(at64), y1 = read_transposed(at64 + 2 * 16 * T::kChunks);
-            const uint32_t y[4] = {y0[0], y0[1], y1[0], y1[1]};
-            u4 d[4];
+            for (int n = 0; n < NH; ++n) {
+              u4 w = __builtin_bit_cast(u4, pf[t][n]);
+              if (PK > 1)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const u4 w = code_pairs(y[i], z10[i], z6[i], magic);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) d[e][i] = w[e];
+                for (int i = 0; i < 4; ++i) w[i] = sub == y ? w[i] : 0u;
+              pm[t][n] = __builtin_bit_cast(h8, w);
             }
-            // MFMA k of them: row m is channel 8 (m / 2) + m % 2 + 2 k
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+          for (int n = 0; n < NH; ++n) {
+            // 1024 + z and 64 + z of the token pairs
+            const float* mn = meta + kMeta * (D == 64 ? p / 2 : p + n) + 128;
+            uint32_t z10[4], z6[4];
 #pragma unroll
-              for (int t = 0; t < RT; ++t) {
-                const int e = 8 * n + 4 * j + k;
-                acc[p * RT + t][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, d[k]), pf[t][n],
-                                                                           acc[p * RT + t][e], 0, 0, 0);
+            for (int g = 0; g < 2; ++g) {
+              const u2 w10 = *reinterpret_cast<const u2*>(mn + 8 * g + 2 * c);
+              const u2 w6 = *reinterpret_cast<const u2*>(mn + 16 + 8 * g + 2 * c);
+              z10[2 * g] = w10[0], z10[2 * g + 1] = w10[1], z6[2 * g] = w6[0], z6[2 * g + 1] = w6[1];
+            }
+#pragma unroll
+            for (int j = 0; j < (D == 64 ? 1 : 2); ++j) {
+              // 64 channels: lane m gets their half word m (four channels, every second
+              // of eight) of its eight tokens, in pairs
+              const int h = 2 * (n + p * NH) + j, q64 = D == 64 ? p : h, t4 = 4 * c + r / 4;
+              const u2* at64 = reinterpret_cast<const u2*>(vd + t4 * T::kChunks + v_place<T::kChunks>(t4, 2 * q64 + r % 4 / 2)) + r % 2;
+              const u2 y0 = read_transposed(at64), y1 = read_transposed(at64 + 2 * 16 * T::kChunks);
+              const uint32_t yw[4] = {y0[0], y0[1], y1[0], y1[1]};
+              u4 d[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const u4 w = code_pairs(yw[i], z10[i], z6[i], magic);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[e][i] = w[e];
               }
+              // MFMA k of them: row m is channel 8 (m / 2) + m % 2 + 2 k
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                  const int e = 8 * n + 4 * j + k;
+                  acc[hp * RT + t][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, d[k]), pm[t][n],
+                                                                              acc[hp * RT + t][e], 0, 0, 0);
+                }
+            }
           }
         }
       }
@@ -611,7 +639,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
         // a thread: two channels of one row
         for (uint32_t y = tid; y < 16 * DB / 2; y += 64 * kWaves) {
           const int rr = y / (DB / 2), ch = 2 * (y % (DB / 2));
-          const uint32_t qrow = row0 + 16 * (x % RT) + rr;
+          const uint32_t qrow = row0 + 16 * (x % RT) + rr % PR;
+          const int h = x / RT * PK + rr / PR;  // of the unit's heads
           if ((int)qrow > row1) continue;
           float o0 = 0.0f, o1 = 0.0f, Mr = kNegInf, L = 0.0f;
 #pragma unroll
@@ -626,12 +655,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
           }
           const uint32_t qi = qrow / (uint32_t)G;
           if (whole) {
-            const int64_t orow = (int64_t)(q0 + qi) * a.Hq + (hg * HP + x / RT) * G + (qrow - qi * G);
+            const int64_t orow = (int64_t)(q0 + qi) * a.Hq + (hg * HP + h) * G + (qrow - qi * G);
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             store_pair(a, orow * D + 128 * n + ch, o0 * inv, o1 * inv);
             if (a.lse && ch == 0 && n == 0) a.lse[orow] = lse_of(Mr, L);
           } else {
-            const int64_t slot = ((int64_t)(2 * wg + (seg > 0)) * HP + x / RT) * urows + (qrow - row0);
+            const int64_t slot = ((int64_t)(2 * wg + (seg > 0)) * HP + h) * urows + (qrow - row0);
             *reinterpret_cast<float2*>(part + slot * D + 128 * n + ch) = make_float2(o0, o1);
             if (ch == 0 && n == 0) *reinterpret_cast<float2*>(stats + 2 * slot) = make_float2(Mr, L);
           }
@@ -740,13 +769,13 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnArgs a, int uro
   if (a.lse && lane == 0) a.lse[orow] = lse_of(M, L);
 }
 
-template <int D, int HP, int RT, bool P32>
+template <int D, int HP, int RT, int PK, bool P32>
 hipError_t launch_main(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream) {
   static std::atomic<uint64_t> raised{0};
   constexpr size_t lds = lds_words<D, HP> * 4;
-  const hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&kv_attn_kernel<D, HP, RT, P32>), lds, raised);
+  const hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&kv_attn_kernel<D, HP, RT, PK, P32>), lds, raised);
   if (e != hipSuccess) return e;
-  kv_attn_kernel<D, HP, RT, P32><<<(unsigned)p.grid, 64 * kWaves, lds, stream>>>(a, p.rtiles, p.urows, p.flat);
+  kv_attn_kernel<D, HP, RT, PK, P32><<<(unsigned)p.grid, 64 * kWaves, lds, stream>>>(a, p.rtiles, p.urows, p.flat);
   if (!p.flat) return hipGetLastError();
   const int64_t rows = (int64_t)a.B * a.max_queries * a.Hq, units = (int64_t)a.B * (a.Hkv / HP) * p.rtiles;
   // many pieces to a row: four waves share them
@@ -757,9 +786,9 @@ hipError_t launch_main(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream)
   return hipGetLastError();
 }
 
-template <int D, int HP, int RT>
+template <int D, int HP, int RT, int PK>
 hipError_t launch_p(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream) {
-  return a.page % 32 == 0 ? launch_main<D, HP, RT, true>(a, p, stream) : launch_main<D, HP, RT, false>(a, p, stream);
+  return a.page % 32 == 0 ? launch_main<D, HP, RT, PK, true>(a, p, stream) : launch_main<D, HP, RT, PK, false>(a, p, stream);
 }
 
 }  // namespace
@@ -775,19 +804,22 @@ int describe_kv_attn(int B, int Hq, int Hkv, int D, int page, int64_t max_contex
   if (p.chunk)
     return snprintf(buf, len, "kv_chunk_kernel<D=%d, HP=%d, RT=%d> grid=%lld block=%d whole units", D, p.HP,
                     p.RT, (long long)p.grid, 64 * kChunkWaves);
-  return snprintf(buf, len, "kv_attn_kernel<D=%d, HP=%d, RT=%d, P32=%d> grid=%lld block=%d %s", D, p.HP, p.RT,
+  return snprintf(buf, len, "kv_attn_kernel<D=%d, HP=%d, RT=%d, PK=%d, P32=%d> grid=%lld block=%d %s", D, p.HP, p.RT, p.PK,
                   page % 32 == 0 ? 1 : 0, (long long)p.grid, 64 * kWaves, p.flat ? "shares" : "whole units");
 }
 
 hipError_t launch_kv_attn(const KvAttnArgs& a, hipStream_t stream) {
   const KvPlan p = plan_kv(a.B, a.Hq, a.Hkv, a.D, a.max_context, a.max_queries);
   if (p.chunk) return launch_kv_chunk(a, p.grid, p.rtiles, stream);
-  if (a.D == 256) return launch_p<256, 1, 1>(a, p, stream);
+  if (a.D == 256) return launch_p<256, 1, 1, 1>(a, p, stream);
   if (a.D == 128) {
-    if (p.RT == 2) return launch_p<128, 1, 2>(a, p, stream);
-    return p.HP == 2 ? launch_p<128, 2, 1>(a, p, stream) : launch_p<128, 1, 1>(a, p, stream);
+    if (p.RT == 2) return launch_p<128, 1, 2, 1>(a, p, stream);
+    if (p.HP == 1) return launch_p<128, 1, 1, 1>(a, p, stream);
+    return p.PK == 2 ? launch_p<128, 2, 1, 2>(a, p, stream) : launch_p<128, 2, 1, 1>(a, p, stream);
   }
-  return p.RT == 2 ? launch_p<64, 2, 2>(a, p, stream) : launch_p<64, 2, 1>(a, p, stream);
+  if (p.RT == 2) return launch_p<64, 2, 2, 1>(a, p, stream);
+  if (p.HP == 4) return launch_p<64, 4, 1, 4>(a, p, stream);
+  return p.PK == 2 ? launch_p<64, 2, 1, 2>(a, p, stream) : launch_p<64, 2, 1, 1>(a, p, stream);
 }
 
 }  // namespace wq
