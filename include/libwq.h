@@ -571,8 +571,9 @@ int wq_prompt_attention(const void* q, const void* k, const void* v, int dtype, 
  * max_context (<= table_width * page_size) are attended.
  *   Queries: one per sequence (q_starts NULL, T == B, max_queries 1), or those
  * of sequence b at q_starts[b] .. q_starts[b + 1] - 1 (device int32 [B + 1],
- * increasing; at most max_queries of each are computed).  The n queries of a
- * sequence are its last n tokens: query i sees tokens t <= context_len - n + i.
+ * increasing; of each sequence the first max_queries are computed).  The n =
+ * q_starts[b + 1] - q_starts[b] queries of a sequence are its last n tokens: query
+ * i sees tokens t <= context_len - n + i.
  *   out[i] = sum_t softmax_t(scale * q_i . k_t) v_t with k and v decoded
  * exactly as s * (q - z); scores and sums in fp32; a softmax weight times its
  * token's V scale is rounded to fp16 for the product with the integers q - z;

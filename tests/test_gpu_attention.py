@@ -405,6 +405,22 @@ def test_cache_attention_long_contexts_are_split_and_joined(B, n, Hq, Hkv, D, pa
     assert torch.equal(got, again) and torch.equal(lse, lse2)  # the same bits
 
 
+@pytest.mark.parametrize("B,nq,most,room", [(3, 6, 4, 256), (2, 9, 2, 2 ** 20), (66, 140, 126, 256)])
+def test_cache_attention_computes_the_first_max_queries(B, nq, most, room):
+    """Sequences with more queries than are computed: the first ones are, and see
+    what they would see among all; the rows of the others stay as they were."""
+    Hq, Hkv, D, page = 8, 8, 128, 16
+    lens, starts = [nq + 3 * b % 50 for b in range(B)], [nq * b for b in range(B + 1)]
+    S = B * 16 * page
+    cache = Cache(nq, S, Hkv, D)
+    table = _tables(1, lens, page, S, width=room // page)
+    q = ref.values(Hq, (starts[-1], Hq, D), HF)
+    out, bound, lse, lb, none = _cache_want(cache, q, table, page, lens, starts, D ** -0.5)[0]
+    none[torch.arange(starts[-1]) % nq >= most] = True
+    got, got_lse = _run_cache(cache.to_dev(), q.cuda(), table, page, lens, starts, max_queries=most)
+    _check_rows(got, got_lse, (out, bound, lse, lb, none))
+
+
 @pytest.mark.parametrize("page", [16, 64])
 @pytest.mark.parametrize("Hq,Hkv,D,nq,plan", [
     (16, 8, 64, 1, "HP=4, RT=1, PK=4"), (8, 8, 64, 4, "HP=4, RT=1, PK=4"), (14, 2, 64, 1, "HP=2, RT=1, PK=2"), (40, 8, 64, 2, "HP=2, RT=1, PK=1"),

@@ -32,14 +32,15 @@ __device__ __forceinline__ float sum_over_halves(float v) {
   return __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
 }
 
-// Queries of sequence b (the first in *q0) and its tokens.
-__device__ __forceinline__ int queries_of(const KvAttnArgs& a, int b, int* q0) {
-  if (!a.q_starts) {
-    *q0 = b;
-    return 1;
-  }
-  *q0 = max(a.q_starts[b], 0);
-  return (int)max((int64_t)0, min(min((int64_t)a.q_starts[b + 1], a.T) - *q0, a.max_queries));
+// The queries of sequence b: `all` of them from q0 on, the first n are computed.
+struct Queries {
+  int q0, n, all;
+};
+__device__ __forceinline__ Queries queries_of(const KvAttnArgs& a, int b) {
+  if (!a.q_starts) return {b, 1, 1};
+  const int q0 = max(a.q_starts[b], 0);
+  const int64_t all = max((int64_t)0, min((int64_t)a.q_starts[b + 1], a.T) - q0);
+  return {q0, (int)min(all, a.max_queries), (int)all};
 }
 __device__ __forceinline__ int length_of(const KvAttnArgs& a, int b) {
   return (int)max((int64_t)0, min((int64_t)a.lens[b], a.max_context));

@@ -93,7 +93,8 @@ KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_q
   // a tile together) once that fills the GPU (below, twice the waves count more)
   p.HP = D == 64 ? 2 : 1;
   const int line = 256 / D;
-  if (p.RT == 1 && (D == 128 || rows <= 4) && Hkv % line == 0 && (int64_t)B * (Hkv / line) * p.rtiles * steps >= 2 * kShares)
+  if (p.RT == 1 && (D == 128 || rows <= 4) && Hkv % line == 0 &&
+      (int64_t)B * (Hkv / line) * p.rtiles * steps >= 2 * kShares)
     p.HP = line;
   p.PK = rows * p.HP <= 16 ? p.HP : 1;
   const int64_t units = (int64_t)B * (Hkv / p.HP) * p.rtiles;
@@ -124,7 +125,7 @@ struct Shares {
 struct ShareLds {  // of every sequence
   uint32_t before[kMaxShared];  // steps before its units
   uint32_t steps[kMaxShared];   // steps of each of them
-  int32_t len[kMaxShared], q0[kMaxShared], nq[kMaxShared];
+  int32_t len[kMaxShared], q0[kMaxShared], nq[kMaxShared], all[kMaxShared];
 };
 __device__ __forceinline__ Shares scan_shares(const KvAttnArgs& a, uint32_t wgs, int HG, int row_tile, int step, int lane,
                                               ShareLds* lds) {
@@ -133,12 +134,13 @@ __device__ __forceinline__ Shares scan_shares(const KvAttnArgs& a, uint32_t wgs,
   for (int w = 0; w < a.B; w += 64) {
     const int b = w + lane;
     uint32_t cost = 0, steps = 1;
-    int q0 = 0, nq = 0, len = 0;
+    Queries qs{0, 0, 0};
+    int len = 0;
     if (b < a.B) {
-      nq = queries_of(a, b, &q0);
+      qs = queries_of(a, b);
       len = length_of(a, b);
       steps = steps_of(len, step);
-      cost = units_of(nq, G, HG, row_tile) * steps;
+      cost = units_of(qs.n, G, HG, row_tile) * steps;
     }
     uint32_t run = cost;
 #pragma unroll
@@ -149,8 +151,9 @@ __device__ __forceinline__ Shares scan_shares(const KvAttnArgs& a, uint32_t wgs,
     lds->before[b] = total + run - cost;
     lds->steps[b] = steps;
     lds->len[b] = len;
-    lds->q0[b] = q0;
-    lds->nq[b] = nq;
+    lds->q0[b] = qs.q0;
+    lds->nq[b] = qs.n;
+    lds->all[b] = qs.all;
     total += (uint32_t)__builtin_amdgcn_readlane((int)run, 63);
   }
   Shares s;
@@ -270,12 +273,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
         const uint64_t le = __ballot(w + lane < a.B && shares->before[w + lane] <= at);
         if (le) b = w + 63 - __builtin_clzll(le);
       }
-      const uint32_t before = __builtin_amdgcn_readfirstlane(shares->before[b]);
+      const uint32_t first = __builtin_amdgcn_readfirstlane(shares->before[b]);
       steps = __builtin_amdgcn_readfirstlane(shares->steps[b]);
-      const uint32_t unit = (at - before) / steps;
+      const uint32_t unit = (at - first) / steps;
       rt = (int)(unit / (uint32_t)HG);
       hg = (int)(unit - (uint32_t)rt * HG);
-      u0 = before + unit * steps;
+      u0 = first + unit * steps;
       s0 = (int)(at - u0);
       s1 = (int)min(steps, (uint32_t)s0 + (at_end - at));
       at += s1 - s0;
@@ -286,14 +289,18 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
       rt = (int)(x - (uint32_t)b * rtiles);
       at = 1;
     }
-    int q0, nq, len;
+    int q0, nq, before, len;  // before: the first query sees tokens 0..before
     if (flat) {
       q0 = __builtin_amdgcn_readfirstlane(shares->q0[b]);
       nq = __builtin_amdgcn_readfirstlane(shares->nq[b]);
       len = __builtin_amdgcn_readfirstlane(shares->len[b]);
+      before = len - __builtin_amdgcn_readfirstlane(shares->all[b]);
     } else {
-      nq = queries_of(a, b, &q0);
+      const Queries qs = queries_of(a, b);
+      q0 = qs.q0;
+      nq = qs.n;
       len = length_of(a, b);
+      before = len - qs.all;
       s1 = (int)(steps = steps_of(len, kStep));
     }
     const bool whole = s0 == 0 && s1 == (int)steps;
@@ -303,8 +310,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
     // of these rows' tokens: what the last row sees ends the walk, what the first
     // sees ends the tiles that need no mask
     const int t_begin = s0 * kStep;
-    const int t_end = min((int)min((int64_t)s1 * kStep, (int64_t)len), len - nq + (int)((uint32_t)row1 / (uint32_t)G) + 1);
-    const int low = min(t_end, len - nq + (int)((uint32_t)row0 / (uint32_t)G) + 1);
+    const int t_end =
+        min((int)min((int64_t)s1 * kStep, (int64_t)len), before + (int)((uint32_t)row1 / (uint32_t)G) + 1);
+    const int low = min(t_end, before + (int)((uint32_t)row0 / (uint32_t)G) + 1);
 
     const uint32_t blk = (uint32_t)hg * HP * D / 128;  // first block of the wave's heads
     const int32_t* table = a.table + (int64_t)b * a.table_width;
@@ -331,7 +339,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
       asm volatile("" : "+v"(off));
 #pragma unroll
       for (int i = 0; i < T::KL; ++i) {
-        const uint8_t* p = from + (int64_t)(P32 ? row + T::kTok * i : __shfl(row, T::kTok * i + lane / T::kChunks)) * rowb;
+        const int at_row = P32 ? row + T::kTok * i : __shfl(row, T::kTok * i + lane / T::kChunks);
+        const uint8_t* p = from + (int64_t)at_row * rowb;
         if constexpr (P32) asm volatile("" : "+s"(p));
         to[i] = *reinterpret_cast<const u4*>(p + off);
       }
@@ -364,7 +373,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
       const int t = x % RT;
       const uint32_t qrow = min(row0 + 16 * t + r % PR, rows - 1);  // rows past the end repeat the last, not stored
       const uint32_t qi = qrow / (uint32_t)G;
-      lim[t] = min(t_end, len - nq + (int)qi + 1);
+      lim[t] = min(t_end, before + (int)qi + 1);
       const int head = (hg * HP + x / RT) * G + (int)(qrow - qi * G);
       const uint16_t* qp = a.q + (int64_t)(q0 + qi) * a.q_stride + (int64_t)head * D;
       u4 raw[NS];
@@ -448,7 +457,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
             const int t16 = 16 * g + r, blkn = D == 64 ? p / 2 : p + n;
             uint32_t kw[NS / NH];
             if constexpr (D == 64) {
-              const u2 w = reinterpret_cast<const u2*>(kd + t16 * T::kChunks + k_place<T::kChunks>(t16, 2 * p + c / 2))[c % 2];
+              const u4* at16 = kd + t16 * T::kChunks + k_place<T::kChunks>(t16, 2 * p + c / 2);
+              const u2 w = reinterpret_cast<const u2*>(at16)[c % 2];
               kw[0] = w[0];
               kw[1] = w[1];
             } else {
@@ -559,7 +569,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
               // 64 channels: lane m gets their half word m (four channels, every second
               // of eight) of its eight tokens, in pairs
               const int h = 2 * (n + p * NH) + j, q64 = D == 64 ? p : h, t4 = 4 * c + r / 4;
-              const u2* at64 = reinterpret_cast<const u2*>(vd + t4 * T::kChunks + v_place<T::kChunks>(t4, 2 * q64 + r % 4 / 2)) + r % 2;
+              const u4* at16 = vd + t4 * T::kChunks + v_place<T::kChunks>(t4, 2 * q64 + r % 4 / 2);
+              const u2* at64 = reinterpret_cast<const u2*>(at16) + r % 2;
               const u2 y0 = read_transposed(at64), y1 = read_transposed(at64 + 2 * 16 * T::kChunks);
               const uint32_t yw[4] = {y0[0], y0[1], y1[0], y1[1]};
               u4 d[4];

@@ -57,13 +57,12 @@ __global__ __launch_bounds__(64 * kChunkWaves, 2) void kv_chunk_kernel(KvAttnArg
   const uint32_t x = blockIdx.x / (uint32_t)a.Hkv;
   const int kvh = (int)(blockIdx.x - x * a.Hkv);
   const int b = (int)(x / (uint32_t)rtiles), rt = (int)(x - (uint32_t)b * rtiles);
-  int q0;
-  const int nq = queries_of(a, b, &q0), len = length_of(a, b);
-  const int rows = nq * G, row0 = rt * (32 * kChunkWaves);
+  const Queries qs = queries_of(a, b);
+  const int q0 = qs.q0, len = length_of(a, b);
+  const int rows = qs.n * G, row0 = rt * (32 * kChunkWaves);
   if (row0 >= rows) return;
   const int row1 = min(row0 + 32 * kChunkWaves, rows) - 1;
-  // query i sees tokens below len - nq + i + 1
-  const int before = len - nq + 1;
+  const int before = len - qs.all + 1;  // query i sees tokens below before + i
   const int t_end = min(len, before + (int)((uint32_t)row1 / (uint32_t)G));
   const int tiles = t_end > 0 ? (t_end + kTok - 1) / kTok : 0;
   const int wrow = min(row0 + 32 * wave, row1);
