@@ -53,7 +53,6 @@ namespace {
 
 constexpr int kShares = 512;     // workgroups that steps are shared out to
 constexpr int kMaxShared = 256;  // sequences that a wave scans for its share
-constexpr int kMinSteps = 4;     // steps of a unit that is worth sharing out
 constexpr int kMeta = 160;       // words of a wave's scales and zero-points of a tile and block
 
 constexpr int kWaves = 4;
@@ -80,27 +79,36 @@ KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_q
   p.urows = 16 * p.RT;
   p.grid = (int64_t)B * Hkv * p.rtiles;
   p.flat = false;
-  // tiles of 128 rows once two workgroups a CU come of it (one a CU: 510 us where
-  // the kernel of 32 rows takes 455) and nearly all of their rows are used
+  // Tiles of 128 rows once two workgroups a CU come of it (512 tokens over 16K of one
+  // sequence, one a CU: 510 us, 455 with tiles of 32 rows; of two sequences 585 and
+  // 789) and nearly all of their rows are used (64 sequences, 128 rows a head: 97 us
+  // and 133; 72 rows: 91 and 75).  D = 256: 660 us and 588, no registers.
   p.chunk = D != 256 && p.grid >= kShares && 5 * ((rows + 31) / 32) >= 16 * p.rtiles;
   if (p.chunk) return p;
-  // more than 16 rows: two tiles share the decoded codes (D = 256: no registers for them)
+  // more than 16 rows: two tiles share the decoded codes (4 contexts of up to 4K
+  // with 32 rows: 29 us, 32 with one; D = 256 has no registers for them)
   p.RT = rows <= 16 || D == 256 ? 1 : 2;
   p.rtiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
   p.urows = (int)(rows < 16 * p.RT ? rows : 16 * p.RT);
   const int64_t steps = (max_context + 32 * kWaves - 1) / (32 * kWaves);
-  // whole 128-byte lines to a wave (two heads of 128; four of 64, if their rows fit
-  // a tile together) once that fills the GPU (below, twice the waves count more)
+  // Whole 128-byte lines to a wave (two heads of 128; four of 64, if their rows fit
+  // a tile together) once there is work for all CUs that way: 64 contexts of up to
+  // 512 tokens 15.7 us, 16.7 without; of up to 8K 109 and 152; 32 of up to 4K (4096
+  // steps) 40 and 47.  Below, twice the workgroups count more: 32 of up to 2K 32 us
+  // and 28 without.
   p.HP = D == 64 ? 2 : 1;
   const int line = 256 / D;
-  if (p.RT == 1 && (D == 128 || rows <= 4) && Hkv % line == 0 &&
-      (int64_t)B * (Hkv / line) * p.rtiles * steps >= 2 * kShares)
-    p.HP = line;
+  const int64_t full = (int64_t)B * (Hkv / line) * p.rtiles;
+  if (p.RT == 1 && (D == 128 || rows <= 4) && Hkv % line == 0 && (full >= 256 || full * steps >= 4096)) p.HP = line;
   p.PK = rows * p.HP <= 16 ? p.HP : 1;
   const int64_t units = (int64_t)B * (Hkv / p.HP) * p.rtiles;
-  // two workgroups a CU
+  // Shares cost a joining kernel and a start for each unit that a workgroup takes
+  // part in; what they win grows with the steps (units x steps, whole and shared:
+  // 8 x 4 9.1 and 11.0 us, 8 x 8 13.2 and 11.1, 8 x 64 69 and 14; 128 x 8 13.6 and
+  // 18.8, 128 x 16 37 and 32; 256 x 16 39 and 43, 256 x 32 67 and 58, 256 x 64 154 and
+  // 110; 800 x 16 98 and 108).  Two workgroups a CU.
   const int64_t n = units * steps < kShares ? units * steps : kShares;
-  p.flat = units < 2 * kShares && steps >= kMinSteps && B <= kMaxShared &&
+  p.flat = units < 2 * kShares && steps >= 8 && 2 * units <= steps * steps && B <= kMaxShared &&
            units * steps < (int64_t)1 << 31;  // steps are counted in 32 bits
   p.grid = p.flat ? n : units;
   return p;
@@ -789,7 +797,8 @@ hipError_t launch_main(const KvAttnArgs& a, const KvPlan& p, hipStream_t stream)
   kv_attn_kernel<D, HP, RT, PK, P32><<<(unsigned)p.grid, 64 * kWaves, lds, stream>>>(a, p.rtiles, p.urows, p.flat);
   if (!p.flat) return hipGetLastError();
   const int64_t rows = (int64_t)a.B * a.max_queries * a.Hq, units = (int64_t)a.B * (a.Hkv / HP) * p.rtiles;
-  // many pieces to a row: four waves share them
+  // many pieces to a row: four waves share them (131072 tokens 42 us, 49 with one;
+  // 64 contexts of up to 8K 119 us, 110 with one)
   if (p.grid > 8 * units)
     kv_attn_join_kernel<D, HP, RT, 4><<<(unsigned)rows, 256, 0, stream>>>(a, p.urows, (uint32_t)p.grid, rows);
   else

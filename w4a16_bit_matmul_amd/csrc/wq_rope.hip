@@ -13,7 +13,9 @@
 // pairs: in the half form values 4l..4l+3 and their partners rot/2 further on
 // (two 8-byte loads), in the interleaved form eight neighbours (one 16-byte
 // load), so the rotation needs no exchange between lanes and the sum of squares
-// is one xor-shuffle tree over the D/8 lanes of the row.
+// is one xor-shuffle tree over the D/8 lanes of the row.  A prompt of 32768 tokens
+// (64 + 8 heads of 128) moves 1.2 GB in 257-270 us, 4.6 TB/s where a large copy
+// reaches 5.0; a decode step of 64 tokens takes 3.0 us, the latency of one row.
 #include "wq_device.h"
 #include "wq_kernels.h"
 
@@ -144,8 +146,9 @@ template <int DT, bool INTER, int LPH>
 hipError_t launch_lph(const QkNormRopeArgs& a, hipStream_t stream) {
   const int64_t rows = a.T * (a.Hq + a.Hkv);
   constexpr int RPB = 256 / LPH;
-  // four rows a lane once that still leaves two thousand workgroups; one below,
-  // where the time is the latency of a row
+  // four rows a lane once that still leaves two thousand workgroups (32768 tokens of
+  // 72 heads: 269 us, 294 with one); one below, where the time is the latency of a
+  // row (64 tokens: 3.0 us, 5.7 with four)
   if (rows >= (int64_t)2048 * RPB * 4)
     qk_norm_rope_kernel<DT, INTER, LPH, 4><<<(unsigned)((rows + 4 * RPB - 1) / (4 * RPB)), 256, 0, stream>>>(a);
   else
