@@ -8,6 +8,7 @@ namespace wq {
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef float f16v __attribute__((ext_vector_type(16)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 
 constexpr float kNegInf = -__builtin_inff();
 // A row's reference point may lag its largest weight by this many powers of two
@@ -46,10 +47,19 @@ __device__ __forceinline__ int length_of(const KvAttnArgs& a, int b) {
   return (int)max((int64_t)0, min((int64_t)a.lens[b], a.max_context));
 }
 
+// fp32 pair -> 16-bit pair, round to nearest even
+template <bool BF>
+__device__ __forceinline__ uint32_t pack_pair(float x, float y) {
+  if constexpr (BF) {
+    const b2 v = {(__bf16)x, (__bf16)y};
+    return __builtin_bit_cast(uint32_t, v);
+  } else {
+    const h2 v = {(_Float16)x, (_Float16)y};
+    return as_u32(v);
+  }
+}
 __device__ __forceinline__ uint32_t pack_out(int dtype, float x, float y) {
-  const uint32_t lo = dtype == 1 ? f32_to_bf16_bits(x) : f32_to_f16_bits(x);
-  const uint32_t hi = dtype == 1 ? f32_to_bf16_bits(y) : f32_to_f16_bits(y);
-  return lo | (hi << 16);
+  return dtype == 1 ? pack_pair<true>(x, y) : pack_pair<false>(x, y);
 }
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.0f ? kNegInf : (m + __builtin_log2f(l)) * 0.6931471805599453f;

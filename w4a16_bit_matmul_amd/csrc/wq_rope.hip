@@ -14,15 +14,14 @@
 // (two 8-byte loads), in the interleaved form eight neighbours (one 16-byte
 // load), so the rotation needs no exchange between lanes and the sum of squares
 // is one xor-shuffle tree over the D/8 lanes of the row.  A prompt of 32768 tokens
-// (64 + 8 heads of 128) moves 1.2 GB in 257-270 us, 4.6 TB/s where a large copy
-// reaches 5.0; a decode step of 64 tokens takes 3.0 us, the latency of one row.
-#include "wq_device.h"
-#include "wq_kernels.h"
+// (64 + 8 heads of 128) moves 1.2 GB in 247 us, the rate of a large copy
+// (5.0 TB/s); with 64-bit row numbers and outputs rounded in integer arithmetic the
+// vector instructions took all of the cycles (268 us).  A decode step of 64 tokens
+// takes 2.7 us, the latency of one row.
+#include "wq_attn.h"
 
 namespace wq {
 namespace {
-
-typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 template <int DT>
 __device__ __forceinline__ void unpack4(u2 w, float (&v)[4]) {
@@ -43,11 +42,7 @@ template <int DT>
 __device__ __forceinline__ u2 pack4(const float (&v)[4]) {
   u2 w;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t a = DT == 1 ? f32_to_bf16_bits(v[2 * i]) : f32_to_f16_bits(v[2 * i]);
-    const uint32_t b = DT == 1 ? f32_to_bf16_bits(v[2 * i + 1]) : f32_to_f16_bits(v[2 * i + 1]);
-    w[i] = a | (b << 16);
-  }
+  for (int i = 0; i < 2; ++i) w[i] = pack_pair<DT == 1>(v[2 * i], v[2 * i + 1]);
   return w;
 }
 
@@ -72,20 +67,20 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRopeArgs a) {
     ca = a.rot + (p0 - half);
     cb = ca + (D - a.rot) / 2;
   }
-  const int64_t rows = a.T * H;
-  const int64_t r0 = (int64_t)blockIdx.x * (RPB * U) + threadIdx.x / LPH;
+  const uint32_t rows = (uint32_t)(a.T * H);  // below 2^31
+  const uint32_t r0 = blockIdx.x * (RPB * U) + threadIdx.x / LPH;
   u2 xa[U], xb[U];
-  int64_t pos[U];
-  int64_t tok[U];
+  int pos[U];
+  uint32_t tok[U];
   int head[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t r = min(r0 + u * RPB, rows - 1);  // past the end: a real row, not stored
-    tok[u] = r / H;
+    const uint32_t r = min(r0 + u * RPB, rows - 1);  // past the end: a real row, not stored
+    tok[u] = r / (uint32_t)H;
     head[u] = (int)(r - tok[u] * H);
     const bool isq = head[u] < a.Hq;
-    const uint16_t* x = isq ? a.q + tok[u] * a.q_stride + (int64_t)head[u] * D
-                            : a.k + tok[u] * a.k_stride + (int64_t)(head[u] - a.Hq) * D;
+    const uint16_t* x = isq ? a.q + (int64_t)tok[u] * a.q_stride + (int64_t)head[u] * D
+                            : a.k + (int64_t)tok[u] * a.k_stride + (int64_t)(head[u] - a.Hq) * D;
     xa[u] = *reinterpret_cast<const u2*>(x + ca);
     xb[u] = *reinterpret_cast<const u2*>(x + cb);
     pos[u] = a.positions[tok[u]];
@@ -122,7 +117,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRopeArgs a) {
     }
     const bool in_table = pos[u] >= 0 && pos[u] < a.P;
     if (turned) {
-      const int64_t at = (in_table ? pos[u] : 0) * half + p0;
+      const int64_t at = (int64_t)(in_table ? pos[u] : 0) * half + p0;
       const f4 c = *reinterpret_cast<const f4*>(a.cos + at), s = *reinterpret_cast<const f4*>(a.sin + at);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -133,8 +128,8 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRopeArgs a) {
       }
     }
     if (r0 + u * RPB < rows && in_table) {
-      uint16_t* o = isq ? a.q_out + tok[u] * a.qo_stride + (int64_t)head[u] * D
-                        : a.k_out + tok[u] * a.ko_stride + (int64_t)(head[u] - a.Hq) * D;
+      uint16_t* o = isq ? a.q_out + (int64_t)tok[u] * a.qo_stride + (int64_t)head[u] * D
+                        : a.k_out + (int64_t)tok[u] * a.ko_stride + (int64_t)(head[u] - a.Hq) * D;
       const float oa[4] = {v[0], v[1], v[2], v[3]}, ob[4] = {v[4], v[5], v[6], v[7]};
       *reinterpret_cast<u2*>(o + ca) = pack4<DT>(oa);
       *reinterpret_cast<u2*>(o + cb) = pack4<DT>(ob);
@@ -147,8 +142,8 @@ hipError_t launch_lph(const QkNormRopeArgs& a, hipStream_t stream) {
   const int64_t rows = a.T * (a.Hq + a.Hkv);
   constexpr int RPB = 256 / LPH;
   // four rows a lane once that still leaves two thousand workgroups (32768 tokens of
-  // 72 heads: 269 us, 294 with one); one below, where the time is the latency of a
-  // row (64 tokens: 3.0 us, 5.7 with four)
+  // 72 heads: 247 us, 265 with one); one below, where the time is the latency of a
+  // row (64 tokens: 2.7 us, 4.6 with four)
   if (rows >= (int64_t)2048 * RPB * 4)
     qk_norm_rope_kernel<DT, INTER, LPH, 4><<<(unsigned)((rows + 4 * RPB - 1) / (4 * RPB)), 256, 0, stream>>>(a);
   else
