@@ -27,7 +27,7 @@
 // stored, to the rows that do see it.
 //
 // Bound by the matrix cores for long prompts: 8K tokens with 64 / 8 heads of 128 in
-// 1.09 ms, 1,006 TFLOP/s (a library product of bf16 reaches 1,415), matrix
+// 1.1 ms, 1,000 TFLOP/s (a library product of bf16 reaches 1,415), matrix
 // instructions half of the cycles and the softmax a third; with heads of 64 the
 // softmax comes first (16 prompts of up to 1500: 66 us, 559 TFLOP/s); short prompts
 // are bound by the latency of a workgroup's start (48 of up to 300 tokens: 83 us,
