@@ -664,10 +664,11 @@ def wq_kv_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, block_t
     sequence, or those of sequence b at q_starts[b] .. q_starts[b+1] - 1 (int32
     [B+1]; they are its last tokens, and see the tokens up to their own).
     max_context and max_queries bound the lengths for the launch and pick the
-    kernel (defaults: the table's width, all T; tighter bounds are faster).  scale defaults to 1/sqrt(D).  Queries that see nothing
-    give zeros; rows outside every sequence are not written.  Returns out
-    [T][Hq][D], or (out, lse) with lse=True or an fp32 [T][Hq] tensor.  Without a
-    workspace, each call that needs one allocates it on its stream."""
+    kernel (defaults: the table's width, all T; tighter bounds are faster).  scale
+    defaults to 1/sqrt(D).  Queries that see nothing give zeros; rows outside every
+    sequence are not written.  Returns out [T][Hq][D], or (out, lse) with lse=True
+    or an fp32 [T][Hq] tensor.  Without a workspace, each call that needs one
+    allocates it on its stream."""
     qs = _heads("q", q)
     T, Hq, D = q.shape
     S, hd = k_cache.S, k_cache.hd
