@@ -423,6 +423,7 @@ def test_cache_attention_computes_the_first_max_queries(B, nq, most, room):
 
 @pytest.mark.parametrize("page", [16, 64])
 @pytest.mark.parametrize("Hq,Hkv,D,nq,plan", [
+    (64, 8, 64, 1, "HP=4, RT=1, PK=2"), (12, 4, 64, 2, "HP=4, RT=1, PK=2"),
     (16, 8, 64, 1, "HP=4, RT=1, PK=4"), (8, 8, 64, 4, "HP=4, RT=1, PK=4"), (14, 2, 64, 1, "HP=2, RT=1, PK=2"), (40, 8, 64, 2, "HP=2, RT=1, PK=1"),
     (48, 8, 64, 3, "HP=2, RT=2, PK=1"), (64, 8, 128, 1, "HP=2, RT=1, PK=2"), (12, 4, 128, 2, "HP=2, RT=1, PK=2"), (18, 2, 128, 1, "HP=2, RT=1, PK=1"),
     (15, 5, 128, 5, "HP=1, RT=1, PK=1"), (24, 8, 128, 7, "HP=1, RT=2, PK=1"), (40, 4, 256, 3, "HP=1, RT=1, PK=1")])

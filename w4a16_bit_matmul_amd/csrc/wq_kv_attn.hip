@@ -94,16 +94,16 @@ KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_q
   p.rtiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
   p.urows = (int)(rows < 16 * p.RT ? rows : 16 * p.RT);
   const int64_t steps = (max_context + 32 * kWaves - 1) / (32 * kWaves);
-  // Whole 128-byte lines to a wave (two heads of 128; four of 64, if their rows fit
-  // a tile together) once there is work for all CUs that way: 64 contexts of up to
-  // 512 tokens 15.7 us, 16.7 without; of up to 8K 109 and 152; 32 of up to 4K (4096
-  // steps) 40 and 47.  Below, twice the workgroups count more: 32 of up to 2K 32 us
-  // and 28 without.
+  // Whole 128-byte lines to a wave (two heads of 128; four of 64 if two of them share
+  // a tile, for registers) once there is work for all CUs that way: 64 contexts of up
+  // to 512 tokens 15.7 us, 16.7 without; of up to 8K 109 and 152, with heads of 64 in
+  // groups of eight 65 and 75; 32 of up to 4K (4096 steps) 40 and 47.  Below, twice
+  // the workgroups count more: 32 of up to 2K 32 us and 28 without.
   p.HP = D == 64 ? 2 : 1;
   const int line = 256 / D;
   const int64_t full = (int64_t)B * (Hkv / line) * p.rtiles;
-  if (p.RT == 1 && (D == 128 || rows <= 4) && Hkv % line == 0 && (full >= 256 || full * steps >= 4096)) p.HP = line;
-  p.PK = rows * p.HP <= 16 ? p.HP : 1;
+  if (p.RT == 1 && (D == 128 || rows <= 8) && Hkv % line == 0 && (full >= 256 || full * steps >= 4096)) p.HP = line;
+  while (2 * p.PK <= p.HP && 2 * p.PK * rows <= 16) p.PK *= 2;
   const int64_t units = (int64_t)B * (Hkv / p.HP) * p.rtiles;
   // Shares cost a joining kernel and a start for each unit that a workgroup takes
   // part in; what they win grows with the steps (units x steps, whole and shared:
@@ -458,45 +458,45 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
       __builtin_amdgcn_sched_barrier(0);
       load(tile, next);
       tile.ok = next_ok;
-      f4 sc[X][2][NH];
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int p = 0; p < HP; ++p)
-#pragma unroll
-          for (int n = 0; n < NH; ++n) {
-            const int t16 = 16 * g + r, blkn = D == 64 ? p / 2 : p + n;
-            uint32_t kw[NS / NH];
-            if constexpr (D == 64) {
-              const u4* at16 = kd + t16 * T::kChunks + k_place<T::kChunks>(t16, 2 * p + c / 2);
-              const u2 w = reinterpret_cast<const u2*>(at16)[c % 2];
-              kw[0] = w[0];
-              kw[1] = w[1];
-            } else {
-              const u4 w = kd[t16 * T::kChunks + k_place<T::kChunks>(t16, 4 * (p + n) + c)];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) kw[j] = w[j];
-            }
-            const u2 z = *reinterpret_cast<const u2*>(meta + kMeta * blkn + 64 + 2 * t16);
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-              if (p % PK == 0) sc[p / PK * RT + t][g][n] = f4{0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < NS / NH; ++j) {
-              const u4 d = code_pairs(kw[j], z[0], z[1], magic);
-#pragma unroll
-              for (int t = 0; t < RT; ++t)
-                sc[p / PK * RT + t][g][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    __builtin_bit_cast(h8, d), qf[p * RT + t][NS / NH * n + j], sc[p / PK * RT + t][g][n], 0, 0, 0);
-            }
-          }
-      // heads (those that share a tile together) in turn: softmax of their row tiles,
-      // then O^T += V^T P^T
+      // heads (those that share a tile together) in turn: scores, softmax of their row
+      // tiles, then O^T += V^T P^T
 #pragma unroll
       for (int hp = 0; hp < HP / PK; ++hp) {
-        const float* mh = meta + kMeta * (D == 64 ? (hp * PK + sub) / 2 : hp * PK + sub);
-        float v_exp = v_top[D == 64 ? hp * PK / 2 : hp * PK].exp;
-        if (PK > 1 && NB > 1 && sub >= PK / 2) v_exp = v_top[NB - 1].exp;
+        f4 sc[RT][2][NH];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int y = 0; y < PK; ++y)
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+              const int p = hp * PK + y, t16 = 16 * g + r, blkn = D == 64 ? p / 2 : p + n;
+              uint32_t kw[NS / NH];
+              if constexpr (D == 64) {
+                const u4* at16 = kd + t16 * T::kChunks + k_place<T::kChunks>(t16, 2 * p + c / 2);
+                const u2 w = reinterpret_cast<const u2*>(at16)[c % 2];
+                kw[0] = w[0];
+                kw[1] = w[1];
+              } else {
+                const u4 w = kd[t16 * T::kChunks + k_place<T::kChunks>(t16, 4 * (p + n) + c)];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) kw[j] = w[j];
+              }
+              const u2 z = *reinterpret_cast<const u2*>(meta + kMeta * blkn + 64 + 2 * t16);
+#pragma unroll
+              for (int t = 0; t < RT; ++t)
+                if (y == 0) sc[t][g][n] = f4{0, 0, 0, 0};
+#pragma unroll
+              for (int j = 0; j < NS / NH; ++j) {
+                const u4 d = code_pairs(kw[j], z[0], z[1], magic);
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                  sc[t][g][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                      __builtin_bit_cast(h8, d), qf[p * RT + t][NS / NH * n + j], sc[t][g][n], 0, 0, 0);
+              }
+            }
+        const int hb = D == 64 ? (hp * PK + sub) / 2 : hp * PK + sub;  // (first) block of the lane's head
+        const float* mh = meta + kMeta * hb;
+        const float v_exp = NB > NH && hb > 0 ? v_top[NB / NH - 1].exp : v_top[0].exp;
         h8 pf[RT][NH];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
@@ -511,7 +511,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 float& v = s8[4 * g + i];
-                v = n == 0 ? sc[x][g][n][i] * ks[i] : __builtin_fmaf(sc[x][g][n][i], ks[i], v);
+                v = n == 0 ? sc[t][g][n][i] * ks[i] : __builtin_fmaf(sc[t][g][n][i], ks[i], v);
               }
             }
           if (masked) {
@@ -841,7 +841,7 @@ hipError_t launch_kv_attn(const KvAttnArgs& a, hipStream_t stream) {
     return p.PK == 2 ? launch_p<128, 2, 1, 2>(a, p, stream) : launch_p<128, 2, 1, 1>(a, p, stream);
   }
   if (p.RT == 2) return launch_p<64, 2, 2, 1>(a, p, stream);
-  if (p.HP == 4) return launch_p<64, 4, 1, 4>(a, p, stream);
+  if (p.HP == 4) return p.PK == 4 ? launch_p<64, 4, 1, 4>(a, p, stream) : launch_p<64, 4, 1, 2>(a, p, stream);
   return p.PK == 2 ? launch_p<64, 2, 1, 2>(a, p, stream) : launch_p<64, 2, 1, 1>(a, p, stream);
 }
 
