@@ -177,5 +177,8 @@ def test_binding_rejects_before_any_call():
         wq.wq_kv_attention(x, c, c, tb, i, page_size=4)
     with pytest.raises(ValueError, match="caches"):
         wq.wq_kv_attention(torch.zeros((2, 4, 100), dtype=torch.float16), c, c, tb, i[:2], page_size=4)
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8, device="meta"), torch.empty((1 << 10, 2), dtype=torch.uint8)[:, 0]):
+        with pytest.raises(ValueError, match="workspace"):
+            wq.wq_kv_attention(x, c, c, tb, i[:2], page_size=4, workspace=ws)
     with pytest.raises(ValueError, match="q_starts"):
         wq.wq_kv_attention(x, c, c, tb, i[:2], page_size=4, q_starts=i[:2])

@@ -693,6 +693,8 @@ def wq_kv_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, block_t
         starts, max_queries = None, min(T, 1)
     if max_context is None:
         max_context = width * page_size
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     L = _lib or lib()
     with _on(dev, stream) as s:
         out, lse = _attn_out(q, out, lse)
