@@ -212,6 +212,27 @@ def test_prompt_attention_later_tokens_do_not_reach_back(dtype, bad):
         assert bool((torch.isnan(x) if math.isnan(bad) else (x == bad) | torch.isnan(x)).all()), (t, x)
 
 
+@pytest.mark.parametrize("D,n", [(64, 333), (128, 530), (256, 170)])
+@pytest.mark.parametrize("bad", [NAN, math.inf])
+def test_prompt_attention_values_that_are_no_numbers_in_longer_prompts(D, n, bad):
+    """The same where a row walks many tiles (a prompt of 512 tokens or more with
+    heads of 128 takes larger ones): bad values in a tile that all rows see, in one
+    that some see, in the last token."""
+    Hq, Hkv = 4, 2
+    q, k, v = (ref.values(90 + i, (n, h, D), BF) for i, h in enumerate((Hq, Hkv, Hkv)))
+    out, bound = _prompt_want(q, k, v, [0, n], D ** -0.5)[:2]
+    at = n // 2
+    v[at, 1, 5], v[n - 1, 0, D - 1] = bad, bad
+    got = _run_prompt(q.cuda(), k.cuda(), v.cuda(), [0, n])[0].cpu()
+    ref.check(got[:at], out[:at], bound[:at], "before")
+    ref.check(got[at:n - 1, :2], out[at:n - 1, :2], bound[at:n - 1, :2], "other heads")
+    keep = torch.ones(D, dtype=torch.bool)
+    keep[5] = False
+    ref.check(got[at:, 2:, keep], out[at:, 2:, keep], bound[at:, 2:, keep], "other channels")
+    for x in (got[at:, 2:, 5], got[n - 1, :2, D - 1]):
+        assert bool((torch.isnan(x) | (x == bad)).all())
+
+
 # ---- attention over the cache ------------------------------------------------------
 
 class Cache:
