@@ -11,7 +11,7 @@ from w4a16_bit_matmul_amd import _build
 
 @pytest.mark.skipif(not os.path.exists(_build.HIPCC), reason="hipcc is not installed")
 @pytest.mark.parametrize("src,kernel,instances", [("wq_kv_attn.hip", "14kv_attn_kernel", 20), ("wq_kv_chunk.hip", "15kv_chunk_kernel", 2),
-                                                  ("wq_prompt_attn.hip", "18prompt_attn_kernel", 8), ("wq_rope.hip", "qk_norm_rope_kernel", 24)])
+                                                  ("wq_prompt_attn.hip", "18prompt_attn_kernel", 8), ("wq_prompt_attn.hip", "19prompt_split_kernel", 4), ("wq_rope.hip", "qk_norm_rope_kernel", 24)])
 def test_attention_kernels_keep_to_their_registers(src, kernel, instances):
     meta = {n: v for n, v in _kernel_metadata(src).items() if kernel in n}
     assert len(meta) == instances, sorted(meta)

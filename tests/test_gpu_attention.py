@@ -212,6 +212,29 @@ def test_prompt_attention_later_tokens_do_not_reach_back(dtype, bad):
         assert bool((torch.isnan(x) if math.isnan(bad) else (x == bad) | torch.isnan(x)).all()), (t, x)
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [([40] * 60 + [0, 1, 129], 16, 8, 64), ([37] * 55 + [200], 6, 6, 128), ([530], 72, 72, 128),
+                                           ([1200], 40, 20, 64), ([512, 700], 66, 33, 128)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_prompt_attention_many_workgroups(lens, Hq, Hkv, D, dtype):
+    """Prompts that fill the GPU, short and long: good values, then one value that
+    is no number in a token that later ones see."""
+    say(f"prompt, many workgroups: {len(lens)} of up to {max(lens)} Hq={Hq} Hkv={Hkv} D={D} {dtype}")
+    starts = [int(x) for x in np.concatenate([[0], np.cumsum(lens)])]
+    T = starts[-1]
+    assert (T * (Hq // Hkv) // 128 + len(lens)) * Hkv >= 256
+    q, k, v = (ref.values(T + i, (T, h, D), dtype, sc) for i, (h, sc) in enumerate(((Hq, 1.0), (Hkv, 1.0), (Hkv, 0.7))))
+    want = _prompt_want(q, k, v, starts, D ** -0.5)
+    got, lse = _run_prompt(q.cuda(), k.cuda(), v.cuda(), starts)
+    _check_rows(got, lse, want)
+    at, end, G = T - lens[-1] // 2, T, Hq // Hkv
+    v[at, 1, 7] = math.inf
+    got = _run_prompt(q.cuda(), k.cuda(), v.cuda(), starts)[0].cpu()
+    hit = torch.zeros((T, Hq, D), dtype=torch.bool)
+    hit[at:end, G:2 * G, 7] = True
+    assert bool((torch.isnan(got[hit]) | torch.isinf(got[hit])).all())
+    ref.check(got[~hit], want[0][~hit], want[1][~hit], "the others")
+
+
 @pytest.mark.parametrize("D,n", [(64, 333), (128, 530), (256, 170)])
 @pytest.mark.parametrize("bad", [NAN, math.inf])
 def test_prompt_attention_values_that_are_no_numbers_in_longer_prompts(D, n, bad):

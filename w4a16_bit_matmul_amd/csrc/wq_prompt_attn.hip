@@ -30,7 +30,7 @@
 // 1.1 ms, 1,000 TFLOP/s (a library product of bf16 reaches 1,415), matrix
 // instructions half of the cycles and the softmax a third; with heads of 64 the
 // softmax comes first (16 prompts of up to 1500: 66 us, 559 TFLOP/s); short prompts
-// are bound by the latency of a workgroup's start (48 of up to 300 tokens: 83 us,
+// are bound by the latency of a workgroup's start (48 of up to 300 tokens: 84 us,
 // 3.2 TB/s).  Two workgroups a CU: while one waits the other works.  128 rows keep
 // four waves in step; 256, or two groups of four waves half a tile apart (one
 // multiplies while the other takes its softmax), measured 1,200 and 1,316 us where
@@ -48,6 +48,7 @@ namespace {
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
 constexpr int kRows = 128;
+constexpr int kSplitRows = 32;
 
 template <bool BF>
 __device__ __forceinline__ f16v mfma32(u4 x, u4 y, f16v c) {
@@ -82,18 +83,37 @@ __device__ __forceinline__ int v_chunk(int t, int j) {
 __device__ __forceinline__ int64_t clamp_start(const int32_t* starts, int b, int64_t T) {
   return min(max((int64_t)starts[b], (int64_t)0), T);
 }
+template <int ROWS>
 __device__ __forceinline__ int find_sequence(const int32_t* starts, int B, int64_t T, int64_t G, int64_t i, int lane) {
   int lo = 0, n = B;
   while (n > 1) {
     const int step = (n + 63) / 64;
     const int b = lo + lane * step;
-    const bool le = lane * step < n && clamp_start(starts, b, T) * G / kRows + b <= i;
+    const bool le = lane * step < n && clamp_start(starts, b, T) * G / ROWS + b <= i;
     const int k = __builtin_popcountll(__ballot(le));
     if (k == 0) return lo;  // the slot lies before the first sequence's
     lo += (k - 1) * step;
     n = min(step, n - (k - 1) * step);
   }
   return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// Infinities and NaNs of the tiles that rows R0..last see only in part: a thread per
+// channel adds them, key by key, to the stored rows that see the key (`any`: the
+// workgroup found one; every row sees keys 0..first).
+template <int D, int KT, bool BF>
+__device__ __forceinline__ void add_odd_values(const PromptAttnArgs& a, const uint16_t* vp, int64_t q0, int kvh, int G,
+                                               int64_t R0, int first, int64_t last, int any) {
+  if (!any || threadIdx.x >= D) return;
+  const int ch = threadIdx.x;
+  for (int64_t t = (int64_t)(first + 1) / KT * KT; t <= last / G; ++t) {
+    const uint32_t v = vp[t * a.v_stride + ch];
+    if (finite_halves<BF>(v) == 0xffffffffu) continue;
+    for (int64_t x = max(t * G, R0); x <= last; ++x) {
+      uint16_t* o = a.out + ((q0 + x / G) * a.Hq + (int64_t)kvh * G + x % G) * D + ch;
+      *o = (uint16_t)pack_pair<BF>(to_f32<BF>(*o) + to_f32<BF>(v), 0.0f);
+    }
+  }
 }
 
 // KT: keys of a tile
@@ -110,7 +130,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_attn_kernel(Prom
   const int G = a.Hq / a.Hkv;
   const int kvh = (int)(blockIdx.x % a.Hkv);
   const int64_t slot = slots - 1 - blockIdx.x / a.Hkv;
-  const int b = find_sequence(a.starts, a.B, a.T, G, slot, lane);
+  const int b = find_sequence<kRows>(a.starts, a.B, a.T, G, slot, lane);
   const int64_t q0 = clamp_start(a.starts, b, a.T);
   const int64_t n = clamp_start(a.starts, b + 1, a.T) - q0;
   const int64_t R0 = (slot - (q0 * G / kRows + b)) * kRows;
@@ -306,19 +326,189 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_attn_kernel(Prom
       if (Rw + rr < n * G) *reinterpret_cast<u4*>(a.out + (q0 * a.Hq + to) * D + 8 * j) = v;
     }
   }
-  // infinities and NaNs of the partly seen tiles: a thread per channel adds them,
-  // key by key, to the stored rows that see the key
-  if (__syncthreads_or(odd != 0) && threadIdx.x < D) {
-    const int ch = threadIdx.x;
-    for (int64_t t = (int64_t)(wg_first + 1) / KT * KT; t <= last / G; ++t) {
-      const uint32_t v = vp[t * a.v_stride + ch];
-      if (finite_halves<BF>(v) == 0xffffffffu) continue;
-      for (int64_t x = max(t * G, R0); x <= last; ++x) {
-        uint16_t* o = a.out + ((q0 + x / G) * a.Hq + (int64_t)kvh * G + x % G) * D + ch;
-        *o = (uint16_t)pack_pair<BF>(to_f32<BF>(*o) + to_f32<BF>(v), 0.0f);
-      }
-    }
+  add_odd_values<D, KT, BF>(a, vp, q0, kvh, G, R0, wg_first, last, __syncthreads_or(odd != 0));
+}
+
+// The same for prompts that give few workgroups: bound by the walk over the keys of
+// the last rows, so a workgroup owns 32 rows, its four waves take every fourth tile of 32 keys each, in LDS of their own, and
+// join at the end (the largest reference point, sums scaled to it, in wave order).
+template <int D, bool BF>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_split_kernel(PromptAttnArgs a, int64_t slots) {
+  constexpr int KT = 32;
+  constexpr int NC = D / 8, NS = D / 16, NB = D / 32;
+  constexpr int LD = KT * NC / 64;  // chunks a lane stages of K, and of V
+  extern __shared__ __attribute__((aligned(16))) u4 tile[];  // [wave][K, V][KT * NC], then [wave][row][D] fp32
+  __shared__ float stat[4][2][kSplitRows];
+  const int lane = threadIdx.x & 63, r = lane & 31, hf = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int G = a.Hq / a.Hkv;
+  const int kvh = (int)(blockIdx.x % a.Hkv);
+  const int64_t slot = slots - 1 - blockIdx.x / a.Hkv;
+  const int b = find_sequence<kSplitRows>(a.starts, a.B, a.T, G, slot, lane);
+  const int64_t q0 = clamp_start(a.starts, b, a.T);
+  const int64_t n = clamp_start(a.starts, b + 1, a.T) - q0;
+  const int64_t R0 = (slot - (q0 * G / kSplitRows + b)) * kSplitRows;
+  if (R0 < 0 || R0 >= n * G) return;
+  const int64_t row = min(R0 + r, n * G - 1);  // past the end: the last row again, not stored
+  const int64_t qi = row / G;
+  const int64_t head = (int64_t)kvh * G + row % G;
+  const int qi32 = (int)qi, first = (int)(R0 / G);  // every row sees keys 0..first
+  const int64_t last = min(R0 + kSplitRows, n * G) - 1;
+  const int tiles = (int)((last / G) / KT) + 1, keys = (int)n;
+
+  u4 qf[NS];
+  {
+    const uint16_t* qp = a.q + (q0 + qi) * a.q_stride + head * D + 8 * hf;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) qf[j] = *reinterpret_cast<const u4*>(qp + 16 * j);
   }
+  const float f = a.scale * 1.4426950408889634f;
+  const uint16_t* kp = a.k + q0 * a.k_stride + (int64_t)kvh * D;
+  const uint16_t* vp = a.v + q0 * a.v_stride + (int64_t)kvh * D;
+  u4* kd = tile + wave * (2 * KT * NC);
+  u4* vd = kd + KT * NC;
+  u4 kreg[LD], vreg[LD];
+  uint32_t odd = 0;
+  auto fetch = [&](int kt) {
+#pragma unroll
+    for (int x = 0; x < LD; ++x) {
+      const int p = 64 * x + lane;
+      const int64_t t = min(kt * KT + p / NC, keys - 1);  // past the sequence: its last key again
+      kreg[x] = *reinterpret_cast<const u4*>(kp + t * a.k_stride + 8 * (p % NC));
+      vreg[x] = *reinterpret_cast<const u4*>(vp + t * a.v_stride + 8 * (p % NC));
+    }
+  };
+  auto stage = [&](int kt) {
+    const bool part = kt * KT + KT - 1 > first;
+#pragma unroll
+    for (int x = 0; x < LD; ++x) {
+      if (part) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t keep = finite_halves<BF>(vreg[x][i]);
+          odd |= ~keep;
+          vreg[x][i] &= keep;
+        }
+      }
+      const int p = 64 * x + lane, t = p / NC, j = p % NC;
+      kd[t * NC + k_chunk<D>(t, j)] = kreg[x];
+      vd[t * NC + v_chunk<D>(t, j)] = vreg[x];
+    }
+  };
+
+  f16v acc[NB];
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+  float m = kNegInf, l = 0.0f;
+  if (wave < tiles) fetch(wave);
+  for (int kt = wave; kt < tiles; kt += 4) {
+    stage(kt);
+    if (kt + 4 < tiles) fetch(kt + 4);
+    f16v s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) s = mfma32<BF>(kd[r * NC + k_chunk<D>(r, 2 * j + hf)], qf[j], s);
+    const int key0 = kt * KT;
+    if (key0 + KT - 1 > first) {
+      const int seen = qi32 - key0 - 4 * hf;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (8 * (i / 4) + i % 4 > seen) s[i] = kNegInf;
+    }
+    float mx = kNegInf;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[i]);
+    mx = max_over_halves(mx) * f;
+    if (__ballot(mx > m + kLag)) {
+      const float mn = fmaxf(m, mx);
+      const float al = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= al;
+#pragma unroll
+      for (int d = 0; d < NB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[d][i] *= al;
+    }
+    const float ms = m == kNegInf ? 0.0f : m;
+    u4 pf[2];
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], f, -ms));
+      const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 1], f, -ms));
+      l += p0 + p1;
+      pf[i / 8][(i % 8) / 2] = pack_pair<BF>(p0, p1);
+    }
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int d = 0; d < NB; ++d) {
+        const int t = 4 * hf + (lane & 15) / 4;
+        const u2* at = reinterpret_cast<const u2*>(vd + 16 * kk * NC) + (lane & 1) +
+                       2 * (t * NC + v_chunk<D>(t, 4 * d + 2 * ((lane >> 4) & 1) + (lane & 3) / 2));
+        const u2 lo = read_transposed(at), hi = read_transposed(at + 2 * 8 * NC);
+        acc[d] = mfma32<BF>(u4{lo[0], lo[1], hi[0], hi[1]}, pf[kk], acc[d]);
+      }
+  }
+  l = sum_over_halves(l);
+  if (hf == 0) {
+    stat[wave][0][r] = m;
+    stat[wave][1][r] = l;
+  }
+  __syncthreads();  // (and the waves are done with their tiles)
+  float top = kNegInf;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) top = fmaxf(top, stat[g][0][r]);
+  // a wave whose sum is 0 saw nothing (a NaN sum stays one)
+  const float k = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+  // fp32 quads of a row turned by the row, so that a quad of all rows spans the banks
+  constexpr int NQ = D / 4;
+  f4* slab = reinterpret_cast<f4*>(kd);
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      slab[r * NQ + ((8 * d + 2 * i + hf) ^ (r & 15))] =
+          f4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]} * k;
+  __syncthreads();
+  for (uint32_t x = threadIdx.x; x < kSplitRows * NC; x += 256) {
+    const uint32_t rr = x / NC, j = x % NC;
+    const int64_t rw = R0 + rr;
+    if (rw >= n * G) continue;
+    float M = kNegInf, L = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) M = fmaxf(M, stat[g][0][rr]);
+    f4 o0 = {0, 0, 0, 0}, o1 = {0, 0, 0, 0};
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float lw = stat[g][1][rr];
+      L += lw == 0.0f ? 0.0f : lw * __builtin_amdgcn_exp2f(stat[g][0][rr] - M);
+      const f4* sl = reinterpret_cast<const f4*>(tile + g * (2 * KT * NC)) + rr * NQ;
+      o0 += sl[(2 * j) ^ (rr & 15)];
+      o1 += sl[(2 * j + 1) ^ (rr & 15)];
+    }
+    const float inv = 1.0f / L;
+    const uint32_t tok = (uint32_t)rw / (uint32_t)G;
+    const int64_t at = (q0 + tok) * a.Hq + (int64_t)kvh * G + ((uint32_t)rw - tok * G);
+    *reinterpret_cast<u4*>(a.out + at * D + 8 * j) =
+        u4{pack_pair<BF>(o0[0] * inv, o0[1] * inv), pack_pair<BF>(o0[2] * inv, o0[3] * inv),
+           pack_pair<BF>(o1[0] * inv, o1[1] * inv), pack_pair<BF>(o1[2] * inv, o1[3] * inv)};
+    if (a.lse && j == 0) a.lse[at] = (M + __builtin_log2f(L)) * 0.6931471805599453f;
+  }
+  add_odd_values<D, KT, BF>(a, vp, q0, kvh, G, R0, first, last, __syncthreads_or(odd != 0));
+}
+
+template <int D, bool BF>
+hipError_t launch_split(const PromptAttnArgs& a, hipStream_t stream) {
+  static std::atomic<uint64_t> raised{0};
+  constexpr size_t lds = (size_t)4 * 2 * 32 * D * 2;
+  const hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&prompt_split_kernel<D, BF>), lds, raised);
+  if (e != hipSuccess) return e;
+  const int64_t slots = a.T * (a.Hq / a.Hkv) / kSplitRows + a.B;
+  prompt_split_kernel<D, BF><<<(unsigned)(slots * a.Hkv), 256, lds, stream>>>(a, slots);
+  return hipGetLastError();
 }
 
 template <int D, int KT, bool BF>
@@ -334,6 +524,12 @@ hipError_t launch_one(const PromptAttnArgs& a, hipStream_t stream) {
 
 template <int D, int KT>
 hipError_t launch_d(const PromptAttnArgs& a, hipStream_t stream) {
+  // fewer workgroups than half the CUs: one prompt of 500 / 1000 / 2000 tokens with
+  // 8 / 1 heads of 128 10.3 / 15.1 / 28.5 us, 16.1 / 25.3 / 44.5 with 128 rows; with
+  // 182 workgroups (four of 700) 22.9 and 20.0.  D = 256 has no registers for it.
+  if constexpr (D != 256)
+    if ((a.T * (a.Hq / a.Hkv) / kRows + a.B) * a.Hkv < 128)
+      return a.dtype == 1 ? launch_split<D, true>(a, stream) : launch_split<D, false>(a, stream);
   return a.dtype == 1 ? launch_one<D, KT, true>(a, stream) : launch_one<D, KT, false>(a, stream);
 }
 
