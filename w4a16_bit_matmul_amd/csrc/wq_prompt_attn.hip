@@ -330,8 +330,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_attn_kernel(Prom
 }
 
 // The same for prompts that give few workgroups: bound by the walk over the keys of
-// the last rows, so a workgroup owns 32 rows, its four waves take every fourth tile of 32 keys each, in LDS of their own, and
-// join at the end (the largest reference point, sums scaled to it, in wave order).
+// the last rows, so a workgroup owns 32 rows, its four waves take every fourth tile
+// of 32 keys each, in LDS of their own, and join at the end (the largest reference
+// point, sums scaled to it, in wave order).
 template <int D, bool BF>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_split_kernel(PromptAttnArgs a, int64_t slots) {
   constexpr int KT = 32;
