@@ -576,8 +576,10 @@ int wq_prompt_attention(const void* q, const void* k, const void* v, int dtype, 
  * i sees tokens t <= context_len - n + i.
  *   out[i] = sum_t softmax_t(scale * q_i . k_t) v_t with k and v decoded
  * exactly as s * (q - z); scores and sums in fp32; a softmax weight times its
- * token's V scale is rounded to fp16 for the product with the integers q - z;
- * one rounding at the end.  A query that sees no token gets zeros (lse: -inf).
+ * token's V scale is rounded to fp16 for the product with the integers q - z (off
+ * by 2^-11 of itself, or by 2^-31 of the row's largest such weight where that is
+ * more); a bf16 query's values are rounded to 2^-25 of its largest where they lie
+ * below 2^-14 of it; one rounding at the end.  A query that sees no token gets zeros (lse: -inf).
  * out [T][Hq][D] contiguous, 16-byte aligned; lse as above (or NULL); rows of T
  * outside every sequence keep what they held.  scale finite and positive.
  *   workspace  wq_kv_attention_workspace_bytes bytes, 256-byte aligned, needed

@@ -11,10 +11,14 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 
 constexpr float kNegInf = -__builtin_inff();
-// A row's reference point may lag its largest weight by this many powers of two
-// (16-bit weights stay below 2^9, the fp32 sums far below their limits), so that
-// it rarely moves.
+// A row's reference point may lag its largest weight by this many powers of two,
+// so that it rarely moves.
 constexpr float kLag = 8.0f;
+// The reference point of fp16 weights lies this many powers of two below the largest
+// one.  With kLag they stay below 2^15, and keep all of their bits down to 2^-21 of
+// the largest and some down to 2^-32 (from 1 on, 2^-14 and 2^-25): many small
+// weights count where one large weight meets a value near 0.
+constexpr float kLift = 7.0f;
 
 // Four 16-bit values of each lane of 16, transposed in blocks of 4 x 16: lane i
 // gets value i % 4 of lanes i / 4, i / 4 + 4, i / 4 + 8, i / 4 + 12.
@@ -88,21 +92,11 @@ __device__ __forceinline__ float score_factor(float scale, float up) {
   return fmaxf(scale * 1.4426950408889634f * up, 1.17549435e-38f);
 }
 
-// A bound on V scales seen so far (fp16 bits), a step below a power of two, and that power.
-struct ScaleTop {
-  uint32_t top = 0;
-  float exp = -25.0f;
-};
-// `bits`: a lane's V scale, 0 where it holds none.
-__device__ __forceinline__ void raise_top(ScaleTop& s, uint32_t bits) {
-  uint32_t top = bits & 0x7fffu;
-  if (__ballot(top > s.top)) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-    top = __builtin_amdgcn_readfirstlane(top);
-    s.exp = (float)((int)(__builtin_bit_cast(uint32_t, f16_bits_to_f32((uint16_t)top)) >> 23) - 126);
-    s.top = top >> 10 ? top | 0x3ffu : 0xffffffffu >> __builtin_clz(top);
-  }
+// The power of two above a V scale (fp16 bits).  A scale of 0 counts as 2^-64: its
+// token adds to the sum of weights, which stays within fp32, and to nothing else.
+__device__ __forceinline__ float scale_power(uint32_t bits) {
+  const uint32_t f = __builtin_bit_cast(uint32_t, f16_bits_to_f32((uint16_t)(bits & 0x7fffu)));
+  return f == 0 ? -64.0f : (float)((int)(f >> 23) - 126);
 }
 
 // The eight codes of a word less their zero-point(s) as four fp16 pairs, of

@@ -9,10 +9,14 @@
 // with the GEMV's shift, four AND-ORs and four packed subtractions a word; the
 // scale of a token multiplies its score in fp32 (K) and its softmax weight in
 // fp32 before that weight is rounded (V).  So nothing is rounded but q (bf16 rows
-// are moved into fp16's range by a power of two) and the weights w_t = p_t s_t (to
-// fp16, half a step of 2^-11 at most: their reference point is the largest score
-// plus the exponent of the largest V scale so far, so the large ones lie near 1
-// for any scale).  Leaving 64 + z of half of the codes to the fp32 sums saves a
+// are moved into fp16's range by a power of two: values below 2^-14 of the row's
+// largest lose bits) and the weights w_t = p_t s_t, both to fp16, the widest type of
+// the matrix instructions of full rate.  A weight is off by 2^-11 of itself at most
+// down to 2^-20 of the row's largest: the reference point of w_t is the largest score +
+// power of two above s_t among the tokens that the row sees, less kLift.  (The largest
+// score and the largest scale, of two tokens perhaps, would hide the other weights:
+// with 2^24 between scales all of them became 0.)  The two blocks of a head of 256 have
+// a reference point each.  Leaving 64 + z of half of the codes to the fp32 sums saves a
 // seventh of the vector instructions but not a microsecond, and loses bits where
 // most codes equal z; codes as fp16 subnormals need no subtraction at all, but the
 // matrix cores sum their products with 2^-15 of the sum lost (measured).
@@ -56,7 +60,7 @@ namespace {
 
 constexpr int kShares = 512;     // workgroups that steps are shared out to
 constexpr int kMaxShared = 256;  // sequences that a wave scans for its share
-constexpr int kMeta = 160;       // words of a wave's scales and zero-points of a tile and block
+constexpr int kMeta = 192;       // words of a wave's scales, zero-points and V scales' powers of a tile and block
 
 constexpr int kWaves = 4;
 
@@ -411,15 +415,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
     }
 
     f4 acc[X][NE];
-    float m[X], l[X];  // weights are 2^(score - m); m follows the largest score + v_top's power
+    // weights are 2^(score - m); m follows the largest score + V scale's power of each
+    // block of the head, l goes by the first one's
+    float m[X][NH], l[X];
 #pragma unroll
     for (int x = 0; x < X; ++x) {
-      m[x] = kNegInf;
+#pragma unroll
+      for (int n = 0; n < NH; ++n) m[x][n] = kNegInf;
       l[x] = 0.0f;
 #pragma unroll
       for (int e = 0; e < NE; ++e) acc[x][e] = f4{0, 0, 0, 0};
     }
-    ScaleTop v_top[NB / NH];  // of each block (a head of two: of both)
 
     // Works on tile tk; the next tile (rows `next`) is loaded as soon as this one
     // lies in LDS.
@@ -443,8 +449,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
         } else {
           reinterpret_cast<uint16_t*>(mn + 128)[ml] = (uint16_t)z10;
           reinterpret_cast<uint16_t*>(mn + 144)[ml] = (uint16_t)z6;
+          mn[160 + ml] = scale_power(sb);
         }
-        raise_top(v_top[n / NH], lane >= 32 ? sb : 0u);
       }
       // tokens of small pages that do not exist, a bit each (P32: all or none)
       const uint32_t gone = P32 ? 0u : ~(uint32_t)__ballot(ok);
@@ -496,7 +502,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
             }
         const int hb = D == 64 ? (hp * PK + sub) / 2 : hp * PK + sub;  // (first) block of the lane's head
         const float* mh = meta + kMeta * hb;
-        const float v_exp = NB > NH && hb > 0 ? v_top[NB / NH - 1].exp : v_top[0].exp;
         h8 pf[RT][NH];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
@@ -522,19 +527,29 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
               if (tok >= seen || (!P32 && (gone >> tok & 1))) s8[i] = kNegInf;
             }
           }
-          float mx = s8[0];
+          // reference points: the largest score + power of its token's V scale
 #pragma unroll
-          for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s8[i]);
-          mx = __builtin_fmaf(max_over_rows16(mx), f[x], v_exp);
-          if (__ballot(mx > m[x] + kLag)) {
-            const float mn = fmaxf(m[x], mx);
-            const float al = m[x] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[x] - mn);
-            m[x] = mn;
-            l[x] *= al;
+          for (int n = 0; n < NH; ++n) {
+            float mx = kNegInf;
 #pragma unroll
-            for (int e = 0; e < NE; ++e) acc[x][e] *= al;
+            for (int g = 0; g < 2; ++g) {
+              const f4 v = *reinterpret_cast<const f4*>(mh + kMeta * n + 160 + 16 * g + 4 * c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mx = fmaxf(mx, __builtin_fmaf(s8[4 * g + i], f[x], v[i]));
+            }
+            mx = max_over_rows16(mx) - kLift;
+            if (__ballot(mx > m[x][n] + kLag)) {
+              const float mn = fmaxf(m[x][n], mx);
+              const float al = m[x][n] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[x][n] - mn);
+              m[x][n] = mn;
+              if (n == 0) l[x] *= al;
+#pragma unroll
+              for (int e = 0; e < NE / NH; ++e) acc[x][NE / NH * n + e] *= al;
+            }
           }
-          const float ms = m[x] == kNegInf ? 0.0f : m[x];
+          const float ms = m[x][0] == kNegInf ? 0.0f : m[x][0];
+          // the second block's weights, from the first one's
+          const float up = NH == 1 || m[x][0] == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ms - m[x][NH - 1]);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             f4 vs[NH];
@@ -545,7 +560,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
               const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s8[4 * g + i], f[x], -ms));
               l[x] += w;
 #pragma unroll
-              for (int n = 0; n < NH; ++n) pf[t][n][4 * g + i] = (_Float16)(w * vs[n][i]);
+              for (int n = 0; n < NH; ++n) pf[t][n][4 * g + i] = (_Float16)((n == 0 ? w : w * up) * vs[n][i]);
             }
           }
         }
@@ -634,7 +649,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
       if (x) __syncthreads();
       const float lt = sum_over_rows16(l[x]);
       if (ce == 0) {
-        stat[wave * 32 + re] = m[x];
+        stat[wave * 32 + re] = m[x][0];
         stat[wave * 32 + 16 + re] = lt;
       }
       __syncthreads();
@@ -642,10 +657,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
 #pragma unroll
       for (int g = 0; g < kWaves; ++g) M = fmaxf(M, stat[g * 32 + re]);
       // a wave whose sum is 0 saw nothing (a NaN sum stays one)
-      const float k = lt == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[x] - M);
+      float k = lt == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[x][0] - M);
 #pragma unroll
       for (int n = 0; n < NH; ++n) {
-        if (n) __syncthreads();
+        if (n) {
+          if (lt != 0.0f) k = __builtin_amdgcn_exp2f(m[x][n] - M);
+          __syncthreads();
+        }
         float* mine = slab + wave * kSlab<D> + re * kSlabRow<D>;
 #pragma unroll
         for (int j = 0; j < DB / 64; ++j)

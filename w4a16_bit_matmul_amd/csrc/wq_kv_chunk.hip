@@ -4,7 +4,7 @@
 // The mathematics of wq_kv_attn.hip: k_t = s_t (c_t - z_t), v_t alike, a running
 // maximum and sum per row; the matrix cores take c - z exactly in fp16, K's scale
 // multiplies the score and V's the softmax weight in fp32, and only q and that
-// weight are rounded (fp16).
+// weight are rounded (fp16, with the reference point of wq_kv_attn.hip).
 //
 // With many rows the decoding and the softmax bound, not the reading.  So a
 // workgroup of four waves owns 128 rows of one KV head (a row is a token and a head
@@ -39,11 +39,22 @@ __device__ __forceinline__ int place_v(int t, int j) {
 constexpr int kTok = 64;  // tokens of a tile
 template <int D>
 constexpr int kTile = 2 * kTok * D / 8;  // 16-byte chunks of a decoded tile, K then V
-// words beside it: K scales, V scales, and V's scale bits or a mark of a missing token
+// words beside it: K scales, V scales, and the powers of two above V's or the mark of a
+// missing token
 constexpr int kMeta = 3 * kTok;
+constexpr float kGone = 128.0f;
 
 __device__ __forceinline__ f16v mfma32(const u4& x, const h8& y, const f16v& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, x), y, c, 0, 0, 0);
+}
+
+// top: the largest of the powers seen so far, with those of the lanes now.
+__device__ __forceinline__ void raise_top(float& top, float power) {
+  if (__ballot(power > top)) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) power = fmaxf(power, __shfl_xor(power, d));
+    top = fmaxf(top, __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, power))));
+  }
 }
 
 template <int D>
@@ -110,8 +121,8 @@ __global__ __launch_bounds__(64 * kChunkWaves, 2) void kv_chunk_kernel(KvAttnArg
   for (int d = 0; d < NB; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
-  float m = kNegInf, l = 0.0f;  // weights are 2^(score - m); m follows the largest score + v_top's power
-  ScaleTop v_top;
+  float m = kNegInf, l = 0.0f;  // weights are 2^(score - m); m follows the largest score + V scale's power
+  float v_top = -64.0f;         // the largest such power so far
 
   // the thread's part of a tile: NW words of token t0, from chunk j0 on
   const int own = threadIdx.x / TPT, j0 = threadIdx.x % TPT * NW;
@@ -155,7 +166,7 @@ __global__ __launch_bounds__(64 * kChunkWaves, 2) void kv_chunk_kernel(KvAttnArg
       float* mt = meta + buf * kMeta + t0;
       mt[0] = ok ? f16_bits_to_f32((uint16_t)ks) : 0.0f;
       mt[kTok] = ok ? f16_bits_to_f32((uint16_t)vs) : 0.0f;
-      reinterpret_cast<uint32_t*>(mt)[2 * kTok] = ok ? vs : 0x10000u;
+      mt[2 * kTok] = ok ? scale_power(vs) : kGone;
     }
   };
   // the lane's places in a tile: of K, chunk hf of token r (chunk 2 j + hf: bits of
@@ -170,9 +181,9 @@ __global__ __launch_bounds__(64 * kChunkWaves, 2) void kv_chunk_kernel(KvAttnArg
     const u4* kd = tile + buf * kTile<D>;
     const u2* vd = reinterpret_cast<const u2*>(kd + kTok * NC);
     const float* mt = meta + buf * kMeta;
-    const uint32_t info = reinterpret_cast<const uint32_t*>(mt)[2 * kTok + lane];
-    raise_top(v_top, info & 0xffffu);
-    const uint64_t gone = __ballot(info >> 16 != 0);
+    const float power = mt[2 * kTok + lane];
+    const uint64_t gone = __ballot(power == kGone);
+    raise_top(v_top, power == kGone ? -64.0f : power);
     int k0 = kat, v0 = vat;  // turned here: held, the places of all steps would fill the registers
     asm volatile("" : "+v"(k0), "+v"(v0));
     f16v s[2];
@@ -211,8 +222,21 @@ __global__ __launch_bounds__(64 * kChunkWaves, 2) void kv_chunk_kernel(KvAttnArg
     for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[tb][i]);
-    mx = __builtin_fmaf(max_over_halves(mx), f, v_top.exp);
+    mx = __builtin_fmaf(max_over_halves(mx), f, v_top) - kLift;
+    // that bounds score + power of every token; only where the bound calls for a new
+    // reference point is the largest sum itself taken, token by token (taken always, the
+    // call of the header's figure is 2.5 % longer)
     if (__ballot(mx > m + kLag)) {
+      mx = kNegInf;
+#pragma unroll
+      for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const f4 v = *reinterpret_cast<const f4*>(mt + 2 * kTok + 32 * tb + 8 * y + 4 * hf);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx = fmaxf(mx, __builtin_fmaf(s[tb][4 * y + i], f, v[i]));
+        }
+      mx = max_over_halves(mx) - kLift;
       const float mn = fmaxf(m, mx);
       const float al = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
       m = mn;
