@@ -552,7 +552,9 @@ int wq_qk_norm_rope(const void* q, const void* k, int dtype, int64_t T, int Hq, 
  * aligned, increasing; the lengths are read on the device and may be 0), and
  *   out[i] = sum_{t <= i} softmax_t(scale * q_i . k_t) v_t
  * over the tokens t of i's own sequence.  Scores and sums in fp32; the softmax
- * weights are rounded to dtype for the product with v; one rounding at the end.
+ * weights are rounded to dtype for the product with v (fp16: off by 2^-11 of
+ * themselves, or by 2^-32 of the row's largest where that is more); one rounding at
+ * the end.
  * out [T][Hq][D] contiguous (16-byte aligned); lse, if not NULL, fp32 [T][Hq]:
  * log sum_t exp(scale * q.k_t).  Tokens outside every sequence keep what out
  * and lse held there.  scale finite and positive. */
@@ -578,8 +580,9 @@ int wq_prompt_attention(const void* q, const void* k, const void* v, int dtype, 
  * exactly as s * (q - z); scores and sums in fp32; a softmax weight times its
  * token's V scale is rounded to fp16 for the product with the integers q - z (off
  * by 2^-11 of itself, or by 2^-31 of the row's largest such weight where that is
- * more); a bf16 query's values are rounded to 2^-25 of its largest where they lie
- * below 2^-14 of it; one rounding at the end.  A query that sees no token gets zeros (lse: -inf).
+ * more); a query's values below 2^-14 of its largest may be off by 2^-25 of that
+ * largest; one rounding at the end.  A query that sees no token
+ * gets zeros (lse: -inf).
  * out [T][Hq][D] contiguous, 16-byte aligned; lse as above (or NULL); rows of T
  * outside every sequence keep what they held.  scale finite and positive.
  *   workspace  wq_kv_attention_workspace_bytes bytes, 256-byte aligned, needed

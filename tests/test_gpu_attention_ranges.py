@@ -12,7 +12,7 @@ import attn_ref as ref
 import oracle
 import w4a16_bit_matmul_amd as wq
 from parity import say
-from test_gpu_attention import BF, HF, Cache, _run_cache, _tables
+from test_gpu_attention import BF, HF, Cache, _run_cache, _run_prompt, _tables
 
 pytestmark = pytest.mark.gpu
 
@@ -236,3 +236,27 @@ def test_a_sink_before_a_long_context():
     cache = make_cache(9, n, Hkv, D, pull, vs)
     table = np.arange(n // page, dtype=np.int32)[None]
     _check(cache, queries(5, cache, 1, Hq, HF), table, page, [n], [0, 1], "out")
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,D", [(3000, 1, 1, 64), (3000, 2, 1, 128), (2100, 9, 9, 64), (2100, 9, 9, 128), (1500, 4, 4, 256), (900, 20, 20, 128)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_a_prompt_behind_a_sink(n, Hq, Hkv, D, dtype):
+    """The first key's score is 17 above the others' and its values are near 0: the
+    output is the others', with weights of e^-17 (fp16: 2^-24.5)."""
+    say(f"prompt behind a sink n={n} Hq={Hq} Hkv={Hkv} D={D} {dtype}")
+    rng = np.random.default_rng(n + D)
+    sign = rng.integers(0, 2, D) * 2 - 1
+    q = torch.from_numpy((sign * rng.uniform(0.9, 1.1, (n, Hq, D))).astype(np.float32)).to(dtype)
+    k = torch.from_numpy((0.05 * rng.standard_normal((n, Hkv, D))).astype(np.float32)).to(dtype)
+    v = torch.from_numpy(rng.uniform(0.5, 1.5, (n, Hkv, D)).astype(np.float32)).to(dtype)
+    k[0] = torch.from_numpy((sign * 17.0 / D ** 0.5).astype(np.float32)).to(dtype)
+    v[0] = 2.0 ** -20
+    got, _ = _run_prompt(q.cuda(), k.cuda(), v.cuda(), [0, n])
+    got = got.double().cpu()
+    seen = torch.tril(torch.ones((n, n), dtype=torch.bool))
+    for h in range(0, Hq, 4):
+        # the absolute part of a weight's rounding: half a step of fp16's subnormals at 2^-7 of
+        # the largest weight (bf16 has none)
+        kv = [x[:, h // (Hq // Hkv)].double() for x in (k, v)]
+        o, b, _, _ = ref.attend(q[:, h].double(), *kv, seen, D ** -0.5, 2.0 ** -8 * float(v.abs().max()), dtype, ref.HALF[dtype])
+        ref.check(got[:, h], o, b, f"head {h}")

@@ -8,8 +8,8 @@
 // The matrix cores take the exact integers c - z in fp16 (|c - z| <= 15), decoded
 // with the GEMV's shift, four AND-ORs and four packed subtractions a word; the
 // scale of a token multiplies its score in fp32 (K) and its softmax weight in
-// fp32 before that weight is rounded (V).  So nothing is rounded but q (bf16 rows
-// are moved into fp16's range by a power of two: values below 2^-14 of the row's
+// fp32 before that weight is rounded (V).  So nothing is rounded but q (rows are
+// moved into fp16's range by a power of two: values below 2^-14 of the row's
 // largest lose bits) and the weights w_t = p_t s_t, both to fp16, the widest type of
 // the matrix instructions of full rate.  A weight is off by 2^-11 of itself at most
 // down to 2^-20 of the row's largest: the reference point of w_t is the largest score +

@@ -3,7 +3,7 @@
 //
 // For query i of a sequence and head h of KV head h / G:
 //   out = sum_{t <= i} p_t v_t / sum p_t,  p_t = exp(scale * q.k_t - max),
-// in one pass over the keys with a running maximum and sum in fp32.
+// in one pass over the keys with a running reference point and sum in fp32.
 //
 // A workgroup owns 128 rows of one KV head, a row being (token, head of the
 // group): its 128 / G tokens share every K and V tile it reads, and a short
@@ -15,6 +15,14 @@
 // its operand of the second product (tokens {8a + 4h .. + 3} of half h).  V^T
 // comes out of the row-major tile by ds_read_b64_tr_b16, which transposes 4 x 16
 // blocks as it reads.
+//
+// The weights are rounded to the inputs' type, the operand type of the matrix
+// instructions of full rate: off by half a step of themselves (bf16 2^-8, fp16 2^-11) in
+// a sum of hundreds of them.  fp16 ones would be subnormal from 2^-14 of the largest on,
+// and behind a key that takes the weight and has little value, as a first token often is,
+// all of the output comes from such; so the reference point lies kLift below the
+// largest score, which keeps their bits down to 2^-21 of it (with the point at the
+// largest score, 3000 keys of weight e^-17 came out 43 % off).
 //
 // LDS rows hold D values as 16-byte chunks; chunk j of K's token t sits at
 // j ^ (t mod 16) (the 16 tokens a b128 read takes at once then fall in
@@ -259,8 +267,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_attn_kernel(Prom
     for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[tb][i]);
-    mx = max_over_halves(mx) * f;
-    // the maximum in use may lag the true one by kLag: weights up to 2^kLag
+    mx = __builtin_fmaf(max_over_halves(mx), f, -kLift);
+    // the reference point in use may lag the true one by kLag: weights up to 2^(kLag + kLift)
     if (__ballot(mx > m + kLag)) {
       const float mn = fmaxf(m, mx);
       const float al = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
@@ -422,7 +430,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_split_kernel(Pro
     float mx = kNegInf;
 #pragma unroll
     for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[i]);
-    mx = max_over_halves(mx) * f;
+    mx = __builtin_fmaf(max_over_halves(mx), f, -kLift);
     if (__ballot(mx > m + kLag)) {
       const float mn = fmaxf(m, mx);
       const float al = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
