@@ -1,0 +1,29 @@
+"""Cache attention on the HIP path at the edges of the bounds that its caller
+gives: max_context, max_queries and workspaces sized from them."""
+import pytest
+import torch
+
+import attn_ref as ref
+import w4a16_bit_matmul_amd as wq
+from parity import say
+from test_gpu_attention import BF, Cache, _cache_want, _check_rows, _run_cache, _tables
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("most", [7, 6, 100])
+def test_a_workspace_sized_for_more_queries_than_there_are(most):
+    """The bytes that wq_kv_attention_workspace_bytes names for these bounds fit the
+    call with the same bounds."""
+    lens, nq, Hq, Hkv, D, page, room = [3000, 2100], [4, 2], 8, 2, 128, 32, 4096
+    T, starts = 6, [0, 4, 6]
+    need = wq.wq_kv_attention_workspace_bytes(T, Hq, Hkv, D, 2, page, room, most)
+    assert need > 0
+    S = 4096 + 2048
+    cache = Cache(most, S, Hkv, D)
+    table = _tables(1, lens, page, S, width=room // page)
+    q = ref.values(2, (T, Hq, D), BF)
+    want, used = _cache_want(cache, q, table, page, lens, starts, D ** -0.5)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    got, lse = _run_cache(cache.to_dev(used), q.cuda(), table, page, lens, starts, max_context=room, max_queries=most, workspace=ws)
+    _check_rows(got, lse, want)

@@ -641,13 +641,15 @@ def wq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_s
 
 def wq_kv_attention_workspace_bytes(T: int, Hq: int, Hkv: int, D: int, B: int, page_size: int, max_context: int,
                                     max_queries: int = 1) -> int:
-    return int(lib().wq_kv_attention_workspace_bytes(T, Hq, Hkv, D, B, page_size, max_context, max_queries))
+    """Bytes of the workspace that wq_kv_attention takes for these sizes (0: none
+    needed, or sizes it would refuse); max_queries past T counts as T, as there."""
+    return int(lib().wq_kv_attention_workspace_bytes(T, Hq, Hkv, D, B, page_size, max_context, min(max_queries, T)))
 
 
 def wq_kv_attention_plan(T: int, Hq: int, Hkv: int, D: int, B: int, page_size: int, max_context: int,
                          max_queries: int = 1) -> str:
     buf = ctypes.create_string_buffer(256)
-    _check(lib().wq_kv_attention_plan(T, Hq, Hkv, D, B, page_size, max_context, max_queries, buf, len(buf)),
+    _check(lib().wq_kv_attention_plan(T, Hq, Hkv, D, B, page_size, max_context, min(max_queries, T), buf, len(buf)),
            "wq_kv_attention_plan")
     return buf.value.decode()
 
@@ -664,9 +666,12 @@ def wq_kv_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, block_t
     sequence, or those of sequence b at q_starts[b] .. q_starts[b+1] - 1 (int32
     [B+1]; they are its last tokens, and see the tokens up to their own).
     max_context and max_queries bound the lengths for the launch and pick the
-    kernel (defaults: the table's width, all T; tighter bounds are faster).  scale
-    defaults to 1/sqrt(D).  Queries that see nothing give zeros; rows outside every
-    sequence are not written.  Returns out [T][Hq][D], or (out, lse) with lse=True
+    kernel (defaults: the table's width, all T; tighter bounds are faster).  With
+    several sequences give max_queries: all T for each of them launches B times the
+    workgroups that have work, picks the kernel for as many rows, and is refused
+    (WQ_EUNSUPPORTED) where B * T * Hq / 16 passes 2^24.  scale defaults to
+    1/sqrt(D).  Queries that see nothing give zeros; rows outside every sequence
+    are not written.  Returns out [T][Hq][D], or (out, lse) with lse=True
     or an fp32 [T][Hq] tensor.  Without a workspace, each call that needs one
     allocates it on its stream."""
     qs = _heads("q", q)
