@@ -567,10 +567,11 @@ int wq_prompt_attention(const void* q, const void* k, const void* v, int dtype, 
  * them, codes 16-byte aligned), shared by B sequences in pages of page_size rows
  * (a power of two up to S): token t of sequence b lies in row
  *   block_table[b][t / page_size] * page_size + t % page_size
- * (device int32 [B][table_width]; a page number outside [0, S / page_size) marks
- * tokens that are not attended).  context_lens[b] (device int32 [B]) counts the
- * sequence's cached tokens, those of this call's queries included; at most
- * max_context (<= table_width * page_size) are attended.
+ * (device int32 [B][table_width], with max_context 0 not read and NULL if empty; a
+ * page number outside [0, S / page_size) marks tokens that are not attended).
+ * context_lens[b] (device int32 [B]) counts the sequence's cached tokens, those of
+ * this call's queries included; at most max_context (<= table_width * page_size) are
+ * attended.
  *   Queries: one per sequence (q_starts NULL, T == B, max_queries 1), or those
  * of sequence b at q_starts[b] .. q_starts[b + 1] - 1 (device int32 [B + 1],
  * increasing; of each sequence the first max_queries are computed).  The n =

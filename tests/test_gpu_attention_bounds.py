@@ -1,12 +1,13 @@
 """Cache attention on the HIP path at the edges of the bounds that its caller
 gives: max_context, max_queries and workspaces sized from them."""
+import numpy as np
 import pytest
 import torch
 
 import attn_ref as ref
 import w4a16_bit_matmul_amd as wq
 from parity import say
-from test_gpu_attention import BF, Cache, _cache_want, _check_rows, _run_cache, _tables
+from test_gpu_attention import BF, HF, Cache, _cache_want, _check_rows, _run_cache, _tables
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +28,19 @@ def test_a_workspace_sized_for_more_queries_than_there_are(most):
     ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
     got, lse = _run_cache(cache.to_dev(used), q.cuda(), table, page, lens, starts, max_context=room, max_queries=most, workspace=ws)
     _check_rows(got, lse, want)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,nq", [(8, 2, 128, 1), (4, 4, 64, 3), (3, 1, 256, 2), (64, 8, 128, 160)])
+def test_no_room_for_any_token(Hq, Hkv, D, nq):
+    """A block table without columns, or max_context 0, whatever the lengths: every
+    query sees nothing."""
+    B = 8
+    starts = [nq * b for b in range(B + 1)]
+    cache = Cache(D, 16, Hkv, D)
+    q = ref.values(3, (B * nq, Hq, D), HF).cuda()
+    if nq == 160:
+        assert "kv_chunk_kernel" in wq.wq_kv_attention_plan(B * nq, Hq, Hkv, D, B, 16, 0, nq)
+    for width, kw in ((0, {}), (3, dict(max_context=0))):
+        out, lse = _run_cache(cache.to_dev(), q, np.full((B, width), -1, np.int32), 16, [0, 5] * (B // 2), None if nq == 1 else starts,
+                              **kw, **({} if nq == 1 else dict(max_queries=nq)))
+        assert bool((out == 0).all()) and bool((lse == -np.inf).all())

@@ -662,8 +662,8 @@ int wq_kv_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D,
   if (max_context > table_width * page_size) return WQ_EINVAL;
   if (!q_starts && (T != B || max_queries != (T > 0 ? 1 : 0))) return WQ_EINVAL;
   if (T == 0 || B == 0 || max_queries == 0) return WQ_OK;
-  if (!q || !k_codes || !k_s_f16 || !k_zpacked || !v_codes || !v_s_f16 || !v_zpacked || !block_table ||
-      !context_lens || !out)
+  if (!q || !k_codes || !k_s_f16 || !k_zpacked || !v_codes || !v_s_f16 || !v_zpacked ||
+      (!block_table && max_context > 0) || !context_lens || !out)
     return WQ_EINVAL;
   if ((st = check_rows(q, q_stride, Hq, D))) return st;
   if (!aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_s_f16, 2) || !aligned(v_s_f16, 2) ||
