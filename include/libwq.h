@@ -570,8 +570,9 @@ int wq_prompt_attention(const void* q, const void* k, const void* v, int dtype, 
  * (device int32 [B][table_width], with max_context 0 not read and NULL if empty; a
  * page number outside [0, S / page_size) marks tokens that are not attended).
  * context_lens[b] (device int32 [B]) counts the sequence's cached tokens, those of
- * this call's queries included; at most max_context (<= table_width * page_size) are
- * attended.
+ * this call's queries included.  max_context (<= table_width * page_size) bounds
+ * them: a longer length counts as max_context, in what its queries see as well (they
+ * are the last of those max_context tokens).
  *   Queries: one per sequence (q_starts NULL, T == B, max_queries 1), or those
  * of sequence b at q_starts[b] .. q_starts[b + 1] - 1 (device int32 [B + 1],
  * increasing; of each sequence the first max_queries are computed).  The n =

@@ -44,3 +44,22 @@ def test_no_room_for_any_token(Hq, Hkv, D, nq):
         out, lse = _run_cache(cache.to_dev(), q, np.full((B, width), -1, np.int32), 16, [0, 5] * (B // 2), None if nq == 1 else starts,
                               **kw, **({} if nq == 1 else dict(max_queries=nq)))
         assert bool((out == 0).all()) and bool((lse == -np.inf).all())
+
+
+@pytest.mark.parametrize("lens,nq,Hq,Hkv,D,page,room,shared", [
+    ([700, 300, 90, 1000], [4, 1, 3, 0], 8, 2, 128, 16, 256, False), ([5000, 4100, 3000], [3, 5, 2], 8, 8, 64, 64, 4096, True),
+    ([1500, 1024, 1025], [9, 2, 9], 4, 1, 256, 32, 1024, True), ([700], [512], 16, 2, 128, 16, 400, False)])
+def test_lengths_past_max_context_count_as_it(lens, nq, Hq, Hkv, D, page, room, shared):
+    """A sequence of more tokens than max_context has that many, and its queries are the
+    last of those."""
+    say(f"lens={lens} past {room}, nq={nq} Hq={Hq} Hkv={Hkv} D={D}")
+    starts = [int(x) for x in np.concatenate([[0], np.cumsum(nq)])]
+    S = (sum(-(-min(n, room) // page) for n in lens) + 2) * page
+    cache = Cache(room + D, S, Hkv, D)
+    table = _tables(D, [min(n, room) for n in lens], page, S, width=-(-max(lens) // page))
+    q = ref.values(4, (starts[-1], Hq, D), BF)
+    plan = wq.wq_kv_attention_plan(starts[-1], Hq, Hkv, D, len(lens), page, room, max(nq))
+    assert plan.endswith("shares") == shared, plan
+    want, used = _cache_want(cache, q, table, page, lens, starts, D ** -0.5, max_context=room)
+    got, lse = _run_cache(cache.to_dev(used), q.cuda(), table, page, lens, starts, max_context=room, max_queries=max(nq))
+    _check_rows(got, lse, want)

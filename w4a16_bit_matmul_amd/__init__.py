@@ -666,12 +666,13 @@ def wq_kv_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, block_t
     sequence, or those of sequence b at q_starts[b] .. q_starts[b+1] - 1 (int32
     [B+1]; they are its last tokens, and see the tokens up to their own).
     max_context and max_queries bound the lengths for the launch and pick the
-    kernel (defaults: the table's width, all T; tighter bounds are faster).  With
-    several sequences give max_queries: all T for each of them launches B times the
-    workgroups that have work, picks the kernel for as many rows, and is refused
-    (WQ_EUNSUPPORTED) where B * T * Hq / 16 passes 2^24.  scale defaults to
-    1/sqrt(D).  Queries that see nothing give zeros; rows outside every sequence
-    are not written.  Returns out [T][Hq][D], or (out, lse) with lse=True
+    kernel (defaults: the table's width, all T; tighter bounds are faster); a
+    length past max_context counts as max_context, its queries as the last of those
+    tokens.  With several sequences give max_queries: all T for each of them
+    launches B times the workgroups that have work, picks the kernel for as many
+    rows, and is refused (WQ_EUNSUPPORTED) where B * T * Hq / 16 passes 2^24.
+    scale defaults to 1/sqrt(D).  Queries that see nothing give zeros; rows outside
+    every sequence are not written.  Returns out [T][Hq][D], or (out, lse) with lse=True
     or an fp32 [T][Hq] tensor.  Without a workspace, each call that needs one
     allocates it on its stream."""
     qs = _heads("q", q)
