@@ -20,3 +20,12 @@ def test_attention_kernels_keep_to_their_registers(src, kernel, instances):
         assert scratch == 0 and vgpr <= (512 if one_a_cu else 256), (name, vgpr, scratch)
         if src == "wq_rope.hip":
             assert vgpr <= 64, (name, vgpr)  # eight waves a SIMD hide a row's latency
+
+
+@pytest.mark.skipif(not os.path.exists(_build.HIPCC), reason="hipcc is not installed")
+def test_the_joining_kernel_keeps_its_pieces_in_registers():
+    """Up to 16 pieces of a row a lane are in flight together, four waves to a SIMD."""
+    meta = {n: v for n, v in _kernel_metadata("wq_kv_attn.hip").items() if "19kv_attn_join_kernel" in n}
+    assert len(meta) == 14, sorted(meta)
+    for name, (vgpr, scratch) in meta.items():
+        assert scratch == 0 and vgpr <= 128, (name, vgpr, scratch)

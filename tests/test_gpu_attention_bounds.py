@@ -63,3 +63,26 @@ def test_lengths_past_max_context_count_as_it(lens, nq, Hq, Hkv, D, page, room, 
     want, used = _cache_want(cache, q, table, page, lens, starts, D ** -0.5, max_context=room)
     got, lse = _run_cache(cache.to_dev(used), q.cuda(), table, page, lens, starts, max_context=room, max_queries=max(nq))
     _check_rows(got, lse, want)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,B,page,room,nq", [(1, 8, 1, 128, 1, 64, 9000, 1), (3, 4, 4, 64, 3, 16, 4500, 1), (2, 4, 1, 256, 2, 32, 5000, 1),
+                                                      (1, 16, 8, 128, 1, 32, 7000, 1), (6, 8, 2, 128, 2, 16, 4000, 3)])
+def test_shared_out_calls_need_their_workspace(T, Hq, Hkv, D, B, page, room, nq):
+    """The long contexts of test_gpu_attention.py are shared out, and the call refuses
+    less than the bytes named for it."""
+    assert wq.wq_kv_attention_plan(T, Hq, Hkv, D, B, page, room, nq).endswith("shares")
+    need = wq.wq_kv_attention_workspace_bytes(T, Hq, Hkv, D, B, page, room, nq)
+    assert need > 0
+    S = -(-room // page) * page
+    c = Cache(D, S, Hkv, D).to_dev()
+    for x in c:
+        x.s.zero_()
+    q = torch.zeros((T, Hq, D), dtype=HF, device="cuda")
+    table = torch.zeros((B, S // page), dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), nq, dtype=torch.int32, device="cuda")
+    starts = None if nq == 1 else torch.arange(0, T + 1, nq, dtype=torch.int32, device="cuda")
+    call = lambda n: wq.wq_kv_attention(q, *c, table, lens, page_size=page, max_context=room, q_starts=starts, max_queries=nq,
+                                        workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(wq.WQError):
+        call(need - 1)
+    assert bool((call(need) == 0).all())
