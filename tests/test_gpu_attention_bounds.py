@@ -86,3 +86,38 @@ def test_shared_out_calls_need_their_workspace(T, Hq, Hkv, D, B, page, room, nq)
     with pytest.raises(wq.WQError):
         call(need - 1)
     assert bool((call(need) == 0).all())
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (4, 4, 64), (3, 1, 256)])
+def test_one_long_context_among_more_sequences_than_are_shared_out(Hq, Hkv, D):
+    """300 sequences of up to 90 tokens and one of 5000: a workgroup walks each, whatever
+    the others' lengths."""
+    rng = np.random.default_rng(D + 1)
+    lens = [int(x) for x in rng.integers(0, 91, 300)]
+    lens[117] = 5000
+    page, S = 32, 300 * 96 + 5024
+    cache = Cache(D + 7, S, Hkv, D)
+    table = _tables(D, lens, page, S)
+    q = ref.values(Hq, (300, Hq, D), HF)
+    assert wq.wq_kv_attention_plan(300, Hq, Hkv, D, 300, page, 5024, 1).endswith("whole units")
+    want, used = _cache_want(cache, q, table, page, lens, list(range(301)), D ** -0.5)
+    got, lse = _run_cache(cache.to_dev(used), q.cuda(), table, page, lens, None)
+    _check_rows(got, lse, want)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,B,nq,kernel", [(64, 8, 128, 64, 16, "kv_chunk_kernel<D=128"), (32, 8, 64, 64, 32, "kv_chunk_kernel<D=64"),
+                                                 (16, 4, 128, 64, 4, "shares"), (8, 1, 256, 20, 3, "shares")])
+def test_short_contexts_under_a_large_max_context(Hq, Hkv, D, B, nq, kernel):
+    """Room for a million tokens a sequence and at most 120 in it."""
+    rng = np.random.default_rng(B + D)
+    lens = [0, 1, nq] + [int(x) for x in rng.integers(0, 121, B - 3)]
+    page, room = 16, 2 ** 20
+    S = (sum(-(-n // page) for n in lens) + 1) * page
+    cache = Cache(D + nq, S, Hkv, D)
+    table = _tables(D, lens, page, S, width=room // page)
+    starts = [nq * b for b in range(B + 1)]
+    q = ref.values(nq, (B * nq, Hq, D), BF)
+    assert kernel in wq.wq_kv_attention_plan(B * nq, Hq, Hkv, D, B, page, room, nq)
+    want, used = _cache_want(cache, q, table, page, lens, starts, D ** -0.5)
+    got, lse = _run_cache(cache.to_dev(used), q.cuda(), table, page, lens, starts, max_queries=nq)
+    _check_rows(got, lse, want)
