@@ -60,7 +60,9 @@ namespace {
 
 constexpr int kShares = 512;     // workgroups that steps are shared out to
 constexpr int kMaxShared = 256;  // sequences that a wave scans for its share
-constexpr int kMeta = 192;       // words of a wave's scales, zero-points and V scales' powers of a tile and block
+// words of a wave's scales, zero-points and V scales' powers of a tile and block, and 32
+// more, so that the same words of two blocks lie in different banks
+constexpr int kMeta = 224;
 
 constexpr int kWaves = 4;
 
