@@ -535,7 +535,8 @@ int wq_kv_dequant(const uint8_t* codes, const uint16_t* s_f16, const uint8_t* zp
  *   rot values (pair i: values i and i + rot/2, or 2i and 2i + 1 when
  *   interleaved is 1), cos and sin being row positions[t] of the fp32 tables
  *   [P][rot / 2]; values rot.. are left at n.
- * fp32 arithmetic, one rounding to dtype at the end.  A token whose position
+ * fp32 arithmetic, one rounding to dtype at the end (squares beyond fp32's range, of
+ * bf16 values from 2^60 on, give zeros).  A token whose position
  * lies outside [0, P) is padding: its output rows are left as they were.  rot: a
  * positive multiple of 16, at most D.  eps finite and not negative.
  *   positions  device int32 [T], 4-byte aligned; cos, sin 16-byte aligned,

@@ -49,8 +49,10 @@
 // results which a second kernel joins.
 //
 // 64 contexts of 4-8K tokens, 64 / 8 heads of 128: the walk 97 us, 4.3 TB/s (a copy
-// reaches 5.0, reads alone 6.2-7.0; vector units 43 % and matrix cores 12 % busy),
-// the join 8.  One of 131072: 35 and 6 us.  One of 201 tokens: 7 us, all latency.
+// reaches 5.0, reads alone 6.2-7.0; vector units 43 % and matrix cores 11 % busy),
+// the join 8.  One of 131072: 35 and 6 us.  One of 201 tokens: 7 us, all latency.  With
+// 9-16 rows of heads of 64 a wave takes half a line and another workgroup the other:
+// 16 contexts of 1-9K, 25 us and 5, half of the 25 for the second reading.
 #include <stdio.h>
 
 #include "wq_attn.h"
@@ -91,11 +93,12 @@ KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_q
   // Tiles of 128 rows once two workgroups a CU come of it (512 tokens over 16K of one
   // sequence, one a CU: 510 us, 455 with tiles of 32 rows; of two sequences 585 and
   // 789) and nearly all of their rows are used (64 sequences, 128 rows a head: 97 us
-  // and 133; 72 rows: 91 and 75).  D = 256: 660 us and 588, no registers.
+  // and 133; 72 rows: 91 and 75).  With heads of 256 (two sequences over 7-8K, 32 / 4
+  // heads) 660 us and 588: decoded tiles of 128 KB leave it one workgroup a CU.
   p.chunk = D != 256 && p.grid >= kShares && 5 * ((rows + 31) / 32) >= 16 * p.rtiles;
   if (p.chunk) return p;
   // more than 16 rows: two tiles share the decoded codes (4 contexts of up to 4K
-  // with 32 rows: 29 us, 32 with one; D = 256 has no registers for them)
+  // with 32 rows: 29 us, 32 with one; with heads of 256 two spill 432 bytes or more)
   p.RT = rows <= 16 || D == 256 ? 1 : 2;
   p.rtiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
   p.urows = (int)(rows < 16 * p.RT ? rows : 16 * p.RT);

@@ -15,10 +15,10 @@
 // product (tokens {8a + 4h .. + 3} of half h), and V^T comes out of the row-major
 // tile by ds_read_b64_tr_b16.
 //
-// Two sequences' next 512 tokens over 12-16K cached ones, 64 / 8 heads of 128: 583
-// us, 835 TFLOP/s (matrix instructions 36 % of the cycles, decoding and softmax 52 %),
+// Two sequences' next 512 tokens over 12-16K cached ones, 64 / 8 heads of 128: 588
+// us, 829 TFLOP/s (matrix instructions 36 % of the cycles, decoding and softmax 52 %),
 // where tiles of 32 rows decoded by each wave took 789.  256 rows a workgroup halve
-// the decoding again but tie eight waves together: 631 us.
+// the decoding again but tie eight waves together: 631 us where this took 583.
 #include "wq_attn.h"
 
 namespace wq {
@@ -224,8 +224,8 @@ __global__ __launch_bounds__(64 * kChunkWaves, 2) void kv_chunk_kernel(KvAttnArg
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[tb][i]);
     mx = __builtin_fmaf(max_over_halves(mx), f, v_top) - kLift;
     // that bounds score + power of every token; only where the bound calls for a new
-    // reference point is the largest sum itself taken, token by token (taken always, the
-    // call of the header's figure is 2.5 % longer)
+    // reference point is the largest sum itself taken, token by token (taken always, 631
+    // us in turn with 605)
     if (__ballot(mx > m + kLag)) {
       mx = kNegInf;
 #pragma unroll

@@ -35,14 +35,14 @@
 // stored, to the rows that do see it.
 //
 // Bound by the matrix cores for long prompts: 8K tokens with 64 / 8 heads of 128 in
-// 1.1 ms, 1,000 TFLOP/s (a library product of bf16 reaches 1,415), matrix
+// 1.1 ms, 980-1,020 TFLOP/s (a library product of bf16 reaches 1,415 in a burst), matrix
 // instructions half of the cycles and the softmax a third; with heads of 64 the
-// softmax comes first (16 prompts of up to 1500: 66 us, 559 TFLOP/s); short prompts
-// are bound by the latency of a workgroup's start (48 of up to 300 tokens: 84 us,
-// 3.2 TB/s).  Two workgroups a CU: while one waits the other works.  128 rows keep
+// softmax comes first (16 prompts of up to 1500: 68 us, 545 TFLOP/s); short prompts
+// are bound by the latency of a workgroup's start (48 of up to 300 tokens: 78-84 us,
+// 3.2-3.4 TB/s).  Two workgroups a CU: while one waits the other works.  128 rows keep
 // four waves in step; 256, or two groups of four waves half a tile apart (one
 // multiplies while the other takes its softmax), measured 1,200 and 1,316 us where
-// this took 1,183.
+// the kernel of that time took 1,183.
 //
 // Workgroups find their sequence from the device's starts: sequence b owns the
 // tile slots from floor(start_b G / 128) + b on, at least as many as it has
@@ -244,7 +244,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_attn_kernel(Prom
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb) s[tb] = mfma32<BF>(kd[32 * tb * NC + kat[j]], qf[j], s[tb]);
     // three steps' reads ahead of the products (left alone, a read waits for the
-    // products before it: 4K tokens with heads of 256 450 us, 416 so; 8K of 128 1240, 1224)
+    // products before it: 4K tokens with 32 / 4 heads of 256 450 us, 416 so; 8K with 64 / 8
+    // of 128 1240, 1224)
     constexpr int kAhead = 3 * TB;
     __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
 #pragma unroll
@@ -535,7 +536,8 @@ template <int D, int KT>
 hipError_t launch_d(const PromptAttnArgs& a, hipStream_t stream) {
   // fewer workgroups than half the CUs: one prompt of 500 / 1000 / 2000 tokens with
   // 8 / 1 heads of 128 10.3 / 15.1 / 28.5 us, 16.1 / 25.3 / 44.5 with 128 rows; with
-  // 182 workgroups (four of 700) 22.9 and 20.0.  D = 256 has no registers for it.
+  // 182 workgroups (four of 700) 22.9 and 20.0.  With heads of 256 this
+  // tiling spills 204 bytes out of 512 registers.
   if constexpr (D != 256)
     if ((a.T * (a.Hq / a.Hkv) / kRows + a.B) * a.Hkv < 128)
       return a.dtype == 1 ? launch_split<D, true>(a, stream) : launch_split<D, false>(a, stream);

@@ -14,10 +14,10 @@
 // (two 8-byte loads), in the interleaved form eight neighbours (one 16-byte
 // load), so the rotation needs no exchange between lanes and the sum of squares
 // is one xor-shuffle tree over the D/8 lanes of the row.  A prompt of 32768 tokens
-// (64 + 8 heads of 128) moves 1.2 GB in 247 us, the rate of a large copy
+// (64 + 8 heads of 128) moves 1.2 GB in 240-250 us, the rate of a large copy
 // (5.0 TB/s); with 64-bit row numbers and outputs rounded in integer arithmetic the
 // vector instructions took all of the cycles (268 us).  A decode step of 64 tokens
-// takes 2.7 us, the latency of one row.
+// takes 2.7 us a call in a replayed graph (traced alone 3.4), the latency of one row.
 #include "wq_attn.h"
 
 namespace wq {
@@ -143,7 +143,7 @@ hipError_t launch_lph(const QkNormRopeArgs& a, hipStream_t stream) {
   constexpr int RPB = 256 / LPH;
   // four rows a lane once that still leaves two thousand workgroups (32768 tokens of
   // 72 heads: 247 us, 265 with one); one below, where the time is the latency of a
-  // row (64 tokens: 2.7 us, 4.6 with four)
+  // row (64 tokens: 2.7 us, 4.6 with four; all in replayed graphs)
   if (rows >= (int64_t)2048 * RPB * 4)
     qk_norm_rope_kernel<DT, INTER, LPH, 4><<<(unsigned)((rows + 4 * RPB - 1) / (4 * RPB)), 256, 0, stream>>>(a);
   else
