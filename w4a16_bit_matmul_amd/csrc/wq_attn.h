@@ -92,11 +92,20 @@ __device__ __forceinline__ float score_factor(float scale, float up) {
   return fmaxf(scale * 1.4426950408889634f * up, 1.17549435e-38f);
 }
 
-// The power of two above a V scale (fp16 bits).  A scale of 0 counts as 2^-64: its
-// token adds to the sum of weights, which stays within fp32, and to nothing else.
-__device__ __forceinline__ float scale_power(uint32_t bits) {
-  const uint32_t f = __builtin_bit_cast(uint32_t, f16_bits_to_f32((uint16_t)(bits & 0x7fffu)));
-  return f == 0 ? -64.0f : (float)((int)(f >> 23) - 126);
+// The power of two above a V scale.  A scale of 0 counts as 2^kNoPower: its token adds
+// to the sum of weights, which stays within fp32, and to nothing else.
+constexpr float kNoPower = -64.0f;
+__device__ __forceinline__ float scale_power(float s) {
+  return (float)__builtin_amdgcn_frexp_expf(fmaxf(fabsf(s), 0x1p-65f));
+}
+
+// top: the largest of the powers seen so far, with those of the lanes now.
+__device__ __forceinline__ void raise_top(float& top, float power) {
+  if (__ballot(power > top)) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) power = fmaxf(power, __shfl_xor(power, d));
+    top = fmaxf(top, __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, power))));
+  }
 }
 
 // The eight codes of a word less their zero-point(s) as four fp16 pairs, of

@@ -254,6 +254,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
   constexpr int NS = D / 32;              // MFMA steps of a score
   constexpr int NE = D / 16;              // MFMAs of an output tile: 16 channels each
   constexpr int kStep = 32 * kWaves;
+  // Where a bound of a row's reference points is looked at first, the largest score plus
+  // the largest power of V's scales so far: with the two points of a head of 256 (512
+  // tokens each over 7-8K of two sequences, 32 / 4 heads: 639 us, 671 without).  Elsewhere
+  // it costs as much as it saves (512 tokens over 16K of one sequence, 64 / 8 heads of 128:
+  // 460 and 467; 4 contexts of up to 4K with 32 rows 28.1 and 27.0; one of 201 tokens 7.0
+  // and 6.8).
+  constexpr bool kBounded = D == 256;
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4, ml = lane & 31;
   const int sub = r / PR;  // (0 unless heads share a tile)
@@ -432,6 +439,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
       for (int e = 0; e < NE; ++e) acc[x][e] = f4{0, 0, 0, 0};
     }
 
+    float v_top[NB];  // (kBounded) the largest power of each block so far
+#pragma unroll
+    for (int n = 0; n < NB; ++n) v_top[n] = kNoPower;
+
     // Works on tile tk; the next tile (rows `next`) is loaded as soon as this one
     // lies in LDS.
     auto compute = [&](int next, bool next_ok) {
@@ -454,8 +465,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
         } else {
           reinterpret_cast<uint16_t*>(mn + 128)[ml] = (uint16_t)z10;
           reinterpret_cast<uint16_t*>(mn + 144)[ml] = (uint16_t)z6;
-          mn[160 + ml] = scale_power(sb);
+          mn[160 + ml] = scale_power(sv);
         }
+        if (kBounded) raise_top(v_top[n], lane < 32 ? kNoPower : scale_power(sv));
       }
       // tokens of small pages that do not exist, a bit each (P32: all or none)
       const uint32_t gone = P32 ? 0u : ~(uint32_t)__ballot(ok);
@@ -533,8 +545,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
             }
           }
           // reference points: the largest score + power of its token's V scale
+          float top = kNegInf;
+          if (kBounded) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, s8[i]);
+            top = max_over_rows16(top);
+          }
 #pragma unroll
           for (int n = 0; n < NH; ++n) {
+            if (kBounded) {
+              if (!__ballot(__builtin_fmaf(top, f[x], v_top[n]) > m[x][n] + (kLag + kLift))) continue;
+            }
             float mx = kNegInf;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {

@@ -48,15 +48,6 @@ __device__ __forceinline__ f16v mfma32(const u4& x, const h8& y, const f16v& c) 
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, x), y, c, 0, 0, 0);
 }
 
-// top: the largest of the powers seen so far, with those of the lanes now.
-__device__ __forceinline__ void raise_top(float& top, float power) {
-  if (__ballot(power > top)) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) power = fmaxf(power, __shfl_xor(power, d));
-    top = fmaxf(top, __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, power))));
-  }
-}
-
 template <int D>
 __global__ __launch_bounds__(64 * kChunkWaves, 2) void kv_chunk_kernel(KvAttnArgs a, int rtiles) {
   constexpr int NC = D / 8;            // chunks of a decoded row
@@ -122,7 +113,7 @@ __global__ __launch_bounds__(64 * kChunkWaves, 2) void kv_chunk_kernel(KvAttnArg
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
   float m = kNegInf, l = 0.0f;  // weights are 2^(score - m); m follows the largest score + V scale's power
-  float v_top = -64.0f;         // the largest such power so far
+  float v_top = kNoPower;       // the largest such power so far
 
   // the thread's part of a tile: NW words of token t0, from chunk j0 on
   const int own = threadIdx.x / TPT, j0 = threadIdx.x % TPT * NW;
@@ -164,9 +155,10 @@ __global__ __launch_bounds__(64 * kChunkWaves, 2) void kv_chunk_kernel(KvAttnArg
     }
     if (j0 == 0) {
       float* mt = meta + buf * kMeta + t0;
+      const float v = f16_bits_to_f32((uint16_t)vs);
       mt[0] = ok ? f16_bits_to_f32((uint16_t)ks) : 0.0f;
-      mt[kTok] = ok ? f16_bits_to_f32((uint16_t)vs) : 0.0f;
-      mt[2 * kTok] = ok ? scale_power(vs) : kGone;
+      mt[kTok] = ok ? v : 0.0f;
+      mt[2 * kTok] = ok ? scale_power(v) : kGone;
     }
   };
   // the lane's places in a tile: of K, chunk hf of token r (chunk 2 j + hf: bits of
@@ -183,7 +175,7 @@ __global__ __launch_bounds__(64 * kChunkWaves, 2) void kv_chunk_kernel(KvAttnArg
     const float* mt = meta + buf * kMeta;
     const float power = mt[2 * kTok + lane];
     const uint64_t gone = __ballot(power == kGone);
-    raise_top(v_top, power == kGone ? -64.0f : power);
+    raise_top(v_top, power == kGone ? kNoPower : power);
     int k0 = kat, v0 = vat;  // turned here: held, the places of all steps would fill the registers
     asm volatile("" : "+v"(k0), "+v"(v0));
     f16v s[2];
@@ -222,11 +214,11 @@ __global__ __launch_bounds__(64 * kChunkWaves, 2) void kv_chunk_kernel(KvAttnArg
     for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[tb][i]);
-    mx = __builtin_fmaf(max_over_halves(mx), f, v_top) - kLift;
+    mx = __builtin_fmaf(max_over_halves(mx), f, v_top);
     // that bounds score + power of every token; only where the bound calls for a new
     // reference point is the largest sum itself taken, token by token (taken always, 631
     // us in turn with 605)
-    if (__ballot(mx > m + kLag)) {
+    if (__ballot(mx > m + (kLag + kLift))) {
       mx = kNegInf;
 #pragma unroll
       for (int tb = 0; tb < 2; ++tb)

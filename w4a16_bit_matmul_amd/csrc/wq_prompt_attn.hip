@@ -20,7 +20,7 @@
 // instructions of full rate: off by half a step of themselves (bf16 2^-8, fp16 2^-11) in
 // a sum of hundreds of them.  fp16 ones would be subnormal from 2^-14 of the largest on,
 // and behind a key that takes the weight and has little value, as a first token often is,
-// all of the output comes from such; so the reference point lies kLift below the
+// all of the output comes from such; so their reference point lies kLift below the
 // largest score, which keeps their bits down to 2^-21 of it (with the point at the
 // largest score, 3000 keys of weight e^-17 came out 43 % off).
 //
@@ -84,6 +84,12 @@ __device__ __forceinline__ int k_chunk(int t, int j) {
 template <int D>
 __device__ __forceinline__ int v_chunk(int t, int j) {
   return D == 64 ? j ^ ((t & 2) << 1) : j ^ ((t & 3) << 2);
+}
+
+// The reference point of weights whose largest score is mx (bf16 has fp32's exponents).
+template <bool BF>
+__device__ __forceinline__ float lowered(float mx) {
+  return BF ? mx : mx - kLift;
 }
 
 // First sequence whose slots start past i, less one: the sequence of slot i.
@@ -268,8 +274,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_attn_kernel(Prom
     for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[tb][i]);
-    mx = __builtin_fmaf(max_over_halves(mx), f, -kLift);
-    // the reference point in use may lag the true one by kLag: weights up to 2^(kLag + kLift)
+    mx = lowered<BF>(max_over_halves(mx) * f);
+    // the reference point in use may lag the true one by kLag: weights up to 2^kLag (bf16) or
+    // 2^(kLag + kLift)
     if (__ballot(mx > m + kLag)) {
       const float mn = fmaxf(m, mx);
       const float al = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
@@ -431,7 +438,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_split_kernel(Pro
     float mx = kNegInf;
 #pragma unroll
     for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[i]);
-    mx = __builtin_fmaf(max_over_halves(mx), f, -kLift);
+    mx = lowered<BF>(max_over_halves(mx) * f);
     if (__ballot(mx > m + kLag)) {
       const float mn = fmaxf(m, mx);
       const float al = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
