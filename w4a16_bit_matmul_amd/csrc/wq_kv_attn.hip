@@ -48,8 +48,8 @@
 // units are shared out equally; units that end up in several workgroups leave fp32
 // results which a second kernel joins.
 //
-// 64 contexts of 4-8K tokens, 64 / 8 heads of 128: the walk 97 us, 4.3 TB/s (a copy
-// reaches 5.0, reads alone 6.2-7.0; vector units 43 % and matrix cores 11 % busy),
+// 64 contexts of 4-8K tokens, 64 / 8 heads of 128: the walk 95-102 us, 4.3 TB/s (a copy
+// reaches 5.0, reads alone 6.2-7.0; vector units 44 % and matrix cores 12 % busy),
 // the join 8.  One of 131072: 35 and 6 us.  One of 201 tokens: 7 us, all latency.  With
 // 9-16 rows of heads of 64 a wave takes half a line and another workgroup the other:
 // 16 contexts of 1-9K, 25 us and 5, half of the 25 for the second reading.
@@ -91,7 +91,7 @@ KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_q
   p.grid = (int64_t)B * Hkv * p.rtiles;
   p.flat = false;
   // Tiles of 128 rows once two workgroups a CU come of it (512 tokens over 16K of one
-  // sequence, one a CU: 510 us, 455 with tiles of 32 rows; of two sequences 585 and
+  // sequence, one a CU: 510 us, 455-465 with tiles of 32 rows; of two sequences 585 and
   // 789) and nearly all of their rows are used (64 sequences, 128 rows a head: 97 us
   // and 133; 72 rows: 91 and 75).  With heads of 256 (two sequences over 7-8K, 32 / 4
   // heads) 660 us and 588: decoded tiles of 128 KB leave it one workgroup a CU.
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
   // tokens each over 7-8K of two sequences, 32 / 4 heads: 639 us, 671 without).  Elsewhere
   // it costs as much as it saves (512 tokens over 16K of one sequence, 64 / 8 heads of 128:
   // 460 and 467; 4 contexts of up to 4K with 32 rows 28.1 and 27.0; one of 201 tokens 7.0
-  // and 6.8).
+  // and 6.8 us).
   constexpr bool kBounded = D == 256;
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4, ml = lane & 31;

@@ -15,8 +15,8 @@
 // product (tokens {8a + 4h .. + 3} of half h), and V^T comes out of the row-major
 // tile by ds_read_b64_tr_b16.
 //
-// Two sequences' next 512 tokens over 12-16K cached ones, 64 / 8 heads of 128: 588
-// us, 829 TFLOP/s (matrix instructions 36 % of the cycles, decoding and softmax 52 %),
+// Two sequences' next 512 tokens over 12-16K cached ones, 64 / 8 heads of 128: 582
+// us, 837 TFLOP/s (matrix instructions 36 % of the cycles, decoding and softmax 52 %),
 // where tiles of 32 rows decoded by each wave took 789.  256 rows a workgroup halve
 // the decoding again but tie eight waves together: 631 us where this took 583.
 #include "wq_attn.h"

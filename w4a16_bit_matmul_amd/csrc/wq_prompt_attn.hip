@@ -37,9 +37,9 @@
 // Bound by the matrix cores for long prompts: 8K tokens with 64 / 8 heads of 128 in
 // 1.1 ms, 980-1,020 TFLOP/s (a library product of bf16 reaches 1,415 in a burst), matrix
 // instructions half of the cycles and the softmax a third; with heads of 64 the
-// softmax comes first (16 prompts of up to 1500: 68 us, 545 TFLOP/s); short prompts
-// are bound by the latency of a workgroup's start (48 of up to 300 tokens: 78-84 us,
-// 3.2-3.4 TB/s).  Two workgroups a CU: while one waits the other works.  128 rows keep
+// softmax comes first (16 prompts of up to 1500: 66 us, 556 TFLOP/s); short prompts
+// are bound by the latency of a workgroup's start (48 of up to 300 tokens: 77-84 us,
+// 3.2-3.5 TB/s).  Two workgroups a CU: while one waits the other works.  128 rows keep
 // four waves in step; 256, or two groups of four waves half a tile apart (one
 // multiplies while the other takes its softmax), measured 1,200 and 1,316 us where
 // the kernel of that time took 1,183.
@@ -250,7 +250,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void prompt_attn_kernel(Prom
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb) s[tb] = mfma32<BF>(kd[32 * tb * NC + kat[j]], qf[j], s[tb]);
     // three steps' reads ahead of the products (left alone, a read waits for the
-    // products before it: 4K tokens with 32 / 4 heads of 256 450 us, 416 so; 8K with 64 / 8
+    // products before it: 4K tokens with 32 / 4 heads of 256 450 us, 416 so (408 now); 8K with 64 / 8
     // of 128 1240, 1224)
     constexpr int kAhead = 3 * TB;
     __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
