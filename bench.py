@@ -8,7 +8,9 @@ consecutive steps never find them in the 256 MB last-level cache.
 
 value = effective GB/s = algorithmic bytes (4-bit codes + fp16 scales + 4-bit
 zero-points + fp16 x + fp16 y) / time per step.  The M=128 GEMM (TFLOP/s), the
-quantization kernel and the CPU oracle are reported alongside in the same line.
+quantization kernel, the matrix-core and the read ceilings are reported alongside
+in the same line; every workload, the other formats and the CPU oracle in a
+"details" record on stderr.
 
 Usage: python bench.py [--gpus 1] [--steps 200] [--warmup 200]
 """
@@ -27,6 +29,7 @@ sys.path.insert(0, ROOT)
 
 HBM_PEAK_GBS = 8000.0           # MI355X HBM3E, AMD published
 FP16_PEAK_TFLOPS = 2516.6       # MI355X dense fp16 MFMA, AMD published (256 CU x 4096 FLOP/clk x 2.4 GHz)
+DETAILS = ("configs", "w8a16", "kv_int4", "awq_fold", "mxfp4", "nvfp4", "cpu_baseline")  # figures printed on stderr
 METRIC = "W4A16 GEMV effective HBM GB/s (% of peak) at M=1; GEMM TFLOP/s at M=128"
 ROTATE_BYTES = 1024 << 20  # four times the 256 MB last-level cache
 SETTLE_MS = 100.0          # untimed back-to-back launches before the headline's warm-up steps
@@ -853,6 +856,11 @@ def main():
         line["read_ceiling"]["gemv_frac_of_ceiling"] = round(line["read_ceiling"]["us_per_launch"] / (t_step * 1e6), 4)
     if not args.no_cpu_baseline:
         line["cpu_baseline"] = cpu_baseline()
+    # the headline line stays short enough (4 KB of 23) to be kept whole by whoever captures
+    # it; the figures of every workload go to stderr, as one JSON record as well
+    details = {k: line.pop(k) for k in DETAILS if k in line}
+    if details:
+        log("[bench] details " + json.dumps(details))
     print(json.dumps(line), flush=True)
 
 
