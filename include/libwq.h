@@ -611,6 +611,121 @@ size_t wq_kv_attention_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int64_
 int wq_kv_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size, int64_t max_context,
                          int64_t max_queries, char* buf, size_t buf_len);
 
+/* ---- A step of speculative decoding over the INT4 KV cache ---------------------
+ * A sequence's last token and the tokens drafted after it are its nodes: n tokens
+ * that go through the model together, in one call each of the following, in this
+ * order.  The conventions of the attention calls above hold: dtype, heads, strides,
+ * pages (block_table, context_lens, page_size), limits, errors, determinism and
+ * capture into graphs.  Sequence b's nodes are tokens q_starts[b] .. q_starts[b + 1]
+ * - 1 of the call (device int32 [B + 1], increasing; NULL: one token a sequence, T ==
+ * B), and the last n of its context_lens[b] cached tokens: node i is its token
+ * context_lens[b] - n + i.  Tokens of the call outside every sequence are neither
+ * computed nor written. */
+
+/* The rotation of queries and keys and the quantization of keys and values into the
+ * cache's pages, in one pass: for a head row x of q or k,
+ *   n = x r w with r = 1 / sqrt(mean(x^2) + eps) where norm is 1 (w: q_weight or
+ *       k_weight [D], or NULL for ones), n = x where norm is 0;
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for the rot / 2 pairs of its first rot
+ *       values (pairs, tables and rot as in wq_qk_norm_rope);
+ *   rounded to dtype: q_out, k_out.
+ * Keys so rounded and the values v are quantized as wq_kv_quantize would, into the
+ * token's cache row.  Every step is one correctly rounded fp32 operation (the mean of
+ * squares the fp32 rounding of a 64-bit sum), so the cache's bytes follow from the
+ * inputs; squares whose mean passes fp32's range (bf16 values from 2^64 on) give zeros.
+ *   q, q_out   may both be NULL: keys and values alone (Hq still a multiple of Hkv)
+ *   positions  device int32 [T], or NULL: the token's place in its sequence.  Outside
+ *              [0, P) it marks padding: nothing of that token is written
+ *   k_out      [T][Hkv][D], or NULL; an output may be its input (same pointer and stride)
+ * A token whose page does not exist (or lies past the table's width) has its q_out
+ * and k_out written and nothing cached; rows not named keep their contents.  Two
+ * tokens in one cache row leave a mixture of both there.  Preconditions as
+ * wq_kv_quantize, for the rotated keys and the values.  Hkv * D is a multiple of
+ * 128; caches' arrays as wq_kv_quantize writes them, codes 16-byte aligned, cos, sin
+ * and weights too. */
+int wq_kv_append(const void* q, const void* k, const void* v, int dtype, int64_t T, int Hq, int Hkv, int D,
+                 int64_t q_stride, int64_t k_stride, int64_t v_stride, int norm, const void* q_weight,
+                 const void* k_weight, float eps, const int32_t* positions, const float* cos, const float* sin, int64_t P,
+                 int rot, int interleaved, uint8_t* k_codes, uint16_t* k_s_f16, uint8_t* k_zpacked, uint8_t* v_codes,
+                 uint16_t* v_s_f16, uint8_t* v_zpacked, int64_t S, int64_t B, const int32_t* block_table,
+                 int64_t table_width, int page_size, const int32_t* context_lens, const int32_t* q_starts, void* q_out,
+                 void* k_out, int64_t q_out_stride, int64_t k_out_stride, void* stream);
+
+/* Attention over the INT4 KV cache for the nodes of draft trees: wq_kv_attention,
+ * but that node i sees, besides all tokens before its sequence's nodes, the nodes j
+ * whose bit is set in its mask:
+ *   tree_mask  device uint64 [T][mask_words], 8-byte aligned: bit j % 64 of word j / 64 of
+ *              a node's row (nodes from 64 * mask_words on are seen by none).  A node's
+ *              own bit and those of its ancestors, as a rule; any mask is allowed
+ * Where context_lens[b] is smaller than n, nodes whose token would lie before the
+ * first do not exist.  max_context, max_queries, lse, workspace (its size and plan as for
+ * wq_kv_attention with the same sizes) and errors as there; WQ_EINVAL also for a NULL
+ * mask, mask_words outside 1..65536 and max_queries above 64 * mask_words. */
+int wq_kv_tree_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D, int64_t q_stride,
+                         const uint8_t* k_codes, const uint16_t* k_s_f16, const uint8_t* k_zpacked,
+                         const uint8_t* v_codes, const uint16_t* v_s_f16, const uint8_t* v_zpacked, int64_t S, int64_t B,
+                         const int32_t* block_table, int64_t table_width, int page_size, const int32_t* context_lens,
+                         int64_t max_context, const int32_t* q_starts, int64_t max_queries, const uint64_t* tree_mask,
+                         int mask_words, float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Names the kernel instance and launch shape of that call (as wq_gemm_plan). */
+int wq_kv_tree_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size, int64_t max_context,
+                              int64_t max_queries, char* buf, size_t buf_len);
+
+/* Drafted tokens against the target's distributions.  Row i of a sequence's logits is
+ * what the target says after its node i; at temperature t > 0 that is p(x) = w(x) / sum w
+ * with w(x) = exp((l(x) - max l) / t), and a token is taken from it with a number u in
+ * [0, 1): the first x whose cumulated weight w(0) + .. + w(x) is above u sum w (the
+ * last x with any weight where rounding leaves none).  At t = 0 (or a t that is not
+ * above 0) it is the likeliest token, the lowest of equals.  Logits of -inf have weight 0; a row
+ * without a finite maximum, or with a NaN or +inf, is no distribution: it gives token -1.
+ *   draft_logits NULL: the drafts are given tokens in a tree.  The root, node 0, is
+ * accepted; every row's token is taken with its own uniform[]; a node is accepted if its
+ * parent is and its token is the one that the parent's row gave (the first such child).
+ *   draft_logits [T][V] (parents NULL): a chain drawn from a draft model; row i is what
+ * node i + 1's token was drawn from (a sequence's last row is not read).  Node i + 1 is
+ * accepted if uniform[] of it times q(x) is below p(x), p and q of row i at the
+ * sequence's temperature; the first refusal ends the way with a token from max(p - q, 0)
+ * (from p, if that is 0 everywhere), the chain's end with one from p, both taken with
+ * uniform[] of the root.  At t = 0 a node is accepted if its token is the likeliest.
+ *   logits     [T][V] WQ_F32, WQ_BF16 or WQ_F16, rows at a stride of at least V values, of any
+ *              alignment that the type has; draft_logits alike, of the same type
+ *   tokens     device int32 [T] (a root's is not read); parents int32 [T], a node's parent
+ *              among its sequence's nodes, smaller than itself (others are never
+ *              reached), or NULL: each node's is the one before it
+ *   uniform    fp32 [T]; temperature fp32 [B], or NULL: 1
+ *   out_tokens, path int32 [B][max_queries], counts int32 [B]: counts[b] nodes are accepted,
+ *              path holds them in order (the root first), out_tokens the tokens of all
+ *              but the root and then the one taken last; -1 behind.  A sequence
+ *              without nodes: 0
+ * Of each sequence the first max_queries (1..1024) nodes count.  Weights and sums are
+ * 64-bit, in a fixed order.  Limits: V up to 2^24, 2^24 workgroups of 8192 logits.
+ *   workspace  wq_verify_drafts_workspace_bytes bytes, 256-byte aligned; as for
+ *              wq_kv_attention.
+ * WQ_EINVAL, WQ_EALIGN, WQ_EWORKSPACE as elsewhere; WQ_EUNSUPPORTED for draft_logits with
+ * parents, for larger max_queries or V and for more workgroups. */
+int wq_verify_drafts(const void* logits, int dtype, int64_t T, int64_t V, int64_t stride, const void* draft_logits,
+                     int64_t draft_stride, int64_t B, const int32_t* q_starts, int64_t max_queries,
+                     const int32_t* tokens, const int32_t* parents, const float* uniform, const float* temperature,
+                     int32_t* out_tokens, int32_t* path, int32_t* counts, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* Workspace bytes of that call (drafts: 1 with draft_logits; 0 for sizes it would
+ * refuse).  Host-only. */
+size_t wq_verify_drafts_workspace_bytes(int64_t T, int64_t V, int64_t B, int drafts);
+
+/* Moves the cache rows of accepted nodes together: for j below counts[b], the row
+ * (K's and V's codes, scales and zero-points) of node path[b][j] becomes that of node j, so that the
+ * accepted tokens are the first counts[b] behind the context.  path int32 [B][path_width] as
+ * wq_verify_drafts writes it: entries below j, or of no node, move nothing; all reads see the
+ * rows as they were.  S rows of hd values (a multiple of 128, up to 2^23); pages that do
+ * not exist neither give nor take a row.  context_lens is not changed. */
+int wq_kv_keep(uint8_t* k_codes, uint16_t* k_s_f16, uint8_t* k_zpacked, uint8_t* v_codes, uint16_t* v_s_f16,
+               uint8_t* v_zpacked, int64_t S, int64_t hd, int64_t T, int64_t B, const int32_t* block_table,
+               int64_t table_width, int page_size, const int32_t* context_lens, const int32_t* q_starts,
+               const int32_t* path, int64_t path_width, const int32_t* counts, void* stream);
+
 /* ---- Streaming-read probe (a measurement aid, not a step of the method) -----
  * A decode product's time is the reading of its weights ("Hardware, formats
  * and the roofline": decode is bound by memory bandwidth), so the rate at which

@@ -62,6 +62,8 @@ EXPORTED = (
     "wq_kv_layout_bytes", "wq_kv_quantize", "wq_kv_dequant",
     "wq_qk_norm_rope", "wq_prompt_attention", "wq_kv_attention", "wq_kv_attention_workspace_bytes",
     "wq_kv_attention_plan",
+    "wq_kv_append", "wq_kv_tree_attention", "wq_kv_tree_attention_plan", "wq_verify_drafts",
+    "wq_verify_drafts_workspace_bytes", "wq_kv_keep",
     "wq_quantize_groups_scaled", "wq_scale_activations", "wq_channel_absmean",
     "wq_layout_bytes_mxfp4", "wq_quantize_mxfp4", "wq_pack_mxfp4", "wq_dequant_mxfp4",
     "wq_gemm_mxfp4_workspace_bytes", "wq_gemm_mxfp4", "wq_gemm_mxfp4_ex", "wq_gemm_mxfp4_plan",
@@ -121,6 +123,14 @@ def lib() -> ctypes.CDLL:
                                 P, P, SZ, P]),
         "wq_kv_attention_workspace_bytes": (SZ, [I64, I, I, I, I64, I, I64, I64]),
         "wq_kv_attention_plan": (I, [I64, I, I, I, I64, I, I64, I64, ctypes.c_char_p, SZ]),
+        "wq_kv_append": (I, [P, P, P, I, I64, I, I, I, I64, I64, I64, I, P, P, F, P, P, P, I64, I, I, P, P, P, P, P, P, I64,
+                             I64, P, I64, I, P, P, P, P, I64, I64, P]),
+        "wq_kv_tree_attention": (I, [P, I, I64, I, I, I, I64, P, P, P, P, P, P, I64, I64, P, I64, I, P, I64, P, I64, P, I,
+                                     F, P, P, P, SZ, P]),
+        "wq_kv_tree_attention_plan": (I, [I64, I, I, I, I64, I, I64, I64, ctypes.c_char_p, SZ]),
+        "wq_verify_drafts": (I, [P, I, I64, I64, I64, P, I64, I64, P, I64, P, P, P, P, P, P, P, P, SZ, P]),
+        "wq_verify_drafts_workspace_bytes": (SZ, [I64, I64, I64, I]),
+        "wq_kv_keep": (I, [P, P, P, P, P, P, I64, I64, I64, I64, P, I64, I, P, P, P, I64, P, P]),
         "wq_quantize_groups_scaled": (I, [P, I, I64, I64, I, I, P, P, P, P, P, P, P]),
         "wq_scale_activations": (I, [P, I64, I64, P, P, P]),
         "wq_channel_absmean": (I, [P, I64, I64, P, P]),
@@ -639,6 +649,26 @@ def wq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_s
     return out if lse is None else (out, lse)
 
 
+def _caches(k_cache: KVCache, v_cache: KVCache, dev: torch.device) -> list:
+    """The addresses of a K and a V cache's arrays (of the same sizes, on dev)."""
+    S, hd = k_cache.S, k_cache.hd
+    nb, kv = hd // 128, []
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        kv += (_dev_array(name + ".codes", c.codes, torch.uint8, (S, hd // 2), dev),
+               _dev_array(name + ".s", c.s, torch.float16, (S, nb), dev),
+               _dev_array(name + ".zpacked", c.zpacked, torch.uint8, (S, (nb + 1) // 2), dev))
+    return kv
+
+
+def _pages(block_table: torch.Tensor, context_lens: torch.Tensor, dev: torch.device):
+    """Sequences, the table's width, and the addresses of table and lengths."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [sequences][pages]")
+    B, width = block_table.shape
+    return (B, width, _dev_array("block_table", block_table, torch.int32, (B, width), dev),
+            _dev_array("context_lens", context_lens, torch.int32, (B,), dev))
+
+
 def wq_kv_attention_workspace_bytes(T: int, Hq: int, Hkv: int, D: int, B: int, page_size: int, max_context: int,
                                     max_queries: int = 1) -> int:
     """Bytes of the workspace that wq_kv_attention takes for these sizes (0: none
@@ -681,17 +711,9 @@ def wq_kv_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, block_t
     if (v_cache.S, v_cache.hd) != (S, hd) or hd % D != 0:
         raise ValueError(f"caches of {S} x {hd} and {v_cache.S} x {v_cache.hd} values, heads of {D}")
     Hkv = hd // D
-    dev, dt, nb = q.device, q.dtype, hd // 128
-    kv = []
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        kv += (_dev_array(name + ".codes", c.codes, torch.uint8, (S, hd // 2), dev),
-               _dev_array(name + ".s", c.s, torch.float16, (S, nb), dev),
-               _dev_array(name + ".zpacked", c.zpacked, torch.uint8, (S, (nb + 1) // 2), dev))
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [sequences][pages]")
-    B, width = block_table.shape
-    table = _dev_array("block_table", block_table, torch.int32, (B, width), dev)
-    lens = _dev_array("context_lens", context_lens, torch.int32, (B,), dev)
+    dev, dt = q.device, q.dtype
+    kv = _caches(k_cache, v_cache, dev)
+    B, width, table, lens = _pages(block_table, context_lens, dev)
     if q_starts is not None:
         starts = _dev_array("q_starts", q_starts, torch.int32, (B + 1,), dev)
         max_queries = T if max_queries is None else min(max_queries, T)
@@ -714,6 +736,232 @@ def wq_kv_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, block_t
                                None if lse is None else lse.data_ptr(), ws, wsb, s)
     _check(st, "wq_kv_attention")
     return out if lse is None else (out, lse)
+
+
+# ---- a step of speculative decoding over the INT4 KV cache -----------------------
+# A sequence's nodes are its last token and the tokens drafted after it: tokens
+# q_starts[b] .. q_starts[b+1] - 1 of a call and the last ones of its cached context.
+
+def wq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: KVCache, v_cache: KVCache, block_table: torch.Tensor,
+                 context_lens: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, *, page_size: int,
+                 q: torch.Tensor | None = None, q_starts: torch.Tensor | None = None,
+                 positions: torch.Tensor | None = None, norm: bool = False, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out: torch.Tensor | None = None, k_out=False, stream=None):
+    """Rotates q [T][Hq][D] (optional) and k [T][Hkv][D], bf16 or fp16, and writes k
+    so rotated and v into the INT4 caches, in one pass; slices of a fused projection
+    are fine.  norm=True takes the norm of every q and k head first (weights [D] or
+    None for ones).  Token i of sequence b's n is its cached token context_lens[b] - n + i
+    (int32 [B], this call's tokens counted), in row block_table[b][token // page_size]
+    * page_size + token % page_size; without q_starts (int32 [B+1]) each sequence has one.
+    positions: int32 [T] rows of the fp32 tables cos, sin [P][rot/2], default each
+    token's place in its sequence; a token with one outside the tables is padding and
+    nothing of it is written, one without a page is not cached.  q_out may be q
+    itself; k_out: False, True or a tensor (k itself).  Returns (q_out, k_out), None
+    for what was not asked for."""
+    ks, vs = _heads("k", k), _heads("v", v, k, k.shape[0])
+    T, Hkv, D = k.shape
+    if v.shape[1] != Hkv:
+        raise ValueError(f"k has {Hkv} heads, v {v.shape[1]}")
+    S, hd = k_cache.S, k_cache.hd
+    if (v_cache.S, v_cache.hd) != (S, hd) or hd != Hkv * D:
+        raise ValueError(f"caches of {S} x {hd} and {v_cache.S} x {v_cache.hd} values, {Hkv} heads of {D}")
+    dev, dt = k.device, k.dtype
+    Hq, qs, qos, kos = Hkv, 0, 0, Hkv * D
+    if q is not None:
+        qs, Hq = _heads("q", q, k, T), q.shape[1]
+        qos = Hq * D
+    if q_out is not None:
+        if q is None or q_out.shape[1] != Hq:
+            raise ValueError("q_out must have the heads of q")
+        qos = _heads("q_out", q_out, q, T)
+    if isinstance(k_out, torch.Tensor):
+        kos = _heads("k_out", k_out, k, T)
+        if k_out.shape[1] != Hkv:
+            raise ValueError(f"k_out has {k_out.shape[1]} heads, expected {Hkv}")
+    P, half = cos.shape
+    c, n = _dev_array("cos", cos, torch.float32, (P, half), dev), _dev_array("sin", sin, torch.float32, (P, half), dev)
+    pos = None if positions is None else _dev_array("positions", positions, torch.int32, (T,), dev)
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights are the norm's: pass norm=True")
+    qw = None if q_weight is None else _dev_array("q_weight", q_weight, dt, (D,), dev)
+    kw = None if k_weight is None else _dev_array("k_weight", k_weight, dt, (D,), dev)
+    kv = _caches(k_cache, v_cache, dev)
+    B, width, table, lens = _pages(block_table, context_lens, dev)
+    starts = None if q_starts is None else _dev_array("q_starts", q_starts, torch.int32, (B + 1,), dev)
+    with _on(dev, stream) as s:
+        if q is not None and q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if k_out is True:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        elif k_out is False:
+            k_out = None
+        st = (_lib or lib()).wq_kv_append(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), _DT16[dt], T, Hq, Hkv,
+                                          D, qs, ks, vs, 1 if norm else 0, qw, kw, eps, pos, c, n, P, 2 * half,
+                                          1 if interleaved else 0, *kv, S, B, table, width, page_size, lens, starts,
+                                          None if q is None else q_out.data_ptr(),
+                                          None if k_out is None else k_out.data_ptr(), qos, kos, s)
+    _check(st, "wq_kv_append")
+    return q_out, k_out
+
+
+def wq_kv_tree_attention_plan(T: int, Hq: int, Hkv: int, D: int, B: int, page_size: int, max_context: int,
+                              max_queries: int = 1) -> str:
+    buf = ctypes.create_string_buffer(256)
+    _check(lib().wq_kv_tree_attention_plan(T, Hq, Hkv, D, B, page_size, max_context, min(max_queries, T), buf, len(buf)),
+           "wq_kv_tree_attention_plan")
+    return buf.value.decode()
+
+
+def wq_kv_tree_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, block_table: torch.Tensor,
+                         context_lens: torch.Tensor, tree_mask: torch.Tensor, *, page_size: int,
+                         max_context: int | None = None, q_starts: torch.Tensor | None = None,
+                         max_queries: int | None = None, scale: float | None = None, out: torch.Tensor | None = None,
+                         lse=False, workspace: torch.Tensor | None = None, stream=None):
+    """Attention of the nodes of draft trees, q [T][Hq][D], over the INT4 caches: as
+    wq_kv_attention, but that a node sees, besides all tokens before its sequence's
+    nodes, those nodes whose bit is set in its row of tree_mask, int64 [T][words] (bit
+    j % 64 of word j // 64 for node j; its ancestors and itself, as a rule).  The other
+    arguments, the workspace (wq_kv_attention_workspace_bytes) and the result as there;
+    max_queries may be 64 times the words at most (its default: all T, or that)."""
+    qs = _heads("q", q)
+    T, Hq, D = q.shape
+    S, hd = k_cache.S, k_cache.hd
+    if (v_cache.S, v_cache.hd) != (S, hd) or hd % D != 0:
+        raise ValueError(f"caches of {S} x {hd} and {v_cache.S} x {v_cache.hd} values, heads of {D}")
+    Hkv = hd // D
+    dev, dt = q.device, q.dtype
+    kv = _caches(k_cache, v_cache, dev)
+    B, width, table, lens = _pages(block_table, context_lens, dev)
+    if tree_mask.dim() != 2:
+        raise ValueError("tree_mask must be [tokens][words]")
+    words = tree_mask.shape[1]
+    mask = _dev_array("tree_mask", tree_mask, torch.int64, (T, words), dev)
+    if q_starts is not None:
+        starts = _dev_array("q_starts", q_starts, torch.int32, (B + 1,), dev)
+        max_queries = min(T, 64 * words) if max_queries is None else min(max_queries, T)
+    else:
+        starts, max_queries = None, min(T, 1)
+    if max_context is None:
+        max_context = width * page_size
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    L = _lib or lib()
+    with _on(dev, stream) as s:
+        out, lse = _attn_out(q, out, lse)
+        if workspace is None:
+            need = L.wq_kv_attention_workspace_bytes(T, Hq, Hkv, D, B, page_size, max_context, max_queries)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        st = L.wq_kv_tree_attention(q.data_ptr(), _DT16[dt], T, Hq, Hkv, D, qs, *kv, S, B, table, width, page_size, lens,
+                                    max_context, starts, max_queries, mask, words, D ** -0.5 if scale is None else scale,
+                                    out.data_ptr(), None if lse is None else lse.data_ptr(), ws, wsb, s)
+    _check(st, "wq_kv_tree_attention")
+    return out if lse is None else (out, lse)
+
+
+def wq_verify_drafts_workspace_bytes(T: int, V: int, B: int, drafts: bool = False) -> int:
+    """Bytes of the workspace that wq_verify_drafts takes for these sizes (0: none
+    needed, or sizes it would refuse); drafts: with draft_logits."""
+    return int(lib().wq_verify_drafts_workspace_bytes(T, V, B, 1 if drafts else 0))
+
+
+def _rows(name: str, x: torch.Tensor) -> int:
+    """x is [T][V] with contiguous rows; its stride between them."""
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be [tokens][vocabulary] with contiguous rows (shape {tuple(x.shape)}, strides {x.stride()})")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def wq_verify_drafts(logits: torch.Tensor, tokens: torch.Tensor, uniform: torch.Tensor, *,
+                     q_starts: torch.Tensor | None = None, max_queries: int | None = None,
+                     parents: torch.Tensor | None = None, draft_logits: torch.Tensor | None = None,
+                     temperature: torch.Tensor | None = None, out_tokens: torch.Tensor | None = None,
+                     path: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """Drafted tokens against the target's distributions, logits [T][V] (float32, bf16
+    or fp16; row i of a sequence after its node i), with random numbers uniform [T] in
+    [0, 1).  tokens int32 [T]: the nodes' (a root's is not read).  Without draft_logits
+    the nodes form a tree of given tokens, parents int32 [T] (a node's parent among its
+    sequence's nodes; None: the one before): each row's token is taken with its own
+    uniform, and a node is accepted if its token is what its accepted parent's row gave.  With
+    draft_logits [T][V] they are a chain, each token drawn from the row before it at the
+    same temperature: accepted where uniform * q < p, the first refusal followed by a
+    token from max(p - q, 0).  temperature: float32 [B] (0: the likeliest token), or None
+    for 1.  Without q_starts (int32 [B+1]) every sequence has one row: plain
+    sampling.  Of each sequence the first max_queries nodes count (default: all T, at most
+    1024).  Returns (out_tokens, path, counts): int32 [B][max_queries] the tokens of the
+    accepted nodes behind the root and the token that follows them, the accepted nodes
+    (root first), -1 behind, and int32 [B] their number; a row that is no distribution
+    gives token -1."""
+    if logits.dtype not in _DT:
+        raise ValueError(f"logits must be float32, bfloat16 or float16 (got {logits.dtype})")
+    stride = _rows("logits", logits)
+    T, V = logits.shape
+    dev, dstride = logits.device, 0
+    if draft_logits is not None:
+        dstride = _rows("draft_logits", draft_logits)
+        if draft_logits.shape != logits.shape or draft_logits.dtype != logits.dtype or draft_logits.device != dev:
+            raise ValueError(f"draft_logits must be like logits (got {draft_logits.dtype}, shape {tuple(draft_logits.shape)}, "
+                             f"on {draft_logits.device})")
+    tok, u = _dev_array("tokens", tokens, torch.int32, (T,), dev), _dev_array("uniform", uniform, torch.float32, (T,), dev)
+    par = None if parents is None else _dev_array("parents", parents, torch.int32, (T,), dev)
+    if q_starts is None:
+        B, starts = T, None
+    else:
+        if q_starts.dim() != 1 or q_starts.numel() < 1:
+            raise ValueError("q_starts must hold B + 1 token numbers")
+        B = q_starts.numel() - 1
+        starts = _dev_array("q_starts", q_starts, torch.int32, (B + 1,), dev)
+    if max_queries is None:
+        max_queries = 1 if q_starts is None else min(max(T, 1), 1024)
+    temp = None if temperature is None else _dev_array("temperature", temperature, torch.float32, (B,), dev)
+    for name, t, shape in (("out_tokens", out_tokens, (B, max_queries)), ("path", path, (B, max_queries)), ("counts", counts, (B,))):
+        if t is not None:
+            _dev_array(name, t, torch.int32, shape, dev)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    L = _lib or lib()
+    with _on(dev, stream) as s:
+        if out_tokens is None:
+            out_tokens = torch.empty((B, max_queries), dtype=torch.int32, device=dev)
+        if path is None:
+            path = torch.empty((B, max_queries), dtype=torch.int32, device=dev)
+        if counts is None:
+            counts = torch.empty((B,), dtype=torch.int32, device=dev)
+        if workspace is None:
+            need = L.wq_verify_drafts_workspace_bytes(T, V, B, 0 if draft_logits is None else 1)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        st = L.wq_verify_drafts(logits.data_ptr(), _DT[logits.dtype], T, V, stride,
+                                None if draft_logits is None else draft_logits.data_ptr(), dstride, B, starts, max_queries, tok,
+                                par, u, temp, out_tokens.data_ptr(), path.data_ptr(), counts.data_ptr(), ws, wsb, s)
+    _check(st, "wq_verify_drafts")
+    return out_tokens, path, counts
+
+
+def wq_kv_keep(k_cache: KVCache, v_cache: KVCache, block_table: torch.Tensor, context_lens: torch.Tensor,
+               path: torch.Tensor, counts: torch.Tensor, *, page_size: int, q_starts: torch.Tensor, stream=None) -> None:
+    """Moves the cache rows of accepted nodes together: the rows of sequence b's nodes
+    path[b][0 .. counts[b] - 1] (int32, as wq_verify_drafts gives them) become those of its nodes
+    0 .. counts[b] - 1.  context_lens still counts all of the nodes, and is not changed."""
+    dev, hd = k_cache.codes.device, k_cache.hd
+    if (v_cache.S, v_cache.hd) != (k_cache.S, hd):
+        raise ValueError(f"caches of {k_cache.S} x {hd} and {v_cache.S} x {v_cache.hd} values")
+    kv = _caches(k_cache, v_cache, dev)
+    B, width, table, lens = _pages(block_table, context_lens, dev)
+    starts = _dev_array("q_starts", q_starts, torch.int32, (B + 1,), dev)
+    if path.dim() != 2:
+        raise ValueError("path must be [sequences][nodes]")
+    p = _dev_array("path", path, torch.int32, (B, path.shape[1]), dev)
+    n = _dev_array("counts", counts, torch.int32, (B,), dev)
+    with _on(dev, stream) as s:
+        # (how many tokens the call had is on the device: all that q_starts names)
+        st = (_lib or lib()).wq_kv_keep(*kv, k_cache.S, hd, (1 << 31) - 1, B, table, width, page_size, lens, starts, p,
+                                        path.shape[1], n, s)
+    _check(st, "wq_kv_keep")
 
 
 # ---- AWQ-style per-input-channel scaling ---------------------------------------

@@ -649,19 +649,22 @@ int wq_kv_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_
   return WQ_OK;
 }
 
-int wq_kv_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D, int64_t q_stride,
-                    const uint8_t* k_codes, const uint16_t* k_s_f16, const uint8_t* k_zpacked, const uint8_t* v_codes,
-                    const uint16_t* v_s_f16, const uint8_t* v_zpacked, int64_t S, int64_t B,
-                    const int32_t* block_table, int64_t table_width, int page_size, const int32_t* context_lens,
-                    int64_t max_context, const int32_t* q_starts, int64_t max_queries, float scale, void* out,
-                    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+namespace {
+
+// Checks a cache attention call and fills its arguments; 1: nothing to do.
+int check_kv_call(wq::KvAttnArgs* to, const void* q, int dtype, int64_t T, int Hq, int Hkv, int D, int64_t q_stride,
+                  const uint8_t* k_codes, const uint16_t* k_s_f16, const uint8_t* k_zpacked, const uint8_t* v_codes,
+                  const uint16_t* v_s_f16, const uint8_t* v_zpacked, int64_t S, int64_t B, const int32_t* block_table,
+                  int64_t table_width, int page_size, const int32_t* context_lens, int64_t max_context,
+                  const int32_t* q_starts, int64_t max_queries, float scale, void* out, float* lse, void* workspace,
+                  size_t workspace_bytes) {
   int st = check_kv_attn(dtype, T, Hq, Hkv, D, B, page_size, max_context, max_queries);
   if (st) return st;
   if (!good_scale(scale) || S <= 0 || S >= kMaxCount || table_width < 0 || table_width >= kMaxCount) return WQ_EINVAL;
   if (page_size > S) return WQ_EUNSUPPORTED;
   if (max_context > table_width * page_size) return WQ_EINVAL;
   if (!q_starts && (T != B || max_queries != (T > 0 ? 1 : 0))) return WQ_EINVAL;
-  if (T == 0 || B == 0 || max_queries == 0) return WQ_OK;
+  if (T == 0 || B == 0 || max_queries == 0) return 1;
   if (!q || !k_codes || !k_s_f16 || !k_zpacked || !v_codes || !v_s_f16 || !v_zpacked ||
       (!block_table && max_context > 0) || !context_lens || !out)
     return WQ_EINVAL;
@@ -676,10 +679,180 @@ int wq_kv_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D,
     if (!workspace || workspace_bytes < need) return WQ_EWORKSPACE;
     if (!aligned(workspace, 256)) return WQ_EALIGN;
   }
-  const wq::KvAttnArgs a{static_cast<const uint16_t*>(q), T, q_stride, dtype, Hq, Hkv, D, k_codes, k_s_f16, k_zpacked,
+  *to = wq::KvAttnArgs{static_cast<const uint16_t*>(q), T, q_stride, dtype, Hq, Hkv, D, k_codes, k_s_f16, k_zpacked,
                          v_codes, v_s_f16, v_zpacked, S, (int)B, block_table, table_width, page_size, context_lens,
-                         max_context, q_starts, max_queries, scale, static_cast<uint16_t*>(out), lse, workspace};
+                         max_context, q_starts, max_queries, scale, static_cast<uint16_t*>(out), lse, workspace, nullptr, 0};
+  return WQ_OK;
+}
+
+}  // namespace
+
+int wq_kv_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D, int64_t q_stride,
+                    const uint8_t* k_codes, const uint16_t* k_s_f16, const uint8_t* k_zpacked, const uint8_t* v_codes,
+                    const uint16_t* v_s_f16, const uint8_t* v_zpacked, int64_t S, int64_t B,
+                    const int32_t* block_table, int64_t table_width, int page_size, const int32_t* context_lens,
+                    int64_t max_context, const int32_t* q_starts, int64_t max_queries, float scale, void* out,
+                    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  wq::KvAttnArgs a;
+  const int st = check_kv_call(&a, q, dtype, T, Hq, Hkv, D, q_stride, k_codes, k_s_f16, k_zpacked, v_codes, v_s_f16,
+                               v_zpacked, S, B, block_table, table_width, page_size, context_lens, max_context, q_starts,
+                               max_queries, scale, out, lse, workspace, workspace_bytes);
+  if (st) return st < 0 ? st : WQ_OK;
   return hip_status(wq::launch_kv_attn(a, static_cast<hipStream_t>(stream)));
+}
+
+// ---- a step of speculative decoding over the INT4 KV cache ----------------------
+
+namespace {
+
+int log2_of(int page_size) { return 31 - __builtin_clz((unsigned)page_size); }
+
+// Pages of a cache of S rows as the append and keep calls take them.
+int check_pages(int64_t S, int64_t T, int64_t B, int64_t table_width, int page_size, const int32_t* q_starts) {
+  if (T < 0 || T >= kMaxCount || B < 0 || B > (1 << 24) || S <= 0 || S >= kMaxCount || table_width < 0 ||
+      table_width >= kMaxCount)
+    return WQ_EINVAL;
+  if (page_size < 1 || (page_size & (page_size - 1)) != 0 || page_size > S) return WQ_EUNSUPPORTED;
+  return !q_starts && T != B ? WQ_EINVAL : WQ_OK;
+}
+
+int check_caches(const void* kc, const void* ks, const void* kz, const void* vc, const void* vs, const void* vz) {
+  if (!kc || !ks || !kz || !vc || !vs || !vz) return WQ_EINVAL;
+  return !aligned(kc, 16) || !aligned(vc, 16) || !aligned(ks, 2) || !aligned(vs, 2) ? WQ_EALIGN : WQ_OK;
+}
+
+// Sizes of a verification.
+int check_verify(int64_t T, int64_t V, int64_t B, bool drafts) {
+  if (T < 0 || T >= kMaxCount || V <= 0 || B < 0 || B > (1 << 24)) return WQ_EINVAL;
+  if (V > (1 << 24)) return WQ_EUNSUPPORTED;
+  const int64_t C = wq::verify_chunks(V);
+  return (drafts ? 2 : 1) * T >= kMaxGrid / C || B >= kMaxGrid / C ? WQ_EUNSUPPORTED : WQ_OK;
+}
+
+}  // namespace
+
+int wq_kv_append(const void* q, const void* k, const void* v, int dtype, int64_t T, int Hq, int Hkv, int D,
+                 int64_t q_stride, int64_t k_stride, int64_t v_stride, int norm, const void* q_weight,
+                 const void* k_weight, float eps, const int32_t* positions, const float* cos, const float* sin, int64_t P,
+                 int rot, int interleaved, uint8_t* k_codes, uint16_t* k_s_f16, uint8_t* k_zpacked, uint8_t* v_codes,
+                 uint16_t* v_s_f16, uint8_t* v_zpacked, int64_t S, int64_t B, const int32_t* block_table,
+                 int64_t table_width, int page_size, const int32_t* context_lens, const int32_t* q_starts, void* q_out,
+                 void* k_out, int64_t q_out_stride, int64_t k_out_stride, void* stream) {
+  int st = check_heads(dtype, T, Hq, Hkv, D);
+  if (st) return st;
+  if ((norm != 0 && norm != 1) || !(eps >= 0.0f && eps <= 3.4028235e38f) || P <= 0 || P > kMaxCount ||
+      (interleaved != 0 && interleaved != 1))
+    return WQ_EINVAL;
+  if (rot <= 0 || rot > D || rot % 16 != 0 || ((int64_t)Hkv * D) % 128 != 0) return WQ_EUNSUPPORTED;
+  if ((st = check_pages(S, T, B, table_width, page_size, q_starts))) return st;
+  if (T == 0 || B == 0) return WQ_OK;
+  if (!k || !v || !cos || !sin || !context_lens || (!block_table && table_width > 0) || !q != !q_out) return WQ_EINVAL;
+  if ((st = check_caches(k_codes, k_s_f16, k_zpacked, v_codes, v_s_f16, v_zpacked))) return st;
+  if ((q && ((st = check_rows(q, q_stride, Hq, D)) || (st = check_rows(q_out, q_out_stride, Hq, D)))) ||
+      (st = check_rows(k, k_stride, Hkv, D)) || (st = check_rows(v, v_stride, Hkv, D)) ||
+      (k_out && (st = check_rows(k_out, k_out_stride, Hkv, D))))
+    return st;
+  if (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(positions, 4) || !aligned(q_weight, 16) ||
+      !aligned(k_weight, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(q_starts, 4))
+    return WQ_EALIGN;
+  if (wq::kv_append_waves(T, q ? Hq : 0, Hkv, D) >= 4 * kMaxGrid) return WQ_EUNSUPPORTED;
+  const wq::KvAppendArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
+                           static_cast<const uint16_t*>(v), T, q_stride, k_stride, v_stride, dtype, Hq, Hkv, D, norm,
+                           static_cast<const uint16_t*>(q_weight), static_cast<const uint16_t*>(k_weight), eps, positions,
+                           cos, sin, P, rot, interleaved, k_codes, k_s_f16, k_zpacked, v_codes, v_s_f16, v_zpacked,
+                           (int)B, block_table, table_width, log2_of(page_size), S >> log2_of(page_size), context_lens,
+                           q_starts, static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_out), q_out_stride,
+                           k_out_stride};
+  return hip_status(wq::launch_kv_append(a, static_cast<hipStream_t>(stream)));
+}
+
+int wq_kv_tree_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size, int64_t max_context,
+                              int64_t max_queries, char* buf, size_t buf_len) {
+  if (!buf || buf_len == 0) return WQ_EINVAL;
+  buf[0] = 0;
+  const int st = check_kv_attn(WQ_BF16, T, Hq, Hkv, D, B, page_size, max_context, max_queries);
+  if (st) return st;
+  if (T == 0 || B == 0 || max_queries == 0) return WQ_OK;
+  wq::describe_kv_tree((int)B, Hq, Hkv, D, page_size, max_context, max_queries, buf, buf_len);
+  return WQ_OK;
+}
+
+int wq_kv_tree_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D, int64_t q_stride,
+                         const uint8_t* k_codes, const uint16_t* k_s_f16, const uint8_t* k_zpacked,
+                         const uint8_t* v_codes, const uint16_t* v_s_f16, const uint8_t* v_zpacked, int64_t S, int64_t B,
+                         const int32_t* block_table, int64_t table_width, int page_size, const int32_t* context_lens,
+                         int64_t max_context, const int32_t* q_starts, int64_t max_queries, const uint64_t* tree_mask,
+                         int mask_words, float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  int st = check_kv_attn(dtype, T, Hq, Hkv, D, B, page_size, max_context, max_queries);
+  if (st) return st;
+  if (mask_words < 1 || mask_words > 65536 || max_queries > 64 * (int64_t)mask_words) return WQ_EINVAL;
+  if (!tree_mask && T > 0 && B > 0 && max_queries > 0) return WQ_EINVAL;
+  if (!aligned(tree_mask, 8)) return WQ_EALIGN;
+  wq::KvAttnArgs a;
+  st = check_kv_call(&a, q, dtype, T, Hq, Hkv, D, q_stride, k_codes, k_s_f16, k_zpacked, v_codes, v_s_f16, v_zpacked, S, B,
+                     block_table, table_width, page_size, context_lens, max_context, q_starts, max_queries, scale, out, lse,
+                     workspace, workspace_bytes);
+  if (st) return st < 0 ? st : WQ_OK;
+  a.tree = tree_mask;
+  a.tree_words = mask_words;
+  return hip_status(wq::launch_kv_tree(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t wq_verify_drafts_workspace_bytes(int64_t T, int64_t V, int64_t B, int drafts) {
+  return check_verify(T, V, B, drafts != 0) || T == 0 || B == 0 ? 0 : wq::verify_workspace_bytes(T, V, B, drafts != 0);
+}
+
+int wq_verify_drafts(const void* logits, int dtype, int64_t T, int64_t V, int64_t stride, const void* draft_logits,
+                     int64_t draft_stride, int64_t B, const int32_t* q_starts, int64_t max_queries,
+                     const int32_t* tokens, const int32_t* parents, const float* uniform, const float* temperature,
+                     int32_t* out_tokens, int32_t* path, int32_t* counts, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  if (dtype != WQ_F32 && dtype != WQ_BF16 && dtype != WQ_F16) return WQ_EINVAL;
+  int st = check_verify(T, V, B, draft_logits != nullptr);
+  if (st) return st;
+  if (max_queries < 1 || (!q_starts && T != B)) return WQ_EINVAL;
+  if (max_queries > 1024 || (draft_logits && parents)) return WQ_EUNSUPPORTED;
+  if (B == 0) return WQ_OK;
+  if (!out_tokens || !path || !counts) return WQ_EINVAL;
+  if (T > 0 && (!logits || !tokens || !uniform || stride < V || stride >= (int64_t(1) << 32) ||
+                (draft_logits && (draft_stride < V || draft_stride >= (int64_t(1) << 32)))))
+    return WQ_EINVAL;
+  const int size = dtype == WQ_F32 ? 4 : 2;
+  if (!aligned(logits, size) || !aligned(draft_logits, size) || !aligned(q_starts, 4) || !aligned(tokens, 4) ||
+      !aligned(parents, 4) || !aligned(uniform, 4) || !aligned(temperature, 4) || !aligned(out_tokens, 4) ||
+      !aligned(path, 4) || !aligned(counts, 4))
+    return WQ_EALIGN;
+  const size_t need = wq_verify_drafts_workspace_bytes(T, V, B, draft_logits != nullptr);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return WQ_EWORKSPACE;
+    if (!aligned(workspace, 256)) return WQ_EALIGN;
+  }
+  const wq::VerifyArgs a{logits, draft_logits, dtype, T, V, stride, draft_stride, (int)B, q_starts, max_queries, tokens,
+                         parents, uniform, temperature, out_tokens, path, counts, workspace};
+  return hip_status(wq::launch_verify(a, static_cast<hipStream_t>(stream)));
+}
+
+int wq_kv_keep(uint8_t* k_codes, uint16_t* k_s_f16, uint8_t* k_zpacked, uint8_t* v_codes, uint16_t* v_s_f16,
+               uint8_t* v_zpacked, int64_t S, int64_t hd, int64_t T, int64_t B, const int32_t* block_table,
+               int64_t table_width, int page_size, const int32_t* context_lens, const int32_t* q_starts,
+               const int32_t* path, int64_t path_width, const int32_t* counts, void* stream) {
+  int st = check_pages(S, T, B, table_width, page_size, q_starts);
+  if (st) return st;
+  if (hd <= 0 || hd > (1 << 23) || path_width < 0 || path_width >= kMaxCount) return WQ_EINVAL;
+  if (hd % 128 != 0) return WQ_EUNSUPPORTED;
+  if (T == 0 || B == 0 || path_width == 0) return WQ_OK;
+  if ((st = check_caches(k_codes, k_s_f16, k_zpacked, v_codes, v_s_f16, v_zpacked))) return st;
+  if ((!block_table && table_width > 0) || !context_lens || !path || !counts) return WQ_EINVAL;
+  if (!aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(q_starts, 4) || !aligned(path, 4) ||
+      !aligned(counts, 4))
+    return WQ_EALIGN;
+  const int nb = (int)(hd / 128);
+  if (2 * B * wq::kv_keep_blocks(nb) >= kMaxGrid) return WQ_EUNSUPPORTED;
+  const wq::KvKeepArgs a{k_codes, k_s_f16, k_zpacked, v_codes, v_s_f16, v_zpacked, nb, (int)B, block_table, table_width,
+                         log2_of(page_size), S >> log2_of(page_size), context_lens, q_starts, T, path, (int)path_width,
+                         counts};
+  return hip_status(wq::launch_kv_keep(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -51,6 +51,40 @@ __device__ __forceinline__ int length_of(const KvAttnArgs& a, int b) {
   return (int)max((int64_t)0, min((int64_t)a.lens[b], a.max_context));
 }
 
+// The sequence that holds token t, its first token, and how many it has; none: b < 0.
+struct Place {
+  int b, q0, n;
+};
+__device__ __forceinline__ Place place_of(const int32_t* starts, int B, int64_t T, int t, int lane) {
+  if (!starts) return {t < B ? t : -1, t, 1};
+  // the last of the starts 0..B that is not above t: 64 probes at a time
+  int lo = 0, len = B + 1, c;
+  while (true) {
+    const int step = (len + 63) / 64;
+    const int at = lo + min(lane * step, len - 1);
+    c = __popcll(__ballot(lane * step < len && starts[at] <= t));
+    if (c == 0) return {-1, 0, 0};
+    lo += (c - 1) * step;
+    len = min(step, len - (c - 1) * step);
+    if (step == 1) break;
+  }
+  if (lo >= B) return {-1, 0, 0};
+  const int q0 = max(starts[lo], 0);
+  return {lo, q0, (int)(min((int64_t)starts[lo + 1], T) - q0)};
+}
+
+// Bit i: node `node` (a query of the call) sees the token `rel` + i places behind
+// its sequence's first node: all before that one, then as its mask words say.
+__device__ __forceinline__ uint64_t tree_window(const KvAttnArgs& a, int node, int rel) {
+  if (rel <= -64) return ~0ull;
+  const uint64_t* w = a.tree + (int64_t)node * a.tree_words;
+  if (rel < 0) return w[0] << -rel | ~(~0ull << -rel);
+  const int i = rel >> 6, s = rel & 63;
+  uint64_t v = i < a.tree_words ? w[i] >> s : 0;
+  if (s && i + 1 < a.tree_words) v |= w[i + 1] << (64 - s);
+  return v;
+}
+
 // fp32 pair -> 16-bit pair, round to nearest even
 template <bool BF>
 __device__ __forceinline__ uint32_t pack_pair(float x, float y) {

@@ -117,6 +117,8 @@ struct KvAttnArgs {
   uint16_t* out;
   float* lse;
   void* workspace;
+  const uint64_t* tree;  // [T][tree_words] masks of the nodes (launch_kv_tree)
+  int tree_words;
 };
 size_t kv_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_queries);
 int describe_kv_attn(int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries, char* buf,
@@ -126,6 +128,83 @@ hipError_t launch_kv_attn(const KvAttnArgs& a, hipStream_t stream);
 // rows of a KV head each.
 constexpr int kChunkWaves = 4;
 hipError_t launch_kv_chunk(const KvAttnArgs& a, int64_t grid, int rtiles, hipStream_t stream);
+
+// The same for the nodes of draft trees (wq_kv_tree.hip): plans and workspaces as above.
+int describe_kv_tree(int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries, char* buf,
+                     size_t len);
+hipError_t launch_kv_tree(const KvAttnArgs& a, hipStream_t stream);
+
+// Rotation (and norm) of queries and keys and quantization of keys and values into
+// cache pages (wq_kv_append.hip).  q NULL: keys and values alone; k_out may be NULL.
+struct KvAppendArgs {
+  const uint16_t *q, *k, *v;
+  int64_t T, q_stride, k_stride, v_stride;
+  int dtype, Hq, Hkv, D, norm;
+  const uint16_t *q_weight, *k_weight;
+  float eps;
+  const int32_t* positions;
+  const float *cos, *sin;
+  int64_t P;
+  int rot, interleaved;
+  uint8_t* k_codes;
+  uint16_t* k_s;
+  uint8_t* k_zp;
+  uint8_t* v_codes;
+  uint16_t* v_s;
+  uint8_t* v_zp;
+  int B;
+  const int32_t* table;
+  int64_t table_width;
+  int lg;         // log2 of the page size
+  int64_t pages;  // of the cache
+  const int32_t* lens;
+  const int32_t* q_starts;
+  uint16_t *q_out, *k_out;
+  int64_t qo_stride, ko_stride;
+};
+int64_t kv_append_waves(int64_t T, int Hq, int Hkv, int D);
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t stream);
+
+// Cache rows of accepted nodes moved together (wq_kv_append.hip); nb: blocks of a row.
+struct KvKeepArgs {
+  uint8_t* k_codes;
+  uint16_t* k_s;
+  uint8_t* k_zp;
+  uint8_t* v_codes;
+  uint16_t* v_s;
+  uint8_t* v_zp;
+  int nb, B;
+  const int32_t* table;
+  int64_t table_width;
+  int lg;
+  int64_t pages;
+  const int32_t* lens;
+  const int32_t* q_starts;
+  int64_t T;
+  const int32_t* path;
+  int width;
+  const int32_t* counts;
+};
+int kv_keep_blocks(int nb);  // workgroups of a sequence and cache
+hipError_t launch_kv_keep(const KvKeepArgs& a, hipStream_t stream);
+
+// Drafted tokens against the target's distributions (wq_verify.hip).  dtype 0 fp32,
+// 1 bf16, 2 fp16; strides in values between rows of logits.
+struct VerifyArgs {
+  const void *logits, *draft;
+  int dtype;
+  int64_t T, V, stride, draft_stride;
+  int B;
+  const int32_t* q_starts;
+  int64_t max_queries;
+  const int32_t *tokens, *parents;
+  const float *uniform, *temperature;
+  int32_t *out_tokens, *path, *counts;
+  void* workspace;
+};
+int verify_chunks(int64_t V);  // workgroups of a row
+size_t verify_workspace_bytes(int64_t T, int64_t V, int64_t B, bool draft);
+hipError_t launch_verify(const VerifyArgs& a, hipStream_t stream);
 
 // Causal attention over packed prompts (wq_prompt_attn.hip).
 struct PromptAttnArgs {
