@@ -726,7 +726,8 @@ int check_verify(int64_t T, int64_t V, int64_t B, bool drafts) {
   if (T < 0 || T >= kMaxCount || V <= 0 || B < 0 || B > (1 << 24)) return WQ_EINVAL;
   if (V > (1 << 24)) return WQ_EUNSUPPORTED;
   const int64_t C = wq::verify_chunks(V);
-  return (drafts ? 2 : 1) * T >= kMaxGrid / C || B >= kMaxGrid / C ? WQ_EUNSUPPORTED : WQ_OK;
+  // workgroups of four chunks
+  return (drafts ? 2 : 1) * T >= 4 * kMaxGrid / C || B >= kMaxGrid / ((C + 3) / 4) ? WQ_EUNSUPPORTED : WQ_OK;
 }
 
 }  // namespace

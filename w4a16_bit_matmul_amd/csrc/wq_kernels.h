@@ -202,7 +202,7 @@ struct VerifyArgs {
   int32_t *out_tokens, *path, *counts;
   void* workspace;
 };
-int verify_chunks(int64_t V);  // workgroups of a row
+int verify_chunks(int64_t V);  // waves of a row
 size_t verify_workspace_bytes(int64_t T, int64_t V, int64_t B, bool draft);
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t stream);
 

@@ -15,247 +15,329 @@
 //
 // Which token that is changes where a cumulated weight passes u sum w, so weights and
 // sums are 64-bit: with 100,000 tokens, 2^-24 of error in the sums would move one
-// pick in a few hundred, 2^-50 none in 10^9.  The 64-bit exponential is 2^f by a
-// polynomial of degree 10 on [-1/2, 1/2] (Chebyshev interpolation, 3e-16 off) times
-// 2^n; 64-bit operations have the rate of 32-bit ones here.
+// pick in a few hundred, 2^-45 none in 10^8.  The 64-bit exponential is 2^f by a
+// polynomial on [-1/2, 1/2] (Chebyshev interpolation) times 2^n; 64-bit operations
+// have the rate of 32-bit ones here.
 //
-// A row is cut into chunks of kChunk logits.  The first kernel reads all rows once:
-// each chunk's maximum and its sum of weights relative to that.  The next ones join
-// them, find the chunk in which a row's threshold falls, and read that chunk again.
+// A row is cut into chunks of kChunk logits, a wave's.  The first kernel reads all rows
+// once and leaves each chunk's maximum and its sum of weights relative to that; it is
+// bound by the exponentials, 17 instructions a logit.  The next ones join the chunks of a row,
+// find the one in which the row's threshold falls, and read a quarter of that again.
 // Every sum has a fixed order.
 #include "wq_attn.h"
 
 namespace wq {
 namespace {
 
-constexpr int kChunk = 8192;
+constexpr int kChunk = 2048;
+constexpr int kFewNodes = 64;    // trees that one workgroup takes
+constexpr int kFewDrafts = 16;   // chains whose rows every workgroup joins for itself
 
-struct Partial {  // of a chunk: sum of weights relative to max, first token with max
+struct Partial {  // of a chunk: sum of weights relative to max, first token with max (greedy)
   double sum;
   float max;
   int top;
 };
+struct Quarters {  // the sum, by quarters of the chunk
+  double sum[4];
+};
 
 // Parts of the workspace, in order of alignment.
 struct Parts {
-  Partial* chunks;  // [rows][C]
-  Partial* rows;    // [rows]: sum relative to the row's maximum
-  double* left;     // [B][C]: sums of max(p - q, 0)
-  int* pick;        // [T]: the rows' tokens; chains: [B] the first refused draft
+  Partial* chunks;      // [rows][C]
+  Quarters* quarters;   // [rows][C]
+  Partial* rows;        // [rows]: sum relative to the row's maximum
+  Quarters* left;       // [B][C]: sums of max(p - q, 0)
+  int* pick;            // [T]: the rows' tokens; chains: [B] the first refused draft
 };
 __host__ __device__ inline Parts parts_of(void* ws, int64_t T, int64_t rows, int64_t B, int C, bool chain) {
   Parts p;
   p.chunks = static_cast<Partial*>(ws);
-  p.rows = p.chunks + rows * C;
-  p.left = reinterpret_cast<double*>(p.rows + rows);
+  p.quarters = reinterpret_cast<Quarters*>(p.chunks + rows * C);
+  p.rows = reinterpret_cast<Partial*>(p.quarters + rows * C);
+  p.left = reinterpret_cast<Quarters*>(p.rows + rows);
   p.pick = reinterpret_cast<int*>(p.left + (chain ? B * C : 0));
   return p;
 }
 
-// 2^y for y <= 0 (NaN stays); below 2^-1100 zero.
-__device__ __forceinline__ double exp2_64(double y) {
-  y = y < -1100.0 ? -1100.0 : y;
-  const double n = rint(y), f = y - n;
-  double p = 0x1.e6063f7217bc6p-28;
-  p = fma(p, f, 0x1.b675bca4eeebbp-24);
-  p = fma(p, f, 0x1.62bfd47773353p-20);
-  p = fma(p, f, 0x1.ffcb54062e698p-17);
-  p = fma(p, f, 0x1.430913096fd9fp-13);
-  p = fma(p, f, 0x1.5d87fe9d7a584p-10);
-  p = fma(p, f, 0x1.3b2ab6fba1ddap-7);
-  p = fma(p, f, 0x1.c6b08d703ce49p-5);
-  p = fma(p, f, 0x1.ebfbdff82c598p-3);
-  p = fma(p, f, 0x1.62e42fefa3a19p-1);
-  p = fma(p, f, 1.0);
-  return __builtin_amdgcn_ldexp(p, (int)n);
-}
-
 constexpr double kLog2e = 1.4426950408889634;
 
-// A logit's weight relative to a finite maximum m; k = log2(e) / temperature.
-__device__ __forceinline__ double weight(float l, float m, double k) {
-  return l == kNegInf ? 0.0 : exp2_64(((double)l - (double)m) * k);
-}
+// Weights at one temperature, k = log2(e) / temperature: of a logit l relative to a
+// finite maximum m, 2^y with y = (l - m) k.  Adding 1.5 * 2^52 leaves the integer n
+// nearest to y in the low word; 2^(y - n) is the polynomial, 1.9e-14 off at most
+// (degree 10 3e-16, degree 8 1.1e-12) and 1 at 0, so that equal logits have whole
+// weights.  y stops at -1100, whose power is 0: masked logits weigh nothing (NaN
+// neither: they are looked for apart).
+struct Weights {
+  double k, low;
+  // in vector registers: an instruction takes one constant from scalar ones, and copying
+  // another each time would be two more
+  double whole = 0x1.8p52, c8 = 0x1.63ef969a64d3cp-20;
+  __device__ __forceinline__ explicit Weights(double k) : k(k), low(-1100.0 / k) {
+    asm("" : "+v"(whole));
+    asm("" : "+v"(c8));
+  }
+  __device__ __forceinline__ double operator()(float l, double m) const {
+    const double d = fmax((double)l - m, low), t = fma(d, k, whole), f = fma(d, k, whole - t);
+    double p = fma(0x1.b6571de2f2351p-24, f, c8);
+    p = fma(p, f, 0x1.ffcb76789860fp-17);
+    p = fma(p, f, 0x1.43088e257f341p-13);
+    p = fma(p, f, 0x1.5d87fe908f88ap-10);
+    p = fma(p, f, 0x1.3b2ab72b175eep-7);
+    p = fma(p, f, 0x1.c6b08d7044119p-5);
+    p = fma(p, f, 0x1.ebfbdff8149f2p-3);
+    p = fma(p, f, 0x1.62e42fefa39f7p-1);
+    p = fma(p, f, 1.0);
+    return __builtin_amdgcn_ldexp(p, (int)(uint32_t)__builtin_bit_cast(uint64_t, t));
+  }
+};
 
 template <int DT>  // 0 fp32, 1 bf16, 2 fp16
 struct Logits {
   static constexpr int E = DT == 0 ? 4 : 8;  // of 16 bytes
-  static constexpr int K = kChunk / (256 * E);
+  static constexpr int K = kChunk / (64 * E);
   static __device__ __forceinline__ float one(const void* base, int64_t at) {
     if constexpr (DT == 0) return static_cast<const float*>(base)[at];
     const uint16_t b = static_cast<const uint16_t*>(base)[at];
     if constexpr (DT == 1) return __builtin_bit_cast(float, (uint32_t)b << 16);
     return f16_bits_to_f32(b);
   }
-  // Logits x..x+E-1 of a row (rows lie at any multiple of the type's size); -inf past the end.
-  static __device__ __forceinline__ void load(const void* base, int64_t row_at, int64_t x, int64_t V, float (&l)[E]) {
-    if (x + E <= V) {
-      u4 w;
-      __builtin_memcpy(&w, static_cast<const char*>(base) + (row_at + x) * (DT == 0 ? 4 : 2), 16);
-      if constexpr (DT == 0) {
+  // Logits x..x+E-1 of a row (rows lie at any multiple of the type's size).
+  static __device__ __forceinline__ void load_whole(const void* base, int64_t at, float (&l)[E]) {
+    u4 w;
+    __builtin_memcpy(&w, static_cast<const char*>(base) + at * (DT == 0 ? 4 : 2), 16);
+    if constexpr (DT == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) l[i] = __builtin_bit_cast(float, (uint32_t)w[i]);
-      } else {
-        widen8(w, DT, l);
-      }
+      for (int i = 0; i < 4; ++i) l[i] = __builtin_bit_cast(float, (uint32_t)w[i]);
     } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) l[i] = x + i < V ? one(base, row_at + x + i) : kNegInf;
+      widen8(w, DT, l);
     }
+  }
+  // N neighbouring blocks of 64 E logits from x on, E a lane of each: chunk c is K of them,
+  // quarter q of it KQ.  -inf past the row's end.
+  template <int N>
+  static __device__ __forceinline__ void load_blocks(const void* base, int64_t row_at, int x, int V, int lane, float (&l)[N][E]) {
+    if (x + N * 64 * E <= V) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) load_whole(base, row_at + (x + lane * E) + 64 * i * E, l[i]);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = x + (64 * i + lane) * E;
+      if (at + E <= V) {
+        load_whole(base, row_at + at, l[i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) l[i][e] = one(base, row_at + min(at + e, V - 1));  // all in flight together
+#pragma unroll
+        for (int e = 0; e < E; ++e) l[i][e] = at + e < V ? l[i][e] : kNegInf;
+      }
+    }
+  }
+  static constexpr int KQ = K / 4;
+  static __device__ __forceinline__ void load_chunk(const void* base, int64_t row_at, int c, int64_t V, int lane,
+                                                    float (&l)[K][E]) {
+    load_blocks<K>(base, row_at, c * kChunk, (int)V, lane, l);
+  }
+  static __device__ __forceinline__ void load_quarter(const void* base, int64_t row_at, int c, int q, int64_t V, int lane,
+                                                      float (&l)[KQ][E]) {
+    load_blocks<KQ>(base, row_at, c * kChunk + q * (kChunk / 4), (int)V, lane, l);
   }
 };
 
-// log2(e) / temperature of sequence b; 0: the likeliest token alone.
+// log2(e) / temperature of sequence b (at least 2^-1000: its inverse is a number).
 __device__ __forceinline__ double sharpness(const VerifyArgs& a, int b) {
   const float t = a.temperature ? a.temperature[b] : 1.0f;
-  return t > 0.0f ? kLog2e / (double)t : 0.0;
+  return t > 0.0f ? fmax(kLog2e / (double)t, 0x1p-1000) : 1.0;
 }
 __device__ __forceinline__ bool is_greedy(const VerifyArgs& a, int b) {
   return a.temperature && !(a.temperature[b] > 0.0f);
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
+// Exchanges within a wave by DPP, a few cycles each where one through LDS takes 60 or
+// more: lane l gets the value of lane l - n of its row of 16 (0x110 + n), of the row
+// before's last lane (0x142), of lane 31 (0x143), or of lane l - 1 (0x138); `none`
+// where there is no such lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp(int none, int v) {
+  return __builtin_amdgcn_update_dpp(none, v, CTRL, ROWS, 0xf, false);
 }
-// The larger maximum; of equal ones the lower token.
-__device__ __forceinline__ void take_larger(float& m, int& top, float om, int otop) {
-  if (om > m || (om == m && otop < top)) {
-    m = om;
-    top = otop;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float none, float v) {
+  return __builtin_bit_cast(float, dpp<CTRL, ROWS>(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double none, double v) {
+  const uint64_t o = __builtin_bit_cast(uint64_t, none), u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = dpp<CTRL, ROWS>((int)o, (int)u), hi = dpp<CTRL, ROWS>((int)(o >> 32), (int)(u >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ int read_lane(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ float read_lane(float v, int l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+__device__ __forceinline__ double read_lane(double v, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)u, l), hi = __builtin_amdgcn_readlane((int)(u >> 32), l);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// op over the lanes up to each one; lane 63 has it of all.
+template <class T, class Op>
+__device__ __forceinline__ T wave_scan(T v, T none, Op op) {
+  v = op(v, dpp<0x111, 0xf>(none, v));
+  v = op(v, dpp<0x112, 0xf>(none, v));
+  v = op(v, dpp<0x114, 0xf>(none, v));
+  v = op(v, dpp<0x118, 0xf>(none, v));
+  v = op(v, dpp<0x142, 0xa>(none, v));
+  return op(v, dpp<0x143, 0xc>(none, v));
+}
+__device__ __forceinline__ double scan_sum(double v) {
+  return wave_scan(v, 0.0, [](double x, double y) { return x + y; });
+}
+__device__ __forceinline__ double wave_sum(double v) { return read_lane(scan_sum(v), 63); }
+// Four sums over the wave at once: lane l gets the one of s[l % 4].
+__device__ __forceinline__ double add_swapped(double v, bool halves) {
+  const u2 w = __builtin_bit_cast(u2, v);
+  uint32_t x[2], y[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    auto a = halves ? __builtin_amdgcn_permlane32_swap(w[i], w[i], false, false)
+                    : __builtin_amdgcn_permlane16_swap(w[i], w[i], false, false);
+    x[i] = a[0], y[i] = a[1];
   }
+  return __builtin_bit_cast(double, u2{x[0], x[1]}) + __builtin_bit_cast(double, u2{y[0], y[1]});
 }
-__device__ __forceinline__ void wave_larger(float& m, int& top) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) take_larger(m, top, __shfl_xor(m, d), __shfl_xor(top, d));
+__device__ __forceinline__ double wave_sum4(const double (&s)[4], int lane) {
+  const bool b0 = lane & 1, b1 = lane & 2;
+  const double x = (b0 ? s[1] : s[0]) + dpp<0xB1, 0xf>(0.0, b0 ? s[0] : s[1]);  // lane l ^ 1
+  const double y = (b0 ? s[3] : s[2]) + dpp<0xB1, 0xf>(0.0, b0 ? s[2] : s[3]);
+  double v = (b1 ? y : x) + dpp<0x4E, 0xf>(0.0, b1 ? x : y);  // lane l ^ 2
+  v += dpp<0x128, 0xf>(0.0, v);                               // rotated by 8 and by 4 within 16 lanes
+  v += dpp<0x124, 0xf>(0.0, v);
+  return add_swapped(add_swapped(v, false), true);
+}
+// A lane's v and those of the three others of its four lanes.
+__device__ __forceinline__ double quad_sum(double v) {
+  v += dpp<0xB1, 0xf>(0.0, v);
+  return v + dpp<0x4E, 0xf>(0.0, v);
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return read_lane(wave_scan(v, kNegInf, [](float x, float y) { return fmaxf(x, y); }), 63);
+}
+__device__ __forceinline__ int wave_min(int v) {
+  return read_lane(wave_scan(v, 0x7fffffff, [](int x, int y) { return min(x, y); }), 63);
 }
 __device__ __forceinline__ bool is_distribution(const Partial& p) {
   return fabsf(p.max) <= 3.4028235e38f && p.sum == p.sum;
 }
 
+// The nodes of sequence b that count.
+__device__ __forceinline__ Place nodes_of(const VerifyArgs& a, int b) {
+  if (!a.q_starts) return {b, b, 1};
+  const int q0 = max(a.q_starts[b], 0);
+  return {b, q0, (int)max((int64_t)0, min(min((int64_t)a.q_starts[b + 1], a.T) - q0, a.max_queries))};
+}
+
 template <int DT>
-__global__ __launch_bounds__(256) void verify_chunks_kernel(VerifyArgs a, int C) {
+__global__ __launch_bounds__(256) void verify_chunks_kernel(VerifyArgs a, int C, uint32_t waves) {
   using L = Logits<DT>;
-  __shared__ float s_max[4];
-  __shared__ int s_top[4];
-  __shared__ double s_sum[4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t r = blockIdx.x / (uint32_t)C;
-  const int c = (int)(blockIdx.x - r * C);
+  const int lane = threadIdx.x & 63;
+  const uint32_t id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (id >= waves) return;
+  const uint32_t r = id / (uint32_t)C;
+  const int c = (int)(id - r * C);
   const bool drafted = r >= a.T;
   const int t = (int)(drafted ? r - a.T : r);
+  float l[L::K][L::E];
+  L::load_chunk(drafted ? a.draft : a.logits, (int64_t)t * (drafted ? a.draft_stride : a.stride), c, a.V, lane, l);
   const Place pl = place_of(a.q_starts, a.B, a.T, t, lane);
   if (pl.b < 0) return;
   const bool greedy = is_greedy(a, pl.b);
   if (drafted && (greedy || t + 1 == pl.q0 + pl.n)) return;  // no token was drawn from it
-  const double k = sharpness(a, pl.b);
-  const void* base = drafted ? a.draft : a.logits;
-  const int64_t at = (int64_t)t * (drafted ? a.draft_stride : a.stride);
-  float l[L::K][L::E];
-#pragma unroll
-  for (int i = 0; i < L::K; ++i)
-    L::load(base, at, (int64_t)c * kChunk + (int64_t)(i * 256 + threadIdx.x) * L::E, a.V, l[i]);
-  float m = kNegInf;
-  int top = 0x7fffffff;
+  float m = kNegInf, mb[L::K];  // largest of the chunk, and of the lane's blocks
   bool odd = false;
 #pragma unroll
-  for (int i = 0; i < L::K; ++i)
+  for (int i = 0; i < L::K; ++i) {
+    mb[i] = kNegInf;
 #pragma unroll
-    for (int e = 0; e < L::E; ++e) {
-      const int x = c * kChunk + (i * 256 + (int)threadIdx.x) * L::E + e;
-      if (l[i][e] > m) {
-        m = l[i][e];
-        top = x;
-      }
-      odd |= l[i][e] != l[i][e];
+    for (int e = 0; e < L::E; e += 2) {
+      mb[i] = fmaxf(fmaxf(mb[i], l[i][e]), l[i][e + 1]);
+      odd |= __builtin_isunordered(l[i][e], l[i][e + 1]);
     }
-  wave_larger(m, top);
-  if (lane == 0) {
-    s_max[wave] = m;
-    s_top[wave] = top;
+    m = fmaxf(m, mb[i]);
   }
-  __syncthreads();
+  m = wave_max(m);
+  double sum = 0.0, quarter = 0.0;
+  int top = 0x7fffffff;
+  if (greedy) {
 #pragma unroll
-  for (int g = 0; g < 4; ++g) take_larger(m, top, s_max[g], s_top[g]);
-  double sum = odd ? __builtin_nan("") : 0.0;
-  if (!greedy && m != kNegInf) {
+    for (int i = L::K - 1; i >= 0; --i)
 #pragma unroll
-    for (int i = 0; i < L::K; ++i)
+      for (int e = L::E - 1; e >= 0; --e)
+        if (l[i][e] == m) top = c * kChunk + (64 * i + lane) * L::E + e;
+    top = wave_min(top);
+  } else if (m != kNegInf) {
+    const Weights weight(sharpness(a, pl.b));
+    const double md = m;
+    double s4[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-      for (int e = 0; e < L::E; ++e) sum += weight(l[i][e], m, k);
+    for (int i = 0; i < L::K; ++i) {
+      // all below 2^-72 of the largest (masked, say): nothing beside it
+      if (!__ballot(((double)mb[i] - md) * weight.k > -72.0)) continue;
+#pragma unroll
+      for (int e = 0; e < L::E; ++e) s4[i / L::KQ] += weight(l[i][e], md);
+    }
+    quarter = wave_sum4(s4, lane);
+    sum = quad_sum(quarter);
   }
-  sum = wave_sum(sum);
-  if (lane == 0) s_sum[wave] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const Parts p = parts_of(a.workspace, a.T, a.draft ? 2 * a.T : a.T, a.B, C, a.draft != nullptr);
-    p.chunks[(int64_t)r * C + c] = {s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3], m, top};
-  }
+  if (__ballot(odd)) sum = __builtin_nan("");
+  const Parts p = parts_of(a.workspace, a.T, a.draft ? 2 * a.T : a.T, a.B, C, a.draft != nullptr);
+  if (lane == 0) p.chunks[(int64_t)r * C + c] = {sum, m, top};
+  if (lane < 4) p.quarters[(int64_t)r * C + c].sum[lane] = quarter;
 }
 
 // A row's chunks joined, one wave.
-__device__ __forceinline__ Partial join_chunks(const Partial* ch, int C, double k, int lane) {
+__device__ __forceinline__ Partial join_chunks(const Partial* ch, int C, const Weights& weight, int lane) {
   Partial p{0.0, kNegInf, 0x7fffffff};
-  for (int c = lane; c < C; c += 64) take_larger(p.max, p.top, ch[c].max, ch[c].top);
-  wave_larger(p.max, p.top);
-  for (int c = lane; c < C; c += 64) p.sum += ch[c].sum == 0.0 ? 0.0 : ch[c].sum * weight(ch[c].max, p.max, k);
+  for (int c = lane; c < C; c += 64)
+    if (ch[c].max > p.max) {
+      p.max = ch[c].max;
+      p.top = ch[c].top;
+    }
+  const float m = wave_max(p.max);
+  p.top = wave_min(p.max == m ? p.top : 0x7fffffff);
+  p.max = m;
+  for (int c = lane; c < C; c += 64) p.sum += ch[c].sum == 0.0 ? 0.0 : ch[c].sum * weight(ch[c].max, p.max);
   p.sum = wave_sum(p.sum);
   return p;
-}
-
-__global__ __launch_bounds__(256) void verify_rows_kernel(VerifyArgs a, int C, uint32_t rows) {
-  const int lane = threadIdx.x & 63;
-  const uint32_t r = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (r >= rows) return;
-  const bool drafted = r >= a.T;
-  const int t = (int)(drafted ? r - a.T : r);
-  const Place pl = place_of(a.q_starts, a.B, a.T, t, lane);
-  if (pl.b < 0 || (drafted && (is_greedy(a, pl.b) || t + 1 == pl.q0 + pl.n))) return;
-  const Parts p = parts_of(a.workspace, a.T, a.draft ? 2 * a.T : a.T, a.B, C, a.draft != nullptr);
-  const Partial j = join_chunks(p.chunks + (int64_t)r * C, C, sharpness(a, pl.b), lane);
-  if (lane == 0) p.rows[r] = j;
 }
 
 // The first lane whose inclusive sum of s is above `limit`, or the last one with
 // s > 0 where none is (-1: no such lane); `before`: the sum of the lanes before it.
 __device__ __forceinline__ int wave_pick(double s, double limit, int lane, double* before, bool* hit, double* all) {
-  double run = s;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double up = __shfl_up(run, d);
-    run += lane >= d ? up : 0.0;
-  }
-  double ex = __shfl_up(run, 1);
-  if (lane == 0) ex = 0.0;
+  const double run = scan_sum(s), ex = dpp<0x138, 0xf>(0.0, run);
   const uint64_t above = __ballot(run > limit && s > 0.0), some = __ballot(s > 0.0);
   const int at = above ? __builtin_ctzll(above) : some ? 63 - __builtin_clzll(some) : -1;
   *hit = above != 0;
-  *before = __shfl(ex, max(at, 0));
-  *all = __shfl(run, 63);
+  *before = read_lane(ex, max(at, 0));
+  *all = read_lane(run, 63);
   return at;
 }
 
-struct PickLds {
-  double sums[64];
-  int token;
-};
-
-// The token in which u of the row's weights is passed: chunk_sum(c) the weights of a
-// chunk, weights(x, w) those of the E tokens from x on.  One workgroup; -1 if no
-// token has any weight.
-template <int E, int K, class ChunkSum, class Weights>
-__device__ __forceinline__ int pick_token(int C, double u, PickLds* lds, ChunkSum chunk_sum, Weights weights) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  // every wave finds the chunk
+// The token in which u of a row's weights is passed, one wave: chunk_sum(c) and
+// quarter_sum(c, q) are the weights of a chunk and of a quarter of it, weights(c, q, w)
+// those of the quarter's tokens.  -1 if no token has any.
+template <int KQ, int E, class ChunkSum, class QuarterSum, class Weights>
+__device__ __forceinline__ int pick_token(int C, double u, int lane, ChunkSum chunk_sum, QuarterSum quarter_sum,
+                                          Weights weights) {
   double total = 0.0;
   for (int c0 = 0; c0 < C; c0 += 64) total += wave_sum(c0 + lane < C ? chunk_sum(c0 + lane) : 0.0);
   const double limit = u * total;
-  double carry = 0.0, rest = 0.0;
+  double carry = 0.0, rest = 0.0, before, all;
+  bool hit;
   int chunk = -1;
   for (int c0 = 0; c0 < C; c0 += 64) {
-    double before, all;
-    bool hit;
     const int at = wave_pick(c0 + lane < C ? chunk_sum(c0 + lane) : 0.0, limit - carry, lane, &before, &hit, &all);
     if (at >= 0) {
       chunk = c0 + at;
@@ -265,99 +347,83 @@ __device__ __forceinline__ int pick_token(int C, double u, PickLds* lds, ChunkSu
     carry += all;
   }
   if (chunk < 0) return -1;
-  double s[K];
+  const int q = wave_pick(lane < 4 ? quarter_sum(chunk, lane) : 0.0, rest, lane, &before, &hit, &all);
+  if (q < 0) return -1;
+  rest -= before;
+  double w[KQ][E], s[KQ], sums = 0.0;
+  weights(chunk, q, w);
 #pragma unroll
-  for (int i = 0; i < K; ++i) {
-    double w[E];
-    weights((int64_t)chunk * kChunk + (int64_t)(i * 256 + threadIdx.x) * E, w);
+  for (int i = 0; i < KQ; ++i) {
     s[i] = 0.0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s[i] += w[e];
-    const double ws = wave_sum(s[i]);
-    if (lane == 0) lds->sums[4 * i + wave] = ws;
-  }
-  if (threadIdx.x == 0) lds->token = -1;
-  __syncthreads();
-  double before, all;
-  bool hit;
-  const int at = wave_pick(lane < 4 * K ? lds->sums[lane] : 0.0, rest, lane, &before, &hit, &all);
-  if (at >= 0 && at % 4 == wave) {
-    const int i0 = at / 4;
-    rest -= before;
-    double mine = 0.0;
-#pragma unroll
-    for (int i = 0; i < K; ++i) mine = i == i0 ? s[i] : mine;
-    const int l = wave_pick(mine, rest, lane, &before, &hit, &all);
-    if (lane == l) {
-      rest -= before;
-      const int64_t x = (int64_t)chunk * kChunk + (int64_t)(i0 * 256 + threadIdx.x) * E;
-      double w[E], run = 0.0;
-      weights(x, w);
-      int token = -1;
-      bool done = false;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        run += w[e];
-        if (!done && w[e] > 0.0) {
-          token = (int)x + e;
-          done = run > rest;
-        }
-      }
-      lds->token = token;
+    for (int e = 0; e < E; ++e) s[i] += w[i][e];
+    if (KQ > 1) {
+      const double ws = wave_sum(s[i]);
+      sums = lane == i ? ws : sums;
     }
   }
-  __syncthreads();
-  return lds->token;
-}
-
-template <int DT>
-__global__ __launch_bounds__(256) void verify_pick_kernel(VerifyArgs a, int C) {
-  using L = Logits<DT>;
-  __shared__ PickLds lds;
-  const int t = (int)blockIdx.x;
-  const Place pl = place_of(a.q_starts, a.B, a.T, t, threadIdx.x & 63);
-  if (pl.b < 0) return;
-  const Parts p = parts_of(a.workspace, a.T, a.T, a.B, C, false);
-  const double k = sharpness(a, pl.b);
-  const Partial row = p.rows[t];
-  int token = -1;
-  if (!is_distribution(row)) {
-  } else if (is_greedy(a, pl.b)) {
-    token = row.top;
-  } else {
-    const Partial* ch = p.chunks + (int64_t)t * C;
-    const int64_t at = (int64_t)t * a.stride;
-    token = pick_token<L::E, L::K>(
-        C, (double)a.uniform[t], &lds,
-        [&](int c) { return ch[c].sum == 0.0 ? 0.0 : ch[c].sum * weight(ch[c].max, row.max, k); },
-        [&](int64_t x, double(&w)[L::E]) {
-          float l[L::E];
-          L::load(a.logits, at, x, a.V, l);
+  int i0 = 0;  // block of all lanes
+  if (KQ > 1) {
+    i0 = wave_pick(sums, rest, lane, &before, &hit, &all);
+    if (i0 < 0) return -1;
+    rest -= before;
+  }
+  double mine = 0.0, own[E];
 #pragma unroll
-          for (int e = 0; e < L::E; ++e) w[e] = weight(l[e], row.max, k);
-        });
+  for (int i = 0; i < KQ; ++i) {
+    mine = i == i0 ? s[i] : mine;
+#pragma unroll
+    for (int e = 0; e < E; ++e) own[e] = i == 0 || i == i0 ? w[i][e] : own[e];
   }
-  if (threadIdx.x == 0) p.pick[t] = token;
+  const int l0 = wave_pick(mine, rest, lane, &before, &hit, &all);
+  if (l0 < 0) return -1;
+  rest -= before;
+  int token = -1;
+  double run = 0.0;
+  bool done = false;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    run += own[e];
+    if (!done && own[e] > 0.0) {
+      token = chunk * kChunk + (64 * (q * KQ + i0) + lane) * E + e;
+      done = run > rest;
+    }
+  }
+  return read_lane(token, l0);
 }
 
-// The way down the tree, a wave a sequence: the nodes' parents and tokens and the
-// rows' picks lie in LDS.
-__global__ __launch_bounds__(64) void verify_walk_kernel(VerifyArgs a, int C) {
-  extern __shared__ int nodes[];
-  const int lane = threadIdx.x, b = blockIdx.x, N = (int)a.max_queries;
-  const Parts p = parts_of(a.workspace, a.T, a.T, a.B, C, false);
-  int q0 = b, n = 1;
-  if (a.q_starts) {
-    q0 = max(a.q_starts[b], 0);
-    n = (int)max((int64_t)0, min(min((int64_t)a.q_starts[b + 1], a.T) - q0, a.max_queries));
-  }
-  int *parent = nodes, *token = nodes + N, *pick = nodes + 2 * N;
-  for (int i = lane; i < n; i += 64) {
-    parent[i] = a.parents ? a.parents[q0 + i] : i - 1;
-    token[i] = a.tokens[q0 + i];
-    pick[i] = p.pick[q0 + i];
-  }
-  __syncthreads();
+// A row's token from its own weights; row: its chunks joined.
+template <int DT>
+__device__ __forceinline__ int pick_of_row(const VerifyArgs& a, const Partial* ch, const Quarters* qs, int C, int64_t t,
+                                           const Partial& row, const Weights& weight, double u, int lane) {
+  using L = Logits<DT>;
+  return pick_token<L::KQ, L::E>(
+      C, u, lane, [&](int c) { return ch[c].sum == 0.0 ? 0.0 : ch[c].sum * weight(ch[c].max, row.max); },
+      [&](int c, int q) { return qs[c].sum[q] * weight(ch[c].max, row.max); },
+      [&](int c, int q, double(&w)[L::KQ][L::E]) {
+        float l[L::KQ][L::E];
+        L::load_quarter(a.logits, t * a.stride, c, q, a.V, lane, l);
+#pragma unroll
+        for (int i = 0; i < L::KQ; ++i)
+#pragma unroll
+          for (int e = 0; e < L::E; ++e) w[i][e] = weight(l[i][e], row.max);
+      });
+}
+
+// The token that row t of sequence b gives, one wave.
+template <int DT>
+__device__ __forceinline__ int token_of_row(const VerifyArgs& a, const Parts& p, int C, int b, int t, int lane) {
+  const Partial* ch = p.chunks + (int64_t)t * C;
+  const Weights weight(sharpness(a, b));
+  const Partial row = join_chunks(ch, C, weight, lane);
+  if (!is_distribution(row)) return -1;
+  return is_greedy(a, b) ? row.top : pick_of_row<DT>(a, ch, p.quarters + (int64_t)t * C, C, t, row, weight, (double)a.uniform[t], lane);
+}
+
+// The way down a tree of n nodes whose parents, tokens and rows' picks lie in LDS, one wave.
+__device__ __forceinline__ void walk(const VerifyArgs& a, int b, int n, const int* parent, const int* token,
+                                     const int* pick, int lane) {
+  const int N = (int)a.max_queries;
   int32_t *out = a.out_tokens + (int64_t)b * N, *path = a.path + (int64_t)b * N;
   int count = 0, node = 0;
   while (node < n) {
@@ -370,8 +436,8 @@ __global__ __launch_bounds__(64) void verify_walk_kernel(VerifyArgs a, int C) {
     int next = n;
     if (x >= 0)
       for (int i0 = node + 1; i0 < n; i0 += 64) {
-        const int i = i0 + lane;
-        const uint64_t yes = __ballot(i < n && parent[min(i, n - 1)] == node && token[min(i, n - 1)] == x);
+        const int i = min(i0 + lane, n - 1);
+        const uint64_t yes = __ballot(i0 + lane < n && parent[i] == node && token[i] == x);
         if (yes) {
           next = i0 + __builtin_ctzll(yes);
           break;
@@ -383,96 +449,169 @@ __global__ __launch_bounds__(64) void verify_walk_kernel(VerifyArgs a, int C) {
   if (lane == 0) a.counts[b] = count;
 }
 
-// Chains: the first refused draft of the sequence (n - 1: none), one workgroup.
+// Small trees: a workgroup a sequence, its waves take the rows in turn.
 template <int DT>
-__device__ __forceinline__ int first_refused(const VerifyArgs& a, const Parts& p, int q0, int n, double k, bool greedy,
-                                             int* lds) {
-  if (threadIdx.x == 0) *lds = n - 1;
+__global__ __launch_bounds__(1024) void verify_tree_kernel(VerifyArgs a, int C) {
+  __shared__ int parent[kFewNodes], token[kFewNodes], pick[kFewNodes];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), b = blockIdx.x;
+  const Parts p = parts_of(a.workspace, a.T, a.T, a.B, C, false);
+  const Place pl = nodes_of(a, b);
+  if ((int)threadIdx.x < pl.n) {
+    parent[threadIdx.x] = a.parents ? a.parents[pl.q0 + threadIdx.x] : (int)threadIdx.x - 1;
+    token[threadIdx.x] = a.tokens[pl.q0 + threadIdx.x];
+  }
+  for (int i = wave; i < pl.n; i += blockDim.x / 64) {
+    const int x = token_of_row<DT>(a, p, C, b, pl.q0 + i, lane);
+    if (lane == 0) pick[i] = x;
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < n - 1; i += 256) {
-    const int r = q0 + i, x = a.tokens[r + 1];
-    const Partial pr = p.rows[r];
+  if (wave == 0) walk(a, b, pl.n, parent, token, pick, lane);
+}
+
+// Larger ones: a wave a row, then a wave a sequence.
+template <int DT>
+__global__ __launch_bounds__(256) void verify_pick_kernel(VerifyArgs a, int C) {
+  const int lane = threadIdx.x & 63;
+  const int t = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= a.T) return;
+  const Place pl = place_of(a.q_starts, a.B, a.T, t, lane);
+  if (pl.b < 0) return;
+  const Parts p = parts_of(a.workspace, a.T, a.T, a.B, C, false);
+  const int x = token_of_row<DT>(a, p, C, pl.b, t, lane);
+  if (lane == 0) p.pick[t] = x;
+}
+
+__global__ __launch_bounds__(64) void verify_walk_kernel(VerifyArgs a, int C) {
+  extern __shared__ int nodes[];
+  const int lane = threadIdx.x, b = blockIdx.x, N = (int)a.max_queries;
+  const Parts p = parts_of(a.workspace, a.T, a.T, a.B, C, false);
+  const Place pl = nodes_of(a, b);
+  int *parent = nodes, *token = nodes + N, *pick = nodes + 2 * N;
+  for (int i = lane; i < pl.n; i += 64) {
+    parent[i] = a.parents ? a.parents[pl.q0 + i] : i - 1;
+    token[i] = a.tokens[pl.q0 + i];
+    pick[i] = p.pick[pl.q0 + i];
+  }
+  __syncthreads();
+  walk(a, b, pl.n, parent, token, pick, lane);
+}
+
+// Chains of many nodes: their rows joined beforehand, a wave each.
+__global__ __launch_bounds__(256) void verify_rows_kernel(VerifyArgs a, int C, uint32_t rows) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t r = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (r >= rows) return;
+  const bool drafted = r >= a.T;
+  const int t = (int)(drafted ? r - a.T : r);
+  const Place pl = place_of(a.q_starts, a.B, a.T, t, lane);
+  if (pl.b < 0 || (drafted && (is_greedy(a, pl.b) || t + 1 == pl.q0 + pl.n))) return;
+  const Parts p = parts_of(a.workspace, a.T, rows, a.B, C, true);
+  const Partial j = join_chunks(p.chunks + (int64_t)r * C, C, Weights(sharpness(a, pl.b)), lane);
+  if (lane == 0) p.rows[r] = j;
+}
+
+// Weights max(p - q, 0) of the tokens whose logits are l and d; pr, qr: the rows' chunks joined.
+template <int K, int E>
+__device__ __forceinline__ void left_weights(const float (&l)[K][E], const float (&d)[K][E], const Partial& pr,
+                                             const Partial& qr, const Weights& weight, double (&w)[K][E]) {
+  const double ip = 1.0 / pr.sum, iq = 1.0 / qr.sum;
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      w[i][e] = fmax(weight(l[i][e], pr.max) * ip - weight(d[i][e], qr.max) * iq, 0.0);
+}
+
+// Chains: which draft is refused first, and the sums of what that leaves to take from.
+// Four chunks of a sequence's refused row a workgroup; every one finds that row for
+// itself.  JOIN: short chains, whose rows each workgroup joins too.
+template <int DT, bool JOIN>
+__global__ __launch_bounds__(256) void verify_left_kernel(VerifyArgs a, int C) {
+  using L = Logits<DT>;
+  __shared__ int stop;
+  __shared__ Partial joined[JOIN ? 2 * kFewDrafts : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int per = (C + 3) / 4, b = blockIdx.x / (uint32_t)per, c = (blockIdx.x % (uint32_t)per) * 4 + wave;
+  const Parts p = parts_of(a.workspace, a.T, 2 * a.T, a.B, C, true);
+  const Place pl = nodes_of(a, b);
+  if (pl.n == 0) return;
+  const bool greedy = is_greedy(a, b);
+  const Weights weight(sharpness(a, b));
+  // rows of a node: the target's, then the draft's
+  auto row_at = [&](int i, int drafted) -> const Partial& {
+    if constexpr (JOIN) return joined[2 * i + drafted];
+    return p.rows[(drafted ? a.T : 0) + pl.q0 + i];
+  };
+  if constexpr (JOIN) {
+    for (int i = wave; i < 2 * pl.n - 1; i += 4) {
+      if (i % 2 && greedy) continue;
+      const int64_t r = (i % 2 ? a.T : 0) + pl.q0 + i / 2;
+      const Partial j = join_chunks(p.chunks + r * C, C, weight, lane);
+      if (lane == 0) joined[i] = j;
+    }
+  }
+  if (threadIdx.x == 0) stop = pl.n - 1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < pl.n - 1; i += 256) {
+    const int64_t r = pl.q0 + i;
+    const int x = a.tokens[r + 1];
+    const Partial pr = row_at(i, 0);
     bool yes = is_distribution(pr);
     if (greedy) {
       yes &= x == pr.top;
     } else {
-      const Partial qr = p.rows[a.T + r];
+      const Partial qr = row_at(i, 1);
       yes &= is_distribution(qr) && x >= 0 && x < a.V;
       if (yes) {
-        const double pw = weight(Logits<DT>::one(a.logits, (int64_t)r * a.stride + x), pr.max, k) / pr.sum;
-        const double qw = weight(Logits<DT>::one(a.draft, (int64_t)r * a.draft_stride + x), qr.max, k) / qr.sum;
+        const double pw = weight(L::one(a.logits, r * a.stride + x), pr.max) / pr.sum;
+        const double qw = weight(L::one(a.draft, r * a.draft_stride + x), qr.max) / qr.sum;
         yes = (double)a.uniform[r + 1] * qw < pw;
       }
     }
-    if (!yes) atomicMin(lds, i);
+    if (!yes) atomicMin(&stop, i);
   }
   __syncthreads();
-  return *lds;
-}
-
-// Weights max(p - q, 0) of a row's tokens.
-template <int DT>
-__device__ __forceinline__ void left_weights(const VerifyArgs& a, int64_t r, int64_t x, const Partial& pr, const Partial& qr,
-                                             double k, double (&w)[Logits<DT>::E]) {
-  using L = Logits<DT>;
-  float l[L::E], d[L::E];
-  L::load(a.logits, r * a.stride, x, a.V, l);
-  L::load(a.draft, r * a.draft_stride, x, a.V, d);
-  const double ip = 1.0 / pr.sum, iq = 1.0 / qr.sum;
-#pragma unroll
-  for (int e = 0; e < L::E; ++e) w[e] = fmax(weight(l[e], pr.max, k) * ip - weight(d[e], qr.max, k) * iq, 0.0);
-}
-
-__device__ __forceinline__ Place chain_of(const VerifyArgs& a, int b) {
-  if (!a.q_starts) return {b, b, 1};
-  const int q0 = max(a.q_starts[b], 0);
-  return {b, q0, (int)max((int64_t)0, min(min((int64_t)a.q_starts[b + 1], a.T) - q0, a.max_queries))};
-}
-
-template <int DT>
-__global__ __launch_bounds__(256) void verify_left_kernel(VerifyArgs a, int C) {
-  using L = Logits<DT>;
-  __shared__ int stop;
-  __shared__ double s_sum[4];
-  const int b = blockIdx.x / (uint32_t)C, c = blockIdx.x % (uint32_t)C;
-  const Parts p = parts_of(a.workspace, a.T, 2 * a.T, a.B, C, true);
-  const Place pl = chain_of(a, b);
-  if (pl.n == 0) return;
-  const bool greedy = is_greedy(a, b);
-  const double k = sharpness(a, b);
-  const int j = first_refused<DT>(a, p, pl.q0, pl.n, k, greedy, &stop);
-  if (c == 0 && threadIdx.x == 0) p.pick[b] = j;
-  if (greedy || j == pl.n - 1) return;
+  const int j = stop;
+  const bool whole = greedy || j == pl.n - 1;
   const int64_t r = pl.q0 + j;
-  const Partial pr = p.rows[r], qr = p.rows[a.T + r];
-  double sum = 0.0;
-  if (is_distribution(pr) && is_distribution(qr)) {
-#pragma unroll
-    for (int i = 0; i < L::K; ++i) {
-      double w[L::E];
-      left_weights<DT>(a, r, (int64_t)c * kChunk + (int64_t)(i * 256 + threadIdx.x) * L::E, pr, qr, k, w);
-#pragma unroll
-      for (int e = 0; e < L::E; ++e) sum += w[e];
+  if (c == 0 && lane == 0) {
+    p.pick[b] = j;
+    if (JOIN) {
+      p.rows[r] = row_at(j, 0);
+      if (!whole) p.rows[a.T + r] = row_at(j, 1);
     }
   }
-  sum = wave_sum(sum);
-  if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) p.left[(int64_t)b * C + c] = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+  if (whole || c >= C) return;
+  const Partial pr = row_at(j, 0), qr = row_at(j, 1);
+  double s4[4] = {0.0, 0.0, 0.0, 0.0};
+  if (is_distribution(pr) && is_distribution(qr)) {
+    float l[L::K][L::E], d[L::K][L::E];
+    L::load_chunk(a.logits, r * a.stride, c, a.V, lane, l);
+    L::load_chunk(a.draft, r * a.draft_stride, c, a.V, lane, d);
+    double w[L::K][L::E];
+    left_weights(l, d, pr, qr, weight, w);
+#pragma unroll
+    for (int i = 0; i < L::K; ++i)
+#pragma unroll
+      for (int e = 0; e < L::E; ++e) s4[i / L::KQ] += w[i][e];
+  }
+  const double quarter = wave_sum4(s4, lane);
+  if (lane < 4) p.left[(int64_t)b * C + c].sum[lane] = quarter;
 }
 
+// The end of a chain: its last token and what is written, a wave a sequence.
 template <int DT>
-__global__ __launch_bounds__(256) void verify_end_kernel(VerifyArgs a, int C) {
+__global__ __launch_bounds__(64) void verify_end_kernel(VerifyArgs a, int C) {
   using L = Logits<DT>;
-  __shared__ PickLds lds;
-  const int b = blockIdx.x, N = (int)a.max_queries;
+  const int lane = threadIdx.x, b = blockIdx.x, N = (int)a.max_queries;
   const Parts p = parts_of(a.workspace, a.T, 2 * a.T, a.B, C, true);
-  const Place pl = chain_of(a, b);
+  const Place pl = nodes_of(a, b);
   int32_t *out = a.out_tokens + (int64_t)b * N, *path = a.path + (int64_t)b * N;
   int count = 0;
   if (pl.n > 0) {
     const bool greedy = is_greedy(a, b);
-    const double k = sharpness(a, b), u = (double)a.uniform[pl.q0];
+    const Weights weight(sharpness(a, b));
+    const double u = (double)a.uniform[pl.q0];
     const int j = p.pick[b];
     const int64_t r = pl.q0 + j;
     const Partial pr = p.rows[r];
@@ -485,50 +624,56 @@ __global__ __launch_bounds__(256) void verify_end_kernel(VerifyArgs a, int C) {
       if (!whole) {
         const Partial qr = p.rows[a.T + r];
         if (is_distribution(qr)) {
-          const double* left = p.left + (int64_t)b * C;
-          token = pick_token<L::E, L::K>(C, u, &lds, [&](int c) { return left[c]; },
-                                         [&](int64_t x, double(&w)[L::E]) { left_weights<DT>(a, r, x, pr, qr, k, w); });
-          whole = token < 0;  // nothing left over: the two are one
+          const Quarters* left = p.left + (int64_t)b * C;
+          token = pick_token<L::KQ, L::E>(
+              C, u, lane, [&](int c) { return left[c].sum[0] + left[c].sum[1] + left[c].sum[2] + left[c].sum[3]; },
+              [&](int c, int q) { return left[c].sum[q]; },
+              [&](int c, int q, double(&w)[L::KQ][L::E]) {
+                float l[L::KQ][L::E], d[L::KQ][L::E];
+                L::load_quarter(a.logits, r * a.stride, c, q, a.V, lane, l);
+                L::load_quarter(a.draft, r * a.draft_stride, c, q, a.V, lane, d);
+                left_weights(l, d, pr, qr, weight, w);
+              });
+          whole = token < 0;  // nothing is left: p and q are one
         }
       }
-      if (whole) {
-        const Partial* ch = p.chunks + r * C;
-        token = pick_token<L::E, L::K>(
-            C, u, &lds, [&](int c) { return ch[c].sum == 0.0 ? 0.0 : ch[c].sum * weight(ch[c].max, pr.max, k); },
-            [&](int64_t x, double(&w)[L::E]) {
-              float l[L::E];
-              L::load(a.logits, r * a.stride, x, a.V, l);
-#pragma unroll
-              for (int e = 0; e < L::E; ++e) w[e] = weight(l[e], pr.max, k);
-            });
-      }
+      if (whole) token = pick_of_row<DT>(a, p.chunks + r * C, p.quarters + r * C, C, r, pr, weight, u, lane);
     }
     count = j + 1;
-    for (int i = threadIdx.x; i < count; i += 256) {
+    for (int i = lane; i < count; i += 64) {
       out[i] = i < j ? a.tokens[pl.q0 + i + 1] : token;
       path[i] = i;
     }
   }
-  for (int i = count + threadIdx.x; i < N; i += 256) out[i] = path[i] = -1;
-  if (threadIdx.x == 0) a.counts[b] = count;
+  for (int i = count + lane; i < N; i += 64) out[i] = path[i] = -1;
+  if (lane == 0) a.counts[b] = count;
 }
 
 template <int DT>
 hipError_t launch_dt(const VerifyArgs& a, hipStream_t stream) {
   const int C = verify_chunks(a.V);
   const int64_t rows = a.draft ? 2 * a.T : a.T;
+  const size_t lds = 3 * a.max_queries * sizeof(int);
   if (rows == 0) {  // sequences without nodes
-    verify_walk_kernel<<<(unsigned)a.B, 64, 3 * a.max_queries * sizeof(int), stream>>>(a, C);
+    verify_walk_kernel<<<(unsigned)a.B, 64, lds, stream>>>(a, C);
     return hipGetLastError();
   }
-  verify_chunks_kernel<DT><<<(unsigned)(rows * C), 256, 0, stream>>>(a, C);
-  verify_rows_kernel<<<(unsigned)((rows + 3) / 4), 256, 0, stream>>>(a, C, (uint32_t)rows);
+  const uint32_t waves = (uint32_t)(rows * C);
+  verify_chunks_kernel<DT><<<(waves + 3) / 4, 256, 0, stream>>>(a, C, waves);
   if (a.draft) {
-    verify_left_kernel<DT><<<(unsigned)((int64_t)a.B * C), 256, 0, stream>>>(a, C);
-    verify_end_kernel<DT><<<(unsigned)a.B, 256, 0, stream>>>(a, C);
+    const unsigned grid = (unsigned)((int64_t)a.B * ((C + 3) / 4));
+    if (a.max_queries <= kFewDrafts) {
+      verify_left_kernel<DT, true><<<grid, 256, 0, stream>>>(a, C);
+    } else {
+      verify_rows_kernel<<<(unsigned)((rows + 3) / 4), 256, 0, stream>>>(a, C, (uint32_t)rows);
+      verify_left_kernel<DT, false><<<grid, 256, 0, stream>>>(a, C);
+    }
+    verify_end_kernel<DT><<<(unsigned)a.B, 64, 0, stream>>>(a, C);
+  } else if (a.max_queries <= kFewNodes) {
+    verify_tree_kernel<DT><<<(unsigned)a.B, 64 * (unsigned)(a.max_queries < 16 ? a.max_queries : 16), 0, stream>>>(a, C);
   } else {
-    verify_pick_kernel<DT><<<(unsigned)a.T, 256, 0, stream>>>(a, C);
-    verify_walk_kernel<<<(unsigned)a.B, 64, 3 * a.max_queries * sizeof(int), stream>>>(a, C);
+    verify_pick_kernel<DT><<<(unsigned)((a.T + 3) / 4), 256, 0, stream>>>(a, C);
+    verify_walk_kernel<<<(unsigned)a.B, 64, lds, stream>>>(a, C);
   }
   return hipGetLastError();
 }
