@@ -658,8 +658,8 @@ int wq_kv_append(const void* q, const void* k, const void* v, int dtype, int64_t
  *              a node's row (nodes from 64 * mask_words on are seen by none).  A node's
  *              own bit and those of its ancestors, as a rule; any mask is allowed
  * Where context_lens[b] is smaller than n, nodes whose token would lie before the
- * first do not exist.  max_context, max_queries, lse, workspace (its size and plan as for
- * wq_kv_attention with the same sizes) and errors as there; WQ_EINVAL also for a NULL
+ * first do not exist.  max_context, max_queries, lse, workspace (of
+ * wq_kv_tree_attention_workspace_bytes) and errors as there; WQ_EINVAL also for a NULL
  * mask, mask_words outside 1..65536 and max_queries above 64 * mask_words. */
 int wq_kv_tree_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D, int64_t q_stride,
                          const uint8_t* k_codes, const uint16_t* k_s_f16, const uint8_t* k_zpacked,
@@ -668,6 +668,11 @@ int wq_kv_tree_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, i
                          int64_t max_context, const int32_t* q_starts, int64_t max_queries, const uint64_t* tree_mask,
                          int mask_words, float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
                          void* stream);
+
+/* Workspace bytes of that call (0: none needed, or sizes it would refuse).
+ * Host-only. */
+size_t wq_kv_tree_attention_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size,
+                                            int64_t max_context, int64_t max_queries);
 
 /* Names the kernel instance and launch shape of that call (as wq_gemm_plan). */
 int wq_kv_tree_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size, int64_t max_context,
@@ -700,7 +705,7 @@ int wq_kv_tree_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int 
  *              but the root and then the one taken last; -1 behind.  A sequence
  *              without nodes: 0
  * Of each sequence the first max_queries (1..1024) nodes count.  Weights and sums are
- * 64-bit, in a fixed order.  Limits: V up to 2^24, 2^24 workgroups of 8192 logits.
+ * 64-bit, in a fixed order.  Limits: V up to 2^24, 2^26 chunks of 2048 logits of a row.
  *   workspace  wq_verify_drafts_workspace_bytes bytes, 256-byte aligned; as for
  *              wq_kv_attention.
  * WQ_EINVAL, WQ_EALIGN, WQ_EWORKSPACE as elsewhere; WQ_EUNSUPPORTED for draft_logits with

@@ -285,7 +285,9 @@ def test_tree_attention(lens, nq, Hq, Hkv, D, page, words, dtype, kind):
 @pytest.mark.parametrize("Hq,Hkv,D,nq,plan", [
     (64, 8, 64, 1, "HP=4, RT=1, PK=2"), (8, 8, 64, 4, "HP=4, RT=1, PK=4"), (14, 2, 64, 1, "HP=2, RT=1, PK=2"), (40, 8, 64, 2, "HP=2, RT=1, PK=1"),
     (48, 8, 64, 3, "HP=2, RT=2, PK=1"), (64, 8, 128, 1, "HP=2, RT=1, PK=2"), (18, 2, 128, 1, "HP=2, RT=1, PK=1"),
-    (15, 5, 128, 5, "HP=1, RT=1, PK=1"), (24, 8, 128, 7, "HP=1, RT=2, PK=1"), (40, 4, 256, 3, "HP=1, RT=1, PK=1")])
+    (15, 5, 128, 5, "HP=1, RT=1, PK=1"), (24, 8, 128, 7, "HP=1, RT=2, PK=1"), (40, 4, 256, 3, "HP=1, RT=1, PK=1"),
+    (64, 8, 128, 5, "kv_tree_kernel<D=128, RG=2"), (24, 2, 128, 9, "kv_tree_kernel<D=128, RG=4"), (32, 8, 64, 9, "kv_tree_kernel<D=64, RG=2"),
+    (16, 2, 64, 30, "kv_tree_kernel<D=64, RG=4"), (7, 1, 128, 43, "kv_tree_kernel<D=128, RG=4")])
 @pytest.mark.parametrize("page", [16, 64])
 def test_tree_attention_kernels_of_long_contexts(Hq, Hkv, D, nq, plan, page):
     """Every variant, its steps shared out: short and long contexts under room for a million tokens, a page gone."""
@@ -305,7 +307,8 @@ def test_tree_attention_kernels_of_long_contexts(Hq, Hkv, D, nq, plan, page):
     _check_rows(got, lse, want)
 
 
-@pytest.mark.parametrize("B,most,Hq,Hkv,D,page", [(66, 125, 8, 8, 128, 16), (37, 12, 160, 16, 128, 64), (64, 250, 4, 4, 64, 1), (86, 33, 18, 6, 64, 32)])
+@pytest.mark.parametrize("B,most,Hq,Hkv,D,page", [(66, 125, 8, 8, 128, 16), (37, 12, 160, 16, 128, 64), (64, 250, 4, 4, 64, 1), (86, 33, 18, 6, 64, 32),
+                                                  (300, 50, 1, 1, 128, 8), (40, 64, 8, 8, 64, 16)])
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_tree_attention_many_rows(B, most, Hq, Hkv, D, page, dtype):
     """The kernel for many rows: sequences of none to `most` nodes, more nodes than tokens, pages that are gone,
@@ -322,17 +325,18 @@ def test_tree_attention_many_rows(B, most, Hq, Hkv, D, page, dtype):
         table[b, gone] = [-1, S // page, 2 ** 31 - 1, -2 ** 31][b % 4]
     q = ref.values(Hq, (starts[-1] + 2, Hq, D), dtype)
     cut = min(250, table.shape[1] * page)
-    assert "kv_chunk_kernel" in wq.wq_kv_tree_attention_plan(q.shape[0], Hq, Hkv, D, B, page, cut, most)
+    assert "kv_tree_kernel" in wq.wq_kv_tree_attention_plan(q.shape[0], Hq, Hkv, D, B, page, cut, most)
     masks, mask = some_masks(B, nq, q.shape[0], 1, -(-most // 64), "any" if dtype == BF else "tree")
     want, used = tree_want(cache, q, table, page, lens, starts, masks, D ** -0.5, max_context=cut)
     got, lse = run_tree(cache.to_dev(used), q.cuda(), table, page, lens, starts, mask, max_context=cut, max_queries=most)
     _check_rows(got, lse, want)
 
 
-@pytest.mark.parametrize("Hq,Hkv,D,page,n", [(8, 2, 128, 16, 5), (64, 8, 64, 32, 7), (4, 1, 256, 64, 3), (8, 8, 128, 16, 140)])
+@pytest.mark.parametrize("Hq,Hkv,D,page,n", [(8, 2, 128, 16, 5), (16, 8, 64, 32, 7), (4, 1, 256, 64, 30), (8, 8, 128, 16, 32)])
 def test_a_chain_is_the_causal_attention_to_the_bit(Hq, Hkv, D, page, n):
-    """Masks of a chain give what wq_kv_attention gives, where one tile's mask is the other's."""
-    B = 70 if n > 100 else 3
+    """Masks of a chain give what wq_kv_attention gives where the two take the same walk (up to 32 rows of a KV head,
+    heads of 256)."""
+    B = 3
     lens = [n + 7 * b % 90 + b for b in range(B)]
     S = (sum(-(-x // page) for x in lens) + 1) * page
     cache = Cache(n, S, Hkv, D)
@@ -350,8 +354,8 @@ def test_a_chain_is_the_causal_attention_to_the_bit(Hq, Hkv, D, page, n):
 
 
 def test_tree_attention_long_contexts_are_split_and_joined():
-    for B, n, Hq, Hkv, D, page, nq in [(1, 9000, 8, 1, 128, 64, 6), (3, 4500, 4, 4, 64, 16, 1), (2, 5000, 4, 1, 256, 32, 3), (1, 7000, 16, 8, 128, 32, 12)]:
-        lens = [n - 1111 * b for b in range(B)]
+    for B, n, Hq, Hkv, D, page, nq in [(1, 9000, 8, 1, 128, 64, 6), (1, 9000, 8, 1, 128, 64, 9), (2, 7000, 20, 4, 64, 16, 40), (3, 4500, 16, 4, 64, 16, 12), (40, 2100, 8, 8, 128, 32, 40), (3, 4500, 4, 4, 64, 16, 1), (2, 5000, 4, 1, 256, 32, 3), (1, 7000, 16, 8, 128, 32, 12)]:
+        lens = [n - min(1111, n // B) * b for b in range(B)]
         say(wq.wq_kv_tree_attention_plan(B * nq, Hq, Hkv, D, B, page, n, nq))
         S = sum(-(-x // page) for x in lens) * page
         cache = Cache(n, S, Hkv, D)
@@ -360,7 +364,8 @@ def test_tree_attention_long_contexts_are_split_and_joined():
         starts = [nq * b for b in range(B + 1)]
         masks, mask = some_masks(n, [nq] * B, B * nq, 0, 1)
         want, _ = tree_want(cache, q, table, page, lens, starts, masks, D ** -0.5)
-        need = wq.wq_kv_attention_workspace_bytes(B * nq, Hq, Hkv, D, B, page, n, nq)
+        need = wq.wq_kv_tree_attention_workspace_bytes(B * nq, Hq, Hkv, D, B, page, n, nq)
+        assert need > 0
         ws = torch.full((max(need, 1),), 0xFF, dtype=torch.uint8, device="cuda")  # NaNs: no content is needed
         got, lse = run_tree(cache.to_dev(), q.cuda(), table, page, lens, starts, mask, max_context=n, workspace=ws, max_queries=nq)
         _check_rows(got, lse, want)

@@ -89,7 +89,7 @@ def test_tree_refusals():
     assert tree(mask=None) == tree(words=0) == tree(words=65537) == EINVAL and tree(mask=P(0x10004)) == EALIGN
     assert tree(T=80, starts=A, max_queries=65, nseq=1) == EINVAL  # more nodes than the mask has bits
     assert tree(max_context=64 * 16 + 1) == tree(max_queries=2) == tree(scale=0.0) == tree(out=None) == EINVAL
-    need = wq.wq_kv_attention_workspace_bytes(2, 8, 2, 128, 2, 16, 65536)
+    need = wq.wq_kv_tree_attention_workspace_bytes(2, 8, 2, 128, 2, 16, 65536)
     long = dict(S=1 << 20, width=4096, max_context=65536)
     assert need > 0 and tree(**long, ws=None) == tree(**long, wsb=need - 1) == EWS and tree(**long, ws=B, wsb=need) == EALIGN
     assert wq.wq_kv_tree_attention_plan(2, 8, 2, 128, 2, 16, 65536) == wq.wq_kv_attention_plan(2, 8, 2, 128, 2, 16, 65536) + ", tree masks"
@@ -105,13 +105,13 @@ def test_verify_refusals():
     assert verify(dtype=5) == verify(T=-1) == verify(V=0) == verify(stride=999) == verify(most=0) == verify(nseq=-1) == EINVAL
     assert verify(draft=A, ds=999, parents=None) == verify(starts=None) == EINVAL
     assert verify(draft=A, ds=1000) == verify(most=1025) == verify(V=2 ** 24 + 1, stride=2 ** 25) == EUNSUP
-    assert verify(T=2 ** 24) == verify(T=2 ** 23, draft=A, ds=1000, parents=None) == verify(T=2 ** 20, V=2 ** 18, stride=2 ** 18) == EUNSUP
+    assert verify(T=2 ** 26) == verify(T=2 ** 25, draft=A, ds=1000, parents=None) == verify(T=2 ** 20, V=2 ** 18, stride=2 ** 18) == EUNSUP
     need = wq.wq_verify_drafts_workspace_bytes(4, 1000, 2)
     both = wq.wq_verify_drafts_workspace_bytes(4, 1000, 2, drafts=True)
     assert 0 < need < both
     assert verify(ws=None) == verify(wsb=need - 1) == verify(draft=A, ds=1000, parents=None, wsb=both - 1) == EWS and verify(ws=B) == EALIGN
     assert wq.wq_verify_drafts_workspace_bytes(0, 1000, 2) == wq.wq_verify_drafts_workspace_bytes(4, 0, 2) == 0
-    assert wq.wq_verify_drafts_workspace_bytes(2 ** 23, 1000, 2, drafts=True) == 0
+    assert wq.wq_verify_drafts_workspace_bytes(2 ** 25, 1000, 2, drafts=True) == 0
 
 
 def test_keep_refusals():

@@ -62,7 +62,7 @@ EXPORTED = (
     "wq_kv_layout_bytes", "wq_kv_quantize", "wq_kv_dequant",
     "wq_qk_norm_rope", "wq_prompt_attention", "wq_kv_attention", "wq_kv_attention_workspace_bytes",
     "wq_kv_attention_plan",
-    "wq_kv_append", "wq_kv_tree_attention", "wq_kv_tree_attention_plan", "wq_verify_drafts",
+    "wq_kv_append", "wq_kv_tree_attention", "wq_kv_tree_attention_workspace_bytes", "wq_kv_tree_attention_plan", "wq_verify_drafts",
     "wq_verify_drafts_workspace_bytes", "wq_kv_keep",
     "wq_quantize_groups_scaled", "wq_scale_activations", "wq_channel_absmean",
     "wq_layout_bytes_mxfp4", "wq_quantize_mxfp4", "wq_pack_mxfp4", "wq_dequant_mxfp4",
@@ -127,6 +127,7 @@ def lib() -> ctypes.CDLL:
                              I64, P, I64, I, P, P, P, P, I64, I64, P]),
         "wq_kv_tree_attention": (I, [P, I, I64, I, I, I, I64, P, P, P, P, P, P, I64, I64, P, I64, I, P, I64, P, I64, P, I,
                                      F, P, P, P, SZ, P]),
+        "wq_kv_tree_attention_workspace_bytes": (SZ, [I64, I, I, I, I64, I, I64, I64]),
         "wq_kv_tree_attention_plan": (I, [I64, I, I, I, I64, I, I64, I64, ctypes.c_char_p, SZ]),
         "wq_verify_drafts": (I, [P, I, I64, I64, I64, P, I64, I64, P, I64, P, P, P, P, P, P, P, P, SZ, P]),
         "wq_verify_drafts_workspace_bytes": (SZ, [I64, I64, I64, I]),
@@ -805,6 +806,12 @@ def wq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: KVCache, v_cache: KV
     return q_out, k_out
 
 
+def wq_kv_tree_attention_workspace_bytes(T: int, Hq: int, Hkv: int, D: int, B: int, page_size: int, max_context: int,
+                                         max_queries: int = 1) -> int:
+    """As wq_kv_attention_workspace_bytes, for wq_kv_tree_attention."""
+    return int(lib().wq_kv_tree_attention_workspace_bytes(T, Hq, Hkv, D, B, page_size, max_context, min(max_queries, T)))
+
+
 def wq_kv_tree_attention_plan(T: int, Hq: int, Hkv: int, D: int, B: int, page_size: int, max_context: int,
                               max_queries: int = 1) -> str:
     buf = ctypes.create_string_buffer(256)
@@ -822,7 +829,7 @@ def wq_kv_tree_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, bl
     wq_kv_attention, but that a node sees, besides all tokens before its sequence's
     nodes, those nodes whose bit is set in its row of tree_mask, int64 [T][words] (bit
     j % 64 of word j // 64 for node j; its ancestors and itself, as a rule).  The other
-    arguments, the workspace (wq_kv_attention_workspace_bytes) and the result as there;
+    arguments, the workspace (wq_kv_tree_attention_workspace_bytes) and the result as there;
     max_queries may be 64 times the words at most (its default: all T, or that)."""
     qs = _heads("q", q)
     T, Hq, D = q.shape
@@ -850,7 +857,7 @@ def wq_kv_tree_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, bl
     with _on(dev, stream) as s:
         out, lse = _attn_out(q, out, lse)
         if workspace is None:
-            need = L.wq_kv_attention_workspace_bytes(T, Hq, Hkv, D, B, page_size, max_context, max_queries)
+            need = L.wq_kv_tree_attention_workspace_bytes(T, Hq, Hkv, D, B, page_size, max_context, max_queries)
             if need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())

@@ -657,7 +657,7 @@ int check_kv_call(wq::KvAttnArgs* to, const void* q, int dtype, int64_t T, int H
                   const uint16_t* v_s_f16, const uint8_t* v_zpacked, int64_t S, int64_t B, const int32_t* block_table,
                   int64_t table_width, int page_size, const int32_t* context_lens, int64_t max_context,
                   const int32_t* q_starts, int64_t max_queries, float scale, void* out, float* lse, void* workspace,
-                  size_t workspace_bytes) {
+                  size_t workspace_bytes, size_t (*bytes)(int, int, int, int, int64_t, int64_t)) {
   int st = check_kv_attn(dtype, T, Hq, Hkv, D, B, page_size, max_context, max_queries);
   if (st) return st;
   if (!good_scale(scale) || S <= 0 || S >= kMaxCount || table_width < 0 || table_width >= kMaxCount) return WQ_EINVAL;
@@ -673,8 +673,7 @@ int check_kv_call(wq::KvAttnArgs* to, const void* q, int dtype, int64_t T, int H
       !aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(q_starts, 4) || !aligned(out, 16) ||
       !aligned(lse, 4))
     return WQ_EALIGN;
-  const size_t need =
-      wq::kv_attn_workspace_bytes((int)B, Hq, Hkv, D, max_context, max_queries);
+  const size_t need = bytes((int)B, Hq, Hkv, D, max_context, max_queries);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return WQ_EWORKSPACE;
     if (!aligned(workspace, 256)) return WQ_EALIGN;
@@ -696,7 +695,7 @@ int wq_kv_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D,
   wq::KvAttnArgs a;
   const int st = check_kv_call(&a, q, dtype, T, Hq, Hkv, D, q_stride, k_codes, k_s_f16, k_zpacked, v_codes, v_s_f16,
                                v_zpacked, S, B, block_table, table_width, page_size, context_lens, max_context, q_starts,
-                               max_queries, scale, out, lse, workspace, workspace_bytes);
+                               max_queries, scale, out, lse, workspace, workspace_bytes, wq::kv_attn_workspace_bytes);
   if (st) return st < 0 ? st : WQ_OK;
   return hip_status(wq::launch_kv_attn(a, static_cast<hipStream_t>(stream)));
 }
@@ -767,6 +766,13 @@ int wq_kv_append(const void* q, const void* k, const void* v, int dtype, int64_t
   return hip_status(wq::launch_kv_append(a, static_cast<hipStream_t>(stream)));
 }
 
+size_t wq_kv_tree_attention_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size,
+                                            int64_t max_context, int64_t max_queries) {
+  if (check_kv_attn(WQ_BF16, T, Hq, Hkv, D, B, page_size, max_context, max_queries)) return 0;
+  if (T == 0 || B == 0 || max_queries == 0) return 0;
+  return wq::kv_tree_workspace_bytes((int)B, Hq, Hkv, D, max_context, max_queries);
+}
+
 int wq_kv_tree_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_size, int64_t max_context,
                               int64_t max_queries, char* buf, size_t buf_len) {
   if (!buf || buf_len == 0) return WQ_EINVAL;
@@ -793,7 +799,7 @@ int wq_kv_tree_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, i
   wq::KvAttnArgs a;
   st = check_kv_call(&a, q, dtype, T, Hq, Hkv, D, q_stride, k_codes, k_s_f16, k_zpacked, v_codes, v_s_f16, v_zpacked, S, B,
                      block_table, table_width, page_size, context_lens, max_context, q_starts, max_queries, scale, out, lse,
-                     workspace, workspace_bytes);
+                     workspace, workspace_bytes, wq::kv_tree_workspace_bytes);
   if (st) return st < 0 ? st : WQ_OK;
   a.tree = tree_mask;
   a.tree_words = mask_words;

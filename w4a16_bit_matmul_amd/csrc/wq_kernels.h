@@ -129,7 +129,8 @@ hipError_t launch_kv_attn(const KvAttnArgs& a, hipStream_t stream);
 constexpr int kChunkWaves = 4;
 hipError_t launch_kv_chunk(const KvAttnArgs& a, int64_t grid, int rtiles, hipStream_t stream);
 
-// The same for the nodes of draft trees (wq_kv_tree.hip): plans and workspaces as above.
+// The same for the nodes of draft trees (wq_kv_tree.hip).
+size_t kv_tree_workspace_bytes(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_queries);
 int describe_kv_tree(int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries, char* buf,
                      size_t len);
 hipError_t launch_kv_tree(const KvAttnArgs& a, hipStream_t stream);
