@@ -37,6 +37,38 @@ __device__ __forceinline__ float sum_over_halves(float v) {
   return __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
 }
 
+// Exchanges within a wave by DPP, a few cycles each where one through LDS takes 60 or
+// more: lane l gets the value of lane l - n of its row of 16 (0x110 + n), the same
+// rotated within the row (0x120 + n), of lane l ^ 1 (0xB1), l ^ 2 (0x4E) or of its mirror
+// image in eight (0x141), of the row before's last lane (0x142), of lane 31 (0x143), or of
+// lane l - 1 (0x138); `none` where there is no such lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp(int none, int v) {
+  return __builtin_amdgcn_update_dpp(none, v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float none, float v) {
+  return __builtin_bit_cast(float, dpp<CTRL, ROWS>(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double none, double v) {
+  const uint64_t o = __builtin_bit_cast(uint64_t, none), u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = dpp<CTRL, ROWS>((int)o, (int)u), hi = dpp<CTRL, ROWS>((int)(o >> 32), (int)(u >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// A lane's v and that of lane l ^ 32 (halves) or l ^ 16.
+__device__ __forceinline__ double add_swapped(double v, bool halves) {
+  const u2 w = __builtin_bit_cast(u2, v);
+  uint32_t x[2], y[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    auto a = halves ? __builtin_amdgcn_permlane32_swap(w[i], w[i], false, false)
+                    : __builtin_amdgcn_permlane16_swap(w[i], w[i], false, false);
+    x[i] = a[0], y[i] = a[1];
+  }
+  return __builtin_bit_cast(double, u2{x[0], x[1]}) + __builtin_bit_cast(double, u2{y[0], y[1]});
+}
+
 // The queries of sequence b: `all` of them from q0 on, the first n are computed.
 struct Queries {
   int q0, n, all;

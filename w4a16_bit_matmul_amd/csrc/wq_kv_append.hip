@@ -23,7 +23,12 @@
 // exchanges, a lane's codes are one word, and two blocks' zero-points a byte.  In the
 // half form a value's partner sits rot / 2 further on: the lane loads those eight
 // values too, from the line that its neighbour brings in, instead of exchanging
-// them.
+// them.  What the lines' second reading and the tables (four bytes of cosine and sine for
+// two of a value) cost is the way through the L1 cache, so a wave of a long prompt
+// takes two such runs, whose lanes have the same channels, with one reading of the
+// tables: 32517 tokens of 64 + 8 heads of 128 move 1.32 GB in 234 us, 5.6 TB/s (a copy
+// reaches 5.1); one run a wave takes 333.  A decode step of 64 tokens takes 4.0 us in a
+// replayed graph.
 #include "wq_attn.h"
 #include "wq_group.h"
 
@@ -59,24 +64,32 @@ __device__ __forceinline__ void scale8(float (&v)[8], float r, const uint16_t* w
   for (int i = 0; i < 8; ++i) v[i] = v[i] * r * y[i];
 }
 
-template <int DT, bool INTER>
+// U: runs of 512 values that a wave works through, whose loads are all issued before the
+// first is used; the lane's channels, and so its cosines and sines, are the same in each.
+template <int DT, bool INTER, int U>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, uint32_t q_units, uint32_t k_units,
                                                         uint32_t waves) {
   const int lane = threadIdx.x & 63;
   const uint32_t id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (id >= waves) return;
   const uint32_t units = q_units + 2 * k_units, t = id / units;
-  uint32_t u = id - t * units;
-  const bool isq = u < q_units, isv = u >= q_units + k_units;
-  u -= isq ? 0 : isv ? q_units + k_units : q_units;
+  uint32_t unit = id - t * units;
+  const bool isq = unit < q_units, isv = unit >= q_units + k_units;
+  unit -= isq ? 0 : isv ? q_units + k_units : q_units;
   const int D = a.D;
-  const int vals = (isq ? a.Hq : a.Hkv) * D;
-  const int v0 = min((int)(512 * u) + 8 * lane, vals - 8);  // past the end: real values, not stored
-  const bool active = (int)(512 * u) + 8 * lane < vals;
+  const int vals = (isq ? a.Hq : a.Hkv) * D, start = (int)(512 * U * unit) + 8 * lane;
+  const int half = a.rot / 2, e = start & (D - 1);  // the lane's channels e..e+7 of its heads
+  const bool turned = !isv && e < a.rot;
+  const int to_partner = INTER || !turned ? 0 : e < half ? half : -half;
   const uint16_t* x = isq ? a.q + (int64_t)t * a.q_stride : isv ? a.v + (int64_t)t * a.v_stride : a.k + (int64_t)t * a.k_stride;
-  const u4 raw = *reinterpret_cast<const u4*>(x + v0);
-  float y[8];
-  unpack8<DT>(raw, y);
+  u4 raw[U], partner[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    // past the end: the token's last head, not stored
+    const int v0 = start + 512 * u < vals ? start + 512 * u : vals - D + e;
+    raw[u] = *reinterpret_cast<const u4*>(x + v0);
+    if (!INTER) partner[u] = *reinterpret_cast<const u4*>(x + v0 + to_partner);
+  }
 
   const Place pl = place_of(a.q_starts, a.B, a.T, (int)t, lane);
   if (pl.b < 0) return;
@@ -84,89 +97,115 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, uint32_t
   const int64_t pos = a.positions ? (int64_t)a.positions[t] : token;
   if (pos < 0 || pos >= a.P) return;  // padding
 
-  u4 out = raw;
-  if (!isv) {
-    const int half = a.rot / 2, e = v0 & (D - 1);  // the lane's channels e..e+7 of its head
-    const uint16_t* w = isq ? a.q_weight : a.k_weight;
-    float r = 1.0f;
-    if (a.norm) {
-      double ss = 0.0;
+  const uint16_t* w = isq ? a.q_weight : a.k_weight;
+  f4 c[2] = {}, s[2] = {};
+  if (turned) {
+    const int at = INTER ? e / 2 : e < half ? e : e - half;
+    const float *cr = a.cos + pos * half + at, *sr = a.sin + pos * half + at;
+    c[0] = *reinterpret_cast<const f4*>(cr), s[0] = *reinterpret_cast<const f4*>(sr);
+    if (!INTER) c[1] = *reinterpret_cast<const f4*>(cr + 4), s[1] = *reinterpret_cast<const f4*>(sr + 4);
+  }
+  const int64_t row = isq ? -1 : cache_row(a.table, a.table_width, a.lg, a.pages, pl.b, token);
+  uint16_t* to = isq ? a.q_out + (int64_t)t * a.qo_stride : !isv && a.k_out ? a.k_out + (int64_t)t * a.ko_stride : nullptr;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += (double)y[i] * (double)y[i];
-      for (int m = 1; m < D / 8; m <<= 1) ss += __shfl_xor(ss, m);
-      r = 1.0f / sqrtf((float)(ss / D) + a.eps);
-      scale8<DT>(y, r, w ? w + e : nullptr);
-    }
-    if (e < a.rot) {
-      const float *cr = a.cos + pos * half, *sr = a.sin + pos * half;
-      if constexpr (INTER) {
-        const f4 c = *reinterpret_cast<const f4*>(cr + e / 2), s = *reinterpret_cast<const f4*>(sr + e / 2);
+  for (int u = 0; u < U; ++u) {
+    const int v0 = start + 512 * u;
+    const bool active = v0 < vals;
+    float y[8];
+    unpack8<DT>(raw[u], y);
+    if (!isv) {
+      float r = 1.0f;
+      if (a.norm) {
+        double ss = 0.0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = y[2 * i], q = y[2 * i + 1];
-          y[2 * i] = p * c[i] - q * s[i];
-          y[2 * i + 1] = q * c[i] + p * s[i];
-        }
-      } else {
-        const bool first = e < half;
-        const int pe = first ? e + half : e - half, at = first ? e : e - half;
-        float z[8];  // the partners
-        unpack8<DT>(*reinterpret_cast<const u4*>(x + v0 + (pe - e)), z);
-        if (a.norm) scale8<DT>(z, r, w ? w + pe : nullptr);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const f4 c = *reinterpret_cast<const f4*>(cr + at + 4 * h), s = *reinterpret_cast<const f4*>(sr + at + 4 * h);
+        for (int i = 0; i < 8; ++i) ss += (double)y[i] * (double)y[i];
+        ss += dpp<0xB1, 0xf>(0.0, ss);  // over the head's D / 8 lanes
+        ss += dpp<0x4E, 0xf>(0.0, ss);
+        ss += dpp<0x141, 0xf>(0.0, ss);
+        if (D > 64) ss += dpp<0x128, 0xf>(0.0, ss);
+        if (D > 128) ss = add_swapped(ss, false);
+        r = 1.0f / sqrtf((float)(ss / D) + a.eps);
+        scale8<DT>(y, r, w ? w + e : nullptr);
+      }
+      if (turned) {
+        if constexpr (INTER) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int j = 4 * h + i;
-            const float own = y[j] * c[i], other = z[j] * s[i];
-            y[j] = first ? own - other : own + other;
+            const float p = y[2 * i], q = y[2 * i + 1];
+            y[2 * i] = p * c[0][i] - q * s[0][i];
+            y[2 * i + 1] = q * c[0][i] + p * s[0][i];
+          }
+        } else {
+          float z[8];
+          unpack8<DT>(partner[u], z);
+          if (a.norm) scale8<DT>(z, r, w ? w + e + to_partner : nullptr);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float own = y[i] * c[i / 4][i % 4], other = z[i] * s[i / 4][i % 4];
+            y[i] = e < half ? own - other : own + other;
           }
         }
       }
+      const u4 out = pack8<DT>(y);
+      if (to && active) *reinterpret_cast<u4*>(to + v0) = out;
+      if (isq) continue;
+      unpack8<DT>(out, y);
     }
-    out = pack8<DT>(y);
-    uint16_t* to = isq ? a.q_out + (int64_t)t * a.qo_stride : a.k_out ? a.k_out + (int64_t)t * a.ko_stride : nullptr;
-    if (to && active) *reinterpret_cast<u4*>(to + v0) = out;
-    if (isq) return;
-    unpack8<DT>(out, y);
-  }
 
-  // a block of 128 values: 16 lanes
-  float lo = y[0], hi = y[0];
+    // a block of 128 values: 16 lanes
+    float lo = y[0], hi = y[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = fminf(lo, y[i]);
-    hi = fmaxf(hi, y[i]);
+    for (int i = 1; i < 8; ++i) {
+      lo = fminf(lo, y[i]);
+      hi = fmaxf(hi, y[i]);
+    }
+    lo = fminf(lo, dpp<0x128, 0xf>(lo, lo)), hi = fmaxf(hi, dpp<0x128, 0xf>(hi, hi));
+    lo = fminf(lo, dpp<0x124, 0xf>(lo, lo)), hi = fmaxf(hi, dpp<0x124, 0xf>(hi, hi));
+    lo = fminf(lo, dpp<0x122, 0xf>(lo, lo)), hi = fmaxf(hi, dpp<0x122, 0xf>(hi, hi));
+    lo = fminf(lo, dpp<0x121, 0xf>(lo, lo)), hi = fmaxf(hi, dpp<0x121, 0xf>(hi, hi));
+    const GroupParams p = group_params(lo, hi);
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) word |= encode(y[i], p) << (4 * nibble_pos(i));
+    uint32_t z = active ? (uint32_t)p.z : 0u;
+    z |= (uint32_t)__shfl_down((int)z, 16) << 4;  // the next block's beside it
+    if (row < 0 || !active) continue;
+    const int nb = vals / 128, blk = v0 / 128;
+    *reinterpret_cast<uint32_t*>((isv ? a.v_codes : a.k_codes) + row * (vals / 2) + v0 / 2) = word;
+    if ((lane & 15) == 0) (isv ? a.v_s : a.k_s)[row * nb + blk] = p.s_bits;
+    if ((lane & 31) == 0) (isv ? a.v_zp : a.k_zp)[row * ((nb + 1) / 2) + blk / 2] = (uint8_t)z;
   }
-#pragma unroll
-  for (int m = 1; m < 16; m <<= 1) {
-    lo = fminf(lo, __shfl_xor(lo, m));
-    hi = fmaxf(hi, __shfl_xor(hi, m));
-  }
-  const GroupParams p = group_params(lo, hi);
-  uint32_t word = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) word |= encode(y[i], p) << (4 * nibble_pos(i));
-  uint32_t z = active ? (uint32_t)p.z : 0u;
-  z |= (uint32_t)__shfl_down((int)z, 16) << 4;  // the next block's beside it
-
-  const int64_t row = cache_row(a.table, a.table_width, a.lg, a.pages, pl.b, token);
-  if (row < 0 || !active) return;
-  const int nb = vals / 128, blk = v0 / 128;
-  uint8_t* codes = (isv ? a.v_codes : a.k_codes) + row * (vals / 2);
-  *reinterpret_cast<uint32_t*>(codes + v0 / 2) = word;
-  if ((lane & 15) == 0) (isv ? a.v_s : a.k_s)[row * nb + blk] = p.s_bits;
-  if ((lane & 31) == 0) (isv ? a.v_zp : a.k_zp)[row * ((nb + 1) / 2) + blk / 2] = (uint8_t)z;
 }
 
 // Row len - n + path[j] of a sequence to row len - n + j, for its accepted nodes j.
-// A thread owns 16 bytes of codes, a scale or a zero-point byte of every row and
-// takes the nodes in order; path[j] >= j, so a row is read before any thread could
-// write it.  Latency bounds: eight rows are in flight at a time.
-__global__ __launch_bounds__(64) void kv_keep_kernel(KvKeepArgs a, int blocks) {
-  const int lane = threadIdx.x;
-  const int cb = blockIdx.x % blocks, bc = blockIdx.x / blocks, b = bc / 2;
+// A workgroup has 64 parts of a row (16 bytes of codes, or a scale or zero-point byte) of
+// one sequence and cache; its four waves take every fourth node, read what 64 nodes
+// need, meet, and write it.  path[j] >= j, so no row is written that later nodes
+// still have to read.  It is all latency: lengths and path, pages, rows, stores one
+// after the other, and each of them once for up to 64 nodes (up to 64 nodes of 200
+// sequences, 9 blocks a row: 9.8 us; eight nodes at a time in one wave 12.9).
+template <class T>
+__device__ __forceinline__ void move_rows(T* base, int64_t stride, int64_t to, int64_t from, int m, int wave, bool mine) {
+  constexpr int K = 16;
+  T v[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int j = wave + 4 * i;
+    const int64_t src = __shfl(from, j);
+    if (j < m && src >= 0 && mine) v[i] = base[src * stride];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int j = wave + 4 * i;
+    const int64_t dst = __shfl(to, j);
+    if (j < m && dst >= 0 && mine) base[dst * stride] = v[i];
+  }
+}
+
+__global__ __launch_bounds__(256) void kv_keep_kernel(KvKeepArgs a, int code_blocks, int blocks) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cb = blockIdx.x % (uint32_t)blocks, bc = blockIdx.x / (uint32_t)blocks, b = bc / 2;
   const bool isv = bc & 1;
   int q0 = b, n = 1;
   if (a.q_starts) {
@@ -175,11 +214,7 @@ __global__ __launch_bounds__(64) void kv_keep_kernel(KvKeepArgs a, int blocks) {
   }
   const int m = min(min(a.counts[b], a.width), n);
   const int64_t first = (int64_t)a.lens[b] - n;
-  const int nb = a.nb, c16 = 4 * nb, zb = (nb + 1) / 2;
-  const int item = cb * 64 + lane;
-  uint8_t* codes = isv ? a.v_codes : a.k_codes;
-  uint16_t* scales = isv ? a.v_s : a.k_s;
-  uint8_t* zeros = isv ? a.v_zp : a.k_zp;
+  const int nb = a.nb, zb = (nb + 1) / 2;
   for (int j0 = 0; j0 < m; j0 += 64) {
     // lane: the rows of node j0 + lane
     int64_t to = -1, from = -1;
@@ -192,38 +227,39 @@ __global__ __launch_bounds__(64) void kv_keep_kernel(KvKeepArgs a, int blocks) {
       }
     }
     if (to < 0 || from < 0) to = from = -1;
-    for (int i0 = 0; i0 < min(64, m - j0); i0 += 8) {
-      u4 v[8];
-      int64_t dst[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t src = __shfl(from, i0 + i);
-        dst[i] = __shfl(to, i0 + i);
-        if (src < 0) continue;
-        if (item < c16) v[i] = *reinterpret_cast<const u4*>(codes + src * (16 * c16) + 16 * item);
-        else if (item < c16 + nb) v[i][0] = scales[src * nb + (item - c16)];
-        else if (item < c16 + nb + zb) v[i][0] = zeros[src * zb + (item - c16 - nb)];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (dst[i] < 0) continue;
-        if (item < c16) *reinterpret_cast<u4*>(codes + dst[i] * (16 * c16) + 16 * item) = v[i];
-        else if (item < c16 + nb) scales[dst[i] * nb + (item - c16)] = (uint16_t)v[i][0];
-        else if (item < c16 + nb + zb) zeros[dst[i] * zb + (item - c16 - nb)] = (uint8_t)v[i][0];
-      }
+    const int most = min(64, m - j0);
+    if (cb < code_blocks) {
+      const int item = cb * 64 + lane;
+      move_rows(reinterpret_cast<u4*>(isv ? a.v_codes : a.k_codes) + item, 4 * nb, to, from, most, wave, item < 4 * nb);
+    } else if (cb < code_blocks + (nb + 63) / 64) {
+      const int item = (cb - code_blocks) * 64 + lane;
+      move_rows((isv ? a.v_s : a.k_s) + item, nb, to, from, most, wave, item < nb);
+    } else {
+      const int item = (cb - code_blocks - (nb + 63) / 64) * 64 + lane;
+      move_rows((isv ? a.v_zp : a.k_zp) + item, zb, to, from, most, wave, item < zb);
     }
   }
 }
 
-template <int DT>
-hipError_t launch_dt(const KvAppendArgs& a, hipStream_t stream) {
-  const uint32_t qu = a.q ? (uint32_t)(((int64_t)a.Hq * a.D + 511) / 512) : 0;
-  const uint32_t ku = (uint32_t)(((int64_t)a.Hkv * a.D + 511) / 512);
+template <int DT, int U>
+hipError_t launch_u(const KvAppendArgs& a, hipStream_t stream) {
+  const uint32_t qu = a.q ? (uint32_t)(((int64_t)a.Hq * a.D + 512 * U - 1) / (512 * U)) : 0;
+  const uint32_t ku = (uint32_t)(((int64_t)a.Hkv * a.D + 512 * U - 1) / (512 * U));
   const uint32_t waves = (uint32_t)a.T * (qu + 2 * ku);  // below 2^26 (checked by the caller)
   const unsigned grid = (waves + 3) / 4;
-  if (a.interleaved) kv_append_kernel<DT, true><<<grid, 256, 0, stream>>>(a, qu, ku, waves);
-  else kv_append_kernel<DT, false><<<grid, 256, 0, stream>>>(a, qu, ku, waves);
+  if (a.interleaved) kv_append_kernel<DT, true, U><<<grid, 256, 0, stream>>>(a, qu, ku, waves);
+  else kv_append_kernel<DT, false, U><<<grid, 256, 0, stream>>>(a, qu, ku, waves);
   return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_dt(const KvAppendArgs& a, hipStream_t stream) {
+  // two runs a wave once there are waves for the whole GPU, two rounds of them (64 + 8 heads of 128, one run and
+  // two: 64 tokens 4.0 and 5.0 us, 512 7.9 and 7.5, 1024 19.7 and 18.0, 8192 75 and 60; a prompt of
+  // 32517 333 and 234, 265 with four); with the norm, whose arithmetic bounds then, always one (32 + 4
+  // heads, 8192 tokens: 42.2 and 43.1 us)
+  return !a.norm && kv_append_waves(a.T, a.q ? a.Hq : 0, a.Hkv, a.D) >= 8192 ? launch_u<DT, 2>(a, stream)
+                                                                            : launch_u<DT, 1>(a, stream);
 }
 
 }  // namespace
@@ -236,11 +272,11 @@ hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t stream) {
   return a.dtype == 1 ? launch_dt<1>(a, stream) : launch_dt<2>(a, stream);
 }
 
-int kv_keep_blocks(int nb) { return (5 * nb + (nb + 1) / 2 + 63) / 64; }
+int kv_keep_blocks(int nb) { return (4 * nb + 63) / 64 + (nb + 63) / 64 + ((nb + 1) / 2 + 63) / 64; }
 
 hipError_t launch_kv_keep(const KvKeepArgs& a, hipStream_t stream) {
   const int blocks = kv_keep_blocks(a.nb);
-  kv_keep_kernel<<<(unsigned)(2 * a.B * blocks), 64, 0, stream>>>(a, blocks);
+  kv_keep_kernel<<<(unsigned)(2 * a.B * blocks), 256, 0, stream>>>(a, (4 * a.nb + 63) / 64, blocks);
   return hipGetLastError();
 }
 

@@ -155,24 +155,6 @@ __device__ __forceinline__ bool is_greedy(const VerifyArgs& a, int b) {
   return a.temperature && !(a.temperature[b] > 0.0f);
 }
 
-// Exchanges within a wave by DPP, a few cycles each where one through LDS takes 60 or
-// more: lane l gets the value of lane l - n of its row of 16 (0x110 + n), of the row
-// before's last lane (0x142), of lane 31 (0x143), or of lane l - 1 (0x138); `none`
-// where there is no such lane.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp(int none, int v) {
-  return __builtin_amdgcn_update_dpp(none, v, CTRL, ROWS, 0xf, false);
-}
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp(float none, float v) {
-  return __builtin_bit_cast(float, dpp<CTRL, ROWS>(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v)));
-}
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double dpp(double none, double v) {
-  const uint64_t o = __builtin_bit_cast(uint64_t, none), u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = dpp<CTRL, ROWS>((int)o, (int)u), hi = dpp<CTRL, ROWS>((int)(o >> 32), (int)(u >> 32));
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
 __device__ __forceinline__ int read_lane(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
 __device__ __forceinline__ float read_lane(float v, int l) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
@@ -197,17 +179,6 @@ __device__ __forceinline__ double scan_sum(double v) {
 }
 __device__ __forceinline__ double wave_sum(double v) { return read_lane(scan_sum(v), 63); }
 // Four sums over the wave at once: lane l gets the one of s[l % 4].
-__device__ __forceinline__ double add_swapped(double v, bool halves) {
-  const u2 w = __builtin_bit_cast(u2, v);
-  uint32_t x[2], y[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    auto a = halves ? __builtin_amdgcn_permlane32_swap(w[i], w[i], false, false)
-                    : __builtin_amdgcn_permlane16_swap(w[i], w[i], false, false);
-    x[i] = a[0], y[i] = a[1];
-  }
-  return __builtin_bit_cast(double, u2{x[0], x[1]}) + __builtin_bit_cast(double, u2{y[0], y[1]});
-}
 __device__ __forceinline__ double wave_sum4(const double (&s)[4], int lane) {
   const bool b0 = lane & 1, b1 = lane & 2;
   const double x = (b0 ? s[1] : s[0]) + dpp<0xB1, 0xf>(0.0, b0 ? s[0] : s[1]);  // lane l ^ 1
