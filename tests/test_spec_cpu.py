@@ -180,3 +180,34 @@ def test_the_plain_chain_has_the_targets_law():
         for y in range(3):
             hits[y] += q[x] * (1 - yes) * (got == y).mean()
     assert np.abs(hits - p).max() <= 2 / N  # a step of the grid in each of two factors
+
+
+def test_binding_takes_tensors_and_sizes_of_32_bits():
+    x = torch.zeros((2, 2, 128), dtype=torch.float16)
+    i = torch.zeros(2, dtype=torch.int32)
+    tb, cs, mask = torch.zeros((2, 4), dtype=torch.int32), torch.zeros((5, 64)), torch.zeros((2, 1), dtype=torch.int64)
+    c = wq.KVCache(torch.zeros((16, 128), dtype=torch.uint8), torch.zeros((16, 2), dtype=torch.float16),
+                   torch.zeros((16, 1), dtype=torch.uint8), 16, 256)
+    starts = torch.zeros(3, dtype=torch.int32)
+    for page in (2 ** 31, -2 ** 31 - 1, 2 ** 32 + 4):
+        for call in (lambda: wq.wq_kv_append(x, x, c, c, tb, i, cs, cs, page_size=page),
+                     lambda: wq.wq_kv_tree_attention(x, c, c, tb, i, mask, page_size=page),
+                     lambda: wq.wq_kv_keep(c, c, tb, i, tb, i, page_size=page, q_starts=starts)):
+            with pytest.raises(ValueError, match="page_size"):
+                call()
+    for page in (4.0, None, "4"):
+        with pytest.raises(TypeError):
+            wq.wq_kv_append(x, x, c, c, tb, i, cs, cs, page_size=page)
+    with pytest.raises(TypeError, match="context_lens must be a tensor"):
+        wq.wq_kv_append(x, x, c, c, tb, [1, 2], cs, cs, page_size=4)
+    with pytest.raises(TypeError, match="tree_mask must be a tensor"):
+        wq.wq_kv_tree_attention(x, c, c, tb, i, None, page_size=4)
+    with pytest.raises(TypeError, match="uniform must be a tensor"):
+        wq.wq_verify_drafts(cs[:2], i, 0.5)
+    with pytest.raises(TypeError):
+        wq.wq_verify_drafts(cs[:2], i, cs[:2, 0].contiguous(), max_queries="1")
+    with pytest.raises(TypeError, match="counts must be a tensor"):
+        wq.wq_kv_keep(c, c, tb, i, tb, None, page_size=4, q_starts=starts)
+    with pytest.raises(ValueError, match=r"positions must be a contiguous torch.int32 tensor of shape \(2,\) on cpu "
+                                         r"\(got torch.int64, shape \(2,\), on cpu\)"):
+        wq.wq_kv_append(x, x, c, c, tb, i, cs, cs, page_size=4, positions=i.long())

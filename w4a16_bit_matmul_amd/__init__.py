@@ -742,6 +742,44 @@ def wq_kv_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, block_t
 # ---- a step of speculative decoding over the INT4 KV cache -----------------------
 # A sequence's nodes are its last token and the tokens drafted after it: tokens
 # q_starts[b] .. q_starts[b+1] - 1 of a call and the last ones of its cached context.
+# Their kernels take a few microseconds where a step is small, less than checking up to
+# twenty tensors does in Python, so the checks, outputs and workspaces are compiled.
+
+_bound = None
+
+
+def _load_calls():
+    """The module with the compiled checks, its calls bound to the loaded libwq.so."""
+    global _bound
+    L = lib()
+    try:
+        from . import _calls as m
+    except ImportError as e:
+        raise ImportError(f"{e}: build it first (python __graft_entry__.py or python w4a16_bit_matmul_amd/_build.py)") from e
+    m.bind(*(ctypes.cast(getattr(L, "wq_" + f), ctypes.c_void_p).value for f in
+             ("kv_append", "kv_tree_attention", "kv_tree_attention_workspace_bytes", "verify_drafts",
+              "verify_drafts_workspace_bytes", "kv_keep")))
+    _bound = m
+    return m
+
+
+def _arrays(c: KVCache):
+    return c.codes, c.s, c.zpacked, c.S, c.hd
+
+
+def _step(name: str, device: torch.device, stream, *args):
+    """A compiled call on its tensors' device and stream; its result, or a WQError for its status."""
+    f = getattr(_bound or _load_calls(), name)
+    if device.type != "cuda":
+        r = f(*args, 0)  # refuses, by the first argument that is wrong
+    else:
+        with _on(device, stream) as s:
+            r = f(*args, s)
+    if type(r) is int:
+        _check(r, "wq_" + name)
+        return None
+    return r
+
 
 def wq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: KVCache, v_cache: KVCache, block_table: torch.Tensor,
                  context_lens: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, *, page_size: int,
@@ -760,50 +798,8 @@ def wq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: KVCache, v_cache: KV
     nothing of it is written, one without a page is not cached.  q_out may be q
     itself; k_out: False, True or a tensor (k itself).  Returns (q_out, k_out), None
     for what was not asked for."""
-    ks, vs = _heads("k", k), _heads("v", v, k, k.shape[0])
-    T, Hkv, D = k.shape
-    if v.shape[1] != Hkv:
-        raise ValueError(f"k has {Hkv} heads, v {v.shape[1]}")
-    S, hd = k_cache.S, k_cache.hd
-    if (v_cache.S, v_cache.hd) != (S, hd) or hd != Hkv * D:
-        raise ValueError(f"caches of {S} x {hd} and {v_cache.S} x {v_cache.hd} values, {Hkv} heads of {D}")
-    dev, dt = k.device, k.dtype
-    Hq, qs, qos, kos = Hkv, 0, 0, Hkv * D
-    if q is not None:
-        qs, Hq = _heads("q", q, k, T), q.shape[1]
-        qos = Hq * D
-    if q_out is not None:
-        if q is None or q_out.shape[1] != Hq:
-            raise ValueError("q_out must have the heads of q")
-        qos = _heads("q_out", q_out, q, T)
-    if isinstance(k_out, torch.Tensor):
-        kos = _heads("k_out", k_out, k, T)
-        if k_out.shape[1] != Hkv:
-            raise ValueError(f"k_out has {k_out.shape[1]} heads, expected {Hkv}")
-    P, half = cos.shape
-    c, n = _dev_array("cos", cos, torch.float32, (P, half), dev), _dev_array("sin", sin, torch.float32, (P, half), dev)
-    pos = None if positions is None else _dev_array("positions", positions, torch.int32, (T,), dev)
-    if not norm and (q_weight is not None or k_weight is not None):
-        raise ValueError("weights are the norm's: pass norm=True")
-    qw = None if q_weight is None else _dev_array("q_weight", q_weight, dt, (D,), dev)
-    kw = None if k_weight is None else _dev_array("k_weight", k_weight, dt, (D,), dev)
-    kv = _caches(k_cache, v_cache, dev)
-    B, width, table, lens = _pages(block_table, context_lens, dev)
-    starts = None if q_starts is None else _dev_array("q_starts", q_starts, torch.int32, (B + 1,), dev)
-    with _on(dev, stream) as s:
-        if q is not None and q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        if k_out is True:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        elif k_out is False:
-            k_out = None
-        st = (_lib or lib()).wq_kv_append(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), _DT16[dt], T, Hq, Hkv,
-                                          D, qs, ks, vs, 1 if norm else 0, qw, kw, eps, pos, c, n, P, 2 * half,
-                                          1 if interleaved else 0, *kv, S, B, table, width, page_size, lens, starts,
-                                          None if q is None else q_out.data_ptr(),
-                                          None if k_out is None else k_out.data_ptr(), qos, kos, s)
-    _check(st, "wq_kv_append")
-    return q_out, k_out
+    return _step("kv_append", k.device, stream, k, v, *_arrays(k_cache), *_arrays(v_cache), block_table, context_lens, cos, sin,
+                 page_size, q, q_starts, positions, norm, q_weight, k_weight, eps, interleaved, q_out, k_out)
 
 
 def wq_kv_tree_attention_workspace_bytes(T: int, Hq: int, Hkv: int, D: int, B: int, page_size: int, max_context: int,
@@ -831,54 +827,14 @@ def wq_kv_tree_attention(q: torch.Tensor, k_cache: KVCache, v_cache: KVCache, bl
     j % 64 of word j // 64 for node j; its ancestors and itself, as a rule).  The other
     arguments, the workspace (wq_kv_tree_attention_workspace_bytes) and the result as there;
     max_queries may be 64 times the words at most (its default: all T, or that)."""
-    qs = _heads("q", q)
-    T, Hq, D = q.shape
-    S, hd = k_cache.S, k_cache.hd
-    if (v_cache.S, v_cache.hd) != (S, hd) or hd % D != 0:
-        raise ValueError(f"caches of {S} x {hd} and {v_cache.S} x {v_cache.hd} values, heads of {D}")
-    Hkv = hd // D
-    dev, dt = q.device, q.dtype
-    kv = _caches(k_cache, v_cache, dev)
-    B, width, table, lens = _pages(block_table, context_lens, dev)
-    if tree_mask.dim() != 2:
-        raise ValueError("tree_mask must be [tokens][words]")
-    words = tree_mask.shape[1]
-    mask = _dev_array("tree_mask", tree_mask, torch.int64, (T, words), dev)
-    if q_starts is not None:
-        starts = _dev_array("q_starts", q_starts, torch.int32, (B + 1,), dev)
-        max_queries = min(T, 64 * words) if max_queries is None else min(max_queries, T)
-    else:
-        starts, max_queries = None, min(T, 1)
-    if max_context is None:
-        max_context = width * page_size
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    L = _lib or lib()
-    with _on(dev, stream) as s:
-        out, lse = _attn_out(q, out, lse)
-        if workspace is None:
-            need = L.wq_kv_tree_attention_workspace_bytes(T, Hq, Hkv, D, B, page_size, max_context, max_queries)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        st = L.wq_kv_tree_attention(q.data_ptr(), _DT16[dt], T, Hq, Hkv, D, qs, *kv, S, B, table, width, page_size, lens,
-                                    max_context, starts, max_queries, mask, words, D ** -0.5 if scale is None else scale,
-                                    out.data_ptr(), None if lse is None else lse.data_ptr(), ws, wsb, s)
-    _check(st, "wq_kv_tree_attention")
-    return out if lse is None else (out, lse)
+    return _step("kv_tree_attention", q.device, stream, q, *_arrays(k_cache), *_arrays(v_cache), block_table, context_lens,
+                 tree_mask, page_size, max_context, q_starts, max_queries, scale, out, lse, workspace)
 
 
 def wq_verify_drafts_workspace_bytes(T: int, V: int, B: int, drafts: bool = False) -> int:
     """Bytes of the workspace that wq_verify_drafts takes for these sizes (0: none
     needed, or sizes it would refuse); drafts: with draft_logits."""
     return int(lib().wq_verify_drafts_workspace_bytes(T, V, B, 1 if drafts else 0))
-
-
-def _rows(name: str, x: torch.Tensor) -> int:
-    """x is [T][V] with contiguous rows; its stride between them."""
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError(f"{name} must be [tokens][vocabulary] with contiguous rows (shape {tuple(x.shape)}, strides {x.stride()})")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
 
 
 def wq_verify_drafts(logits: torch.Tensor, tokens: torch.Tensor, uniform: torch.Tensor, *,
@@ -902,51 +858,8 @@ def wq_verify_drafts(logits: torch.Tensor, tokens: torch.Tensor, uniform: torch.
     accepted nodes behind the root and the token that follows them, the accepted nodes
     (root first), -1 behind, and int32 [B] their number; a row that is no distribution
     gives token -1."""
-    if logits.dtype not in _DT:
-        raise ValueError(f"logits must be float32, bfloat16 or float16 (got {logits.dtype})")
-    stride = _rows("logits", logits)
-    T, V = logits.shape
-    dev, dstride = logits.device, 0
-    if draft_logits is not None:
-        dstride = _rows("draft_logits", draft_logits)
-        if draft_logits.shape != logits.shape or draft_logits.dtype != logits.dtype or draft_logits.device != dev:
-            raise ValueError(f"draft_logits must be like logits (got {draft_logits.dtype}, shape {tuple(draft_logits.shape)}, "
-                             f"on {draft_logits.device})")
-    tok, u = _dev_array("tokens", tokens, torch.int32, (T,), dev), _dev_array("uniform", uniform, torch.float32, (T,), dev)
-    par = None if parents is None else _dev_array("parents", parents, torch.int32, (T,), dev)
-    if q_starts is None:
-        B, starts = T, None
-    else:
-        if q_starts.dim() != 1 or q_starts.numel() < 1:
-            raise ValueError("q_starts must hold B + 1 token numbers")
-        B = q_starts.numel() - 1
-        starts = _dev_array("q_starts", q_starts, torch.int32, (B + 1,), dev)
-    if max_queries is None:
-        max_queries = 1 if q_starts is None else min(max(T, 1), 1024)
-    temp = None if temperature is None else _dev_array("temperature", temperature, torch.float32, (B,), dev)
-    for name, t, shape in (("out_tokens", out_tokens, (B, max_queries)), ("path", path, (B, max_queries)), ("counts", counts, (B,))):
-        if t is not None:
-            _dev_array(name, t, torch.int32, shape, dev)
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    L = _lib or lib()
-    with _on(dev, stream) as s:
-        if out_tokens is None:
-            out_tokens = torch.empty((B, max_queries), dtype=torch.int32, device=dev)
-        if path is None:
-            path = torch.empty((B, max_queries), dtype=torch.int32, device=dev)
-        if counts is None:
-            counts = torch.empty((B,), dtype=torch.int32, device=dev)
-        if workspace is None:
-            need = L.wq_verify_drafts_workspace_bytes(T, V, B, 0 if draft_logits is None else 1)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        st = L.wq_verify_drafts(logits.data_ptr(), _DT[logits.dtype], T, V, stride,
-                                None if draft_logits is None else draft_logits.data_ptr(), dstride, B, starts, max_queries, tok,
-                                par, u, temp, out_tokens.data_ptr(), path.data_ptr(), counts.data_ptr(), ws, wsb, s)
-    _check(st, "wq_verify_drafts")
-    return out_tokens, path, counts
+    return _step("verify_drafts", logits.device, stream, logits, tokens, uniform, q_starts, max_queries, parents, draft_logits,
+                 temperature, out_tokens, path, counts, workspace)
 
 
 def wq_kv_keep(k_cache: KVCache, v_cache: KVCache, block_table: torch.Tensor, context_lens: torch.Tensor,
@@ -954,21 +867,8 @@ def wq_kv_keep(k_cache: KVCache, v_cache: KVCache, block_table: torch.Tensor, co
     """Moves the cache rows of accepted nodes together: the rows of sequence b's nodes
     path[b][0 .. counts[b] - 1] (int32, as wq_verify_drafts gives them) become those of its nodes
     0 .. counts[b] - 1.  context_lens still counts all of the nodes, and is not changed."""
-    dev, hd = k_cache.codes.device, k_cache.hd
-    if (v_cache.S, v_cache.hd) != (k_cache.S, hd):
-        raise ValueError(f"caches of {k_cache.S} x {hd} and {v_cache.S} x {v_cache.hd} values")
-    kv = _caches(k_cache, v_cache, dev)
-    B, width, table, lens = _pages(block_table, context_lens, dev)
-    starts = _dev_array("q_starts", q_starts, torch.int32, (B + 1,), dev)
-    if path.dim() != 2:
-        raise ValueError("path must be [sequences][nodes]")
-    p = _dev_array("path", path, torch.int32, (B, path.shape[1]), dev)
-    n = _dev_array("counts", counts, torch.int32, (B,), dev)
-    with _on(dev, stream) as s:
-        # (how many tokens the call had is on the device: all that q_starts names)
-        st = (_lib or lib()).wq_kv_keep(*kv, k_cache.S, hd, (1 << 31) - 1, B, table, width, page_size, lens, starts, p,
-                                        path.shape[1], n, s)
-    _check(st, "wq_kv_keep")
+    _step("kv_keep", k_cache.codes.device, stream, *_arrays(k_cache), *_arrays(v_cache), block_table, context_lens, path,
+          counts, page_size, q_starts)
 
 
 # ---- AWQ-style per-input-channel scaling ---------------------------------------

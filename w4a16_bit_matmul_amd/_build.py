@@ -9,6 +9,7 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libwq.so")
+CALLS = os.path.join(HERE, "_calls.so")  # the compiled part of the Python binding
 BUILD = os.path.join(HERE, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -53,11 +54,32 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_calls(verbose: bool) -> None:
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-fPIC", "-std=c++17", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{d}" for d in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                                      sysconfig.get_paths()["include"])),
+           os.path.join(CSRC, "wq_calls.cpp"), "-o", CALLS + ".tmp", "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("g++ failed for wq_calls.cpp")
+    os.replace(CALLS + ".tmp", CALLS)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = [os.path.join(CSRC, f) for f in PER_FILE]
     with ThreadPoolExecutor(max_workers=min(4, len(srcs))) as ex:
+        calls = ex.submit(_compile_calls, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        calls.result()
     tmp = OUT + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:
