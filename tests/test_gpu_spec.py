@@ -332,6 +332,44 @@ def test_tree_attention_many_rows(B, most, Hq, Hkv, D, page, dtype):
     _check_rows(got, lse, want)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,nodes,room,plan", [
+    (8, 8, 64, 4, 2 ** 20, "HP=4, RT=1, PK=4"), (8, 8, 64, 4, 1200, "HP=2, RT=1, PK=2"), (64, 8, 128, 2, 2 ** 20, "HP=2, RT=1, PK=1"),
+    (64, 8, 128, 2, 1200, "HP=1, RT=1, PK=1"), (24, 8, 128, 7, 1200, "RT=2"), (4, 1, 256, 30, 1200, "kv_attn_kernel<D=256"),
+    (64, 8, 128, 8, 2 ** 20, "D=128, RG=2"), (64, 8, 128, 16, 2 ** 20, "D=128, RG=4"), (16, 8, 64, 20, 1200, "D=64, RG=2"),
+    (28, 2, 64, 25, 1200, "D=64, RG=4")])
+@pytest.mark.parametrize("bad", [NAN, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_tree_attention_scales_of_other_branches(Hq, Hkv, D, nodes, room, plan, bad, dtype):
+    """A node whose cache scales are infinite or NaN reaches the rows that see it and no other: two branches from the
+    root by turns, the first of them bad in K, V or both, and a node that no row sees."""
+    B, page = 6, 16
+    lens = [nodes + x for x in (0, 3, 50, 200, 331, 1000)]
+    starts = [nodes * b for b in range(B + 1)]
+    S = (sum(-(-n // page) for n in lens) + 2) * page
+    cache = Cache(D + nodes, S, Hkv, D)
+    table = _tables(B, lens, page, S, width=room // page)
+    q = ref.values(Hq, (starts[-1], Hq, D), dtype)
+    # node i sees the root and the nodes of its parity, but for the last one, which only itself would
+    tree = [{j for j in range(i + 1) if (j == 0 or j % 2 == i % 2) and j != nodes - 1} for i in range(nodes)]
+    masks, mask = [tree] * B, torch.cat([spec_ref.mask_words(tree, 1)] * B)
+    assert plan in wq.wq_kv_tree_attention_plan(q.shape[0], Hq, Hkv, D, B, page, room, nodes)
+    want, used = tree_want(cache, q, table, page, lens, starts, masks, D ** -0.5)
+    for which in ((0,), (1,), (0, 1)):
+        dev = cache.to_dev(used)
+        hit = torch.tensor([any(j % 2 for j in s) for s in tree] * B)
+        for b in range(B):
+            for j in [j for j in range(nodes) if j % 2 or j == nodes - 1]:
+                at = lens[b] - nodes + j
+                for c in which:
+                    dev[c].s[table[b][at // page] * page + at % page] = bad
+        got, lse = run_tree(dev, q.cuda(), table, page, lens, starts, mask)
+        if 1 in which or math.isnan(bad):  # (a score of -inf has no weight)
+            assert not bool(torch.isfinite(got.cpu()[hit]).all(-1).any())
+        got[hit.cuda()], lse[hit.cuda()] = 7.0, 7.0
+        none = want[4] | hit[:, None]
+        _check_rows(got, lse, tuple(x.masked_fill(hit.view(-1, *[1] * (x.dim() - 1)), NAN) for x in want[:4]) + (none,))
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,page,n", [(8, 2, 128, 16, 5), (16, 8, 64, 32, 7), (4, 1, 256, 64, 30), (8, 8, 128, 16, 32)])
 def test_a_chain_is_the_causal_attention_to_the_bit(Hq, Hkv, D, page, n):
     """Masks of a chain give what wq_kv_attention gives where the two take the same walk (up to 32 rows of a KV head,

@@ -535,10 +535,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
                 v = n == 0 ? sc[t][g][n][i] * ks[i] : __builtin_fmaf(sc[t][g][n][i], ks[i], v);
               }
             }
+          uint32_t miss = 0;  // TREE: bit i: the row does not see token i of the tile
           if (masked) {
             if constexpr (TREE) {
-              // bit i: the row does not see token i of the tile
-              uint32_t miss = ~(uint32_t)tree_window(a, q0 + lim[t], tk - before) | gone;
+              miss = ~(uint32_t)tree_window(a, q0 + lim[t], tk - before) | gone;
               if (tk + 32 > t_end) miss |= 0xffffffffu << (t_end - tk);
               if (P32 && !ok) miss = 0xffffffffu;
 #pragma unroll
@@ -599,6 +599,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
 #pragma unroll
               for (int n = 0; n < NH; ++n) pf[t][n][4 * g + i] = (_Float16)((n == 0 ? w : w * up) * vs[n][i]);
             }
+          }
+          if (TREE && masked) {  // a weight of 0 times the scale of a node of another branch, which may be infinite or NaN
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int n = 0; n < NH; ++n)
+                if (miss >> (16 * (i / 4) + 4 * c + i % 4) & 1) pf[t][n][i] = (_Float16)0.0f;
           }
         }
         __builtin_amdgcn_sched_barrier(0);
