@@ -334,7 +334,7 @@ def test_tree_attention_many_rows(B, most, Hq, Hkv, D, page, dtype):
 
 @pytest.mark.parametrize("Hq,Hkv,D,nodes,room,plan", [
     (8, 8, 64, 4, 2 ** 20, "HP=4, RT=1, PK=4"), (8, 8, 64, 4, 1200, "HP=2, RT=1, PK=2"), (64, 8, 128, 2, 2 ** 20, "HP=2, RT=1, PK=1"),
-    (64, 8, 128, 2, 1200, "HP=1, RT=1, PK=1"), (24, 8, 128, 7, 1200, "RT=2"), (4, 1, 256, 30, 1200, "kv_attn_kernel<D=256"),
+    (64, 8, 128, 2, 1200, "HP=1, RT=1, PK=1"), (24, 8, 128, 7, 1200, "HP=1, RT=1"), (24, 8, 128, 7, 2 ** 20, "RT=2"), (48, 8, 64, 4, 1200, "HP=2, RT=1, PK=1"), (4, 1, 256, 30, 1200, "kv_attn_kernel<D=256"),
     (64, 8, 128, 8, 2 ** 20, "D=128, RG=2"), (64, 8, 128, 16, 2 ** 20, "D=128, RG=4"), (16, 8, 64, 20, 1200, "D=64, RG=2"),
     (28, 2, 64, 25, 1200, "D=64, RG=4")])
 @pytest.mark.parametrize("bad", [NAN, math.inf, -math.inf])

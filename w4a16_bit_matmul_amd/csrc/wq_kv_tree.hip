@@ -24,8 +24,6 @@
 // contexts long and of different lengths: all steps of all units are shared out
 // equally over two workgroups a CU, as in wq_kv_walk.h, and kv_tree_join_kernel joins the
 // units that end up in several.
-#include <stdio.h>
-
 #include "wq_kv_walk.h"
 
 namespace wq {
@@ -527,14 +525,18 @@ TreePlan plan_tree(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t m
   // 512 x 40 168-253 and 164-245).
   p.flat = B <= kMaxShared && steps > 1 && (units < 256 || (units < kShares && steps >= 16)) &&
            units * steps < (int64_t)1 << 31;  // (steps are counted in 32 bits)
-  // Fewer units and steps than that leave CUs idle or pieces small, and the walk with its tiles
-  // of 16 and 32 rows is faster (units x steps, this and the walk, us: heads of 128 8 x 3 13.3 and
-  // 12.9, 8 x 10 14.8 and 16.7, 32 x 5 16.9 and 15.6, 32 x 20 26 and 29, 128 x 10 29.9 and 23.0, 128 x 20
-  // 36.6 and 35.9, 128 x 40 54 and 64, 128 x 157 173 and 260; with 128 rows 32 x 20 32.9 and 30.5, 32 x 157
-  // 79 and 135; heads of 64 32 x 3 11.9 and 15.8, 128 x 5 21.6 and 19.6, 128 x 10 23 and 30).  Heads of
-  // 256 always take it: a tile would fill the LDS.
-  const bool much = units >= 256 || steps == 1 || units * steps >= (D == 64 ? 1024 : 1536) ||
-                    (D == 64 ? units <= 64 : units <= 8 && steps >= 10);
+  // Where units and steps are few, pieces are small or CUs idle, and the walk with its tiles of 16
+  // rows is faster (tiles x steps, this and the walk, us.  Heads of 128: 64 x 1 8.2 and 7.1, 512 x 1
+  // 9.4 and 8.4, 1024 x 1 9.8 and 12.5; 64 x 3 17 and 9.2, 512 x 8 31 and 20, 1024 x 8 35 and 29; 128 x 16 27 and
+  // 21, 512 x 16 35.5 and 31.5, 1024 x 16 46 and 43; 64 x 32 27 and 21, 256 x 32 34 and 36, 512 x 32 46 and 56, 1024 x
+  // 32 66 and 80; 32 x 63 27 and 25, 64 x 63 31 and 30, 128 x 63 38 and 41, 256 x 63 49 and 67.  Of 64: 64 x 1 6.6 and
+  // 7.8; 64 x 3 12.6 and 10.6, 512 x 3 17 and 11; 64 x 5 12.5 and 12.9, 128 x 8 14.2 and 17.0, 256 x 5 16.9 and
+  // 13.5, 512 x 8 20.7 and 18.7; 128 x 16 18.7 and 18.8, 256 x 16 21 and 24, 512 x 16 26 and 29).  Units for all
+  // CUs: this (heads of 128 2048 x 3 19 and 33, 2048 x 16 67 and 78; of 64 1024 x 3 11.2 and 14.1).  Heads of 256
+  // always take the walk: a tile would fill the LDS.
+  const int64_t tiles = (int64_t)B * Hkv * ((rows + 15) / 16);
+  const bool much = units >= 256 || (D == 64 ? steps == 1 || steps > 8 || (steps > 4 && tiles <= 128)
+                                             : steps == 1 ? tiles > 512 : steps >= 24 && tiles * steps > 4096);
   p.wide = rows > 32 && D != 256 && much;
   p.grid = !p.flat ? units : units * steps < kShares ? units * steps : kShares;
   return p;
@@ -560,7 +562,7 @@ hipError_t launch_tree(const KvAttnArgs& a, const TreePlan& p, hipStream_t strea
 size_t kv_tree_workspace_bytes(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_queries) {
   const TreePlan p = plan_tree(B, Hq, Hkv, D, max_context, max_queries);
   return p.wide ? (p.flat ? (size_t)2 * p.grid * (32 * p.RG) * (D + 2) * 4 : 0)
-                : kv_attn_workspace_bytes(B, Hq, Hkv, D, max_context, max_queries);
+                : walk_workspace_bytes(plan_kv(B, Hq, Hkv, D, max_context, max_queries, true), D);
 }
 
 int describe_kv_tree(int B, int Hq, int Hkv, int D, int page, int64_t max_context, int64_t max_queries, char* buf,
@@ -568,7 +570,7 @@ int describe_kv_tree(int B, int Hq, int Hkv, int D, int page, int64_t max_contex
   const TreePlan p = plan_tree(B, Hq, Hkv, D, max_context, max_queries);
   if (p.wide) return snprintf(buf, len, "kv_tree_kernel<D=%d, RG=%d> grid=%lld block=256 %s", D, p.RG, (long long)p.grid,
                     p.flat ? "shares" : "whole units");
-  const int n = describe_kv_attn(B, Hq, Hkv, D, page, max_context, max_queries, buf, len);
+  const int n = describe_walk(plan_kv(B, Hq, Hkv, D, max_context, max_queries, true), D, page, buf, len);
   if (n >= 0 && (size_t)n < len) snprintf(buf + n, len - n, ", tree masks");
   return n;
 }
@@ -579,7 +581,7 @@ hipError_t launch_kv_tree(const KvAttnArgs& a, hipStream_t stream) {
     if (a.D == 64) return t.RG == 2 ? launch_tree<64, 2>(a, t, stream) : launch_tree<64, 4>(a, t, stream);
     return t.RG == 2 ? launch_tree<128, 2>(a, t, stream) : launch_tree<128, 4>(a, t, stream);
   }
-  return launch_walk<true>(a, plan_kv(a.B, a.Hq, a.Hkv, a.D, a.max_context, a.max_queries), stream);
+  return launch_walk<true>(a, plan_kv(a.B, a.Hq, a.Hkv, a.D, a.max_context, a.max_queries, true), stream);
 }
 
 }  // namespace wq

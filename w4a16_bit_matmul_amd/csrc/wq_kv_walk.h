@@ -54,6 +54,8 @@
 // 9-16 rows of heads of 64 a wave takes half a line and another workgroup the other:
 // 16 contexts of 1-9K, 25 us and 5, half of the 25 for the second reading.
 #pragma once
+#include <stdio.h>
+
 #include "wq_attn.h"
 
 namespace wq {
@@ -80,7 +82,8 @@ struct KvPlan {
 
 // A unit is HP heads of one sequence and one tile of query rows; its steps are
 // the runs of 32 kWaves tokens that a workgroup's waves take together.
-KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_queries) {
+// tree: of a draft tree's nodes.
+KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_queries, bool tree) {
   KvPlan p;
   const int64_t G = Hq / Hkv, rows = max_queries * G;
   p.HP = p.PK = 1;
@@ -98,10 +101,18 @@ KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_q
   if (p.chunk) return p;
   // more than 16 rows: two tiles share the decoded codes (4 contexts of up to 4K
   // with 32 rows: 29 us, 32 with one; with heads of 256 two spill 432 bytes or more)
-  p.RT = rows <= 16 || D == 256 ? 1 : 2;
+  // Of trees only where codes are many.  A step is one tile's vector instructions after
+  // another's, so one tile a wave, in twice the workgroups, is faster until decoding them again
+  // bounds (us, one and two; tiles x steps, heads of 128: 16 x 3 9.1 and 13.3, 128 x 16 21 and 24,
+  // 128 x 32 27 and 27, 128 x 63 57 and 41, 256 x 16 23 and 29, 256 x 32 40 and 36, 512 x 8 20.4 and 21.0,
+  // 1024 x 3 19 and 19, 1024 x 8 32 and 29; of 64: 16 x 3 10.4 and 16.0, 256 x 32 30.6 and 31.6, 256 x 63 60
+  // and 49, 512 x 16 29 and 36, 1024 x 8 25 and 28).
+  const int64_t tiles = (int64_t)B * Hkv * ((rows + 15) / 16);
+  const int64_t steps = (max_context + 32 * kWaves - 1) / (32 * kWaves);
+  const bool few = tree && tiles <= 65536 / D && tiles * steps * D <= 1 << 19;
+  p.RT = rows <= 16 || D == 256 || few ? 1 : 2;
   p.rtiles = (int)((rows + 16 * p.RT - 1) / (16 * p.RT));
   p.urows = (int)(rows < 16 * p.RT ? rows : 16 * p.RT);
-  const int64_t steps = (max_context + 32 * kWaves - 1) / (32 * kWaves);
   // Whole 128-byte lines to a wave (two heads of 128; four of 64 if two of them share
   // a tile, for registers) once there is work for all CUs that way: 64 contexts of up
   // to 512 tokens 15.7 us, 16.7 without; of up to 8K 109 and 152, with heads of 64 in
@@ -110,7 +121,7 @@ KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_q
   p.HP = D == 64 ? 2 : 1;
   const int line = 256 / D;
   const int64_t full = (int64_t)B * (Hkv / line) * p.rtiles;
-  if (p.RT == 1 && (D == 128 || rows <= 8) && Hkv % line == 0 && (full >= 256 || full * steps >= 4096)) p.HP = line;
+  if (rows <= (D == 128 ? 16 : 8) && D != 256 && Hkv % line == 0 && (full >= 256 || full * steps >= 4096)) p.HP = line;
   while (2 * p.PK <= p.HP && 2 * p.PK * rows <= 16) p.PK *= 2;
   const int64_t units = (int64_t)B * (Hkv / p.HP) * p.rtiles;
   // Shares cost a joining kernel and a start for each unit that a workgroup takes
@@ -132,6 +143,12 @@ __device__ __forceinline__ uint32_t units_of(int nq, int G, int HG, int row_tile
 }
 __device__ __forceinline__ uint32_t steps_of(int len, int step) {
   return max((uint32_t)(len + step - 1) / (uint32_t)step, 1u);
+}
+
+size_t walk_workspace_bytes(const KvPlan& p, int D) { return p.flat ? (size_t)2 * p.grid * p.HP * p.urows * (D + 2) * 4 : 0; }
+int describe_walk(const KvPlan& p, int D, int page, char* buf, size_t len) {
+  return snprintf(buf, len, "kv_attn_kernel<D=%d, HP=%d, RT=%d, PK=%d, P32=%d> grid=%lld block=%d %s", D, p.HP, p.RT, p.PK,
+                  page % 32 == 0 ? 1 : 0, (long long)p.grid, 64 * kWaves, p.flat ? "shares" : "whole units");
 }
 
 // Equal shares of the steps of all units: with n workgroups and total = q n + r
