@@ -9,9 +9,9 @@
 // each row's lanes read the window of its mask that falls on the tile, one or two
 // 64-bit words, in place of a comparison of token numbers.
 //
-// Up to 32 query rows of a KV head (a row is a node and a head of the group) take
-// the walk of wq_kv_walk.h, where every wave decodes its own tiles.  A tree has more as a
-// rule, 8 nodes of 8 heads, say: then decoding and softmax bound, not the reading, and
+// Up to 32 query rows of a KV head (a row is a node and a head of the group), and
+// small calls, take the walk of wq_kv_walk.h, where every wave decodes its own tiles.
+// With more rows and long contexts decoding and softmax bound, not the reading, and
 // kv_tree_kernel below lets a workgroup of four waves decode each tile of 64 tokens
 // once for 64 or 128 rows.  The mathematics and the two products are those of
 // wq_kv_walk.h and wq_kv_chunk.hip: the integers c - z exactly in fp16, K's scale times
@@ -24,6 +24,12 @@
 // contexts long and of different lengths: all steps of all units are shared out
 // equally over two workgroups a CU, as in wq_kv_walk.h, and kv_tree_join_kernel joins the
 // units that end up in several.
+//
+// 48 trees of 5-16 nodes over 3-6K tokens, 64 / 8 heads of 128: 170 us and 14 for the
+// join (75 GFLOP, 440 TFLOP/s), matrix instructions 24 % and others 41 % of the
+// cycles; tiles decoded by each wave for itself, in the walk, took 260.  Four of
+// 100-120 nodes over 7-12K, 32 / 8 heads of 64: 97 us and 7.5, 18 % and 48 % (126 in the
+// walk).  One of 8 nodes over 308 tokens, in the walk: 9 us, all latency.
 #include "wq_kv_walk.h"
 
 namespace wq {
@@ -79,7 +85,11 @@ __global__ __launch_bounds__(256, 2) void kv_tree_kernel(KvAttnArgs a, int rtile
   const int turned = RG == 4 ? (wave + (blockIdx.x >> 8 & 1) * 2) % 4 : wave;
   const int group = turned % RG, part = turned / RG, tb0 = part * TB;
   const int G = a.Hq / a.Hkv;
-  const uint32_t wg = blockIdx.x;
+  // Neighbouring shares, the other heads of the same tokens as a rule, to one XCD and its L2: a
+  // head has half or a quarter of a cache line (us, so and as the workgroups are numbered: 32 trees of 8 nodes
+  // over 8K, heads of 128, 133 and 143, of 16 nodes over 8K 197 and 209, of heads of 64 93 and 100; 16 over 4K, heads of
+  // 64, 34.4 and 33.9).
+  const uint32_t wg = gridDim.x % 8 == 0 ? (blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8 : blockIdx.x;
   uint32_t at = 0, at_end = 1;  // this workgroup's steps, counted over all units
   if (flat) {
     const Shares sh = scan_shares(a, gridDim.x, a.Hkv, 32 * RG, kTreeStep, lane, shares);
