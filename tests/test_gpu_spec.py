@@ -3,6 +3,7 @@ INT4 cache against a definition that is fixed to the bit, attention of draft tre
 against a plain 64-bit implementation, verification token by token in 64 bits, the
 moving of accepted rows, and all of them run together."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -807,3 +808,39 @@ def test_steps_on_two_streams_at_once():
     s.synchronize()
     for u, v in zip(out, want[0][2:]):
         assert torch.equal(u, v)
+
+
+def test_steps_in_two_threads():
+    """Two threads, each with a loop and stream of its own and workspaces made for them, give what the loops give
+    alone; a call that is refused in one of them is an error there."""
+    want, loops = [], []
+    for seed in (1, 2):
+        lp = Loop([2500, 40], 5, page=32)
+        lp.fill(seed)
+        want.append([t.clone() for t in lp.step()])
+        lp.fill(seed)
+        loops.append(lp)
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            s, lp = torch.cuda.Stream(), loops[i]
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    lp.old.copy_(i32([2500, 40]))
+                    got = lp.step()
+                    with pytest.raises(ValueError, match="uniform"):
+                        wq.wq_verify_drafts(lp.logits, lp.tokens, lp.u[:-1])
+                    s.synchronize()
+                    for u, v in zip(got, want[i]):
+                        assert torch.equal(u, v)
+        except BaseException as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed[0]
