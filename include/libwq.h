@@ -682,8 +682,9 @@ int wq_kv_tree_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int 
 /* Drafted tokens against the target's distributions.  Row i of a sequence's logits is
  * what the target says after its node i; at temperature t > 0 that is p(x) = w(x) / sum w
  * with w(x) = exp((l(x) - max l) / t), and a token is taken from it with a number u in
- * [0, 1): the first x whose cumulated weight w(0) + .. + w(x) is above u sum w (the
- * last x with any weight where rounding leaves none).  At t = 0 (or a t that is not
+ * [0, 1): the first x whose cumulated weight w(0) + .. + w(x) is above u sum w (where
+ * rounding leaves none, the last x with any weight), u counted as 2^-60 at least: a number of 0
+ * takes no token that lies far below all others.  At t = 0 (or a t that is not
  * above 0) it is the likeliest token, the lowest of equals.  Logits of -inf have weight 0; a row
  * without a finite maximum, or with a NaN or +inf, is no distribution: it gives token -1.
  *   draft_logits NULL: the drafts are given tokens in a tree.  The root, node 0, is

@@ -4,7 +4,9 @@
 // A row of logits l at temperature t is the distribution p(x) = w(x) / sum w,
 // w(x) = exp((l(x) - max l) / t); at t = 0 it is its likeliest token.  A token is
 // taken from it with one number u in [0, 1): the first x whose cumulated weight is
-// above u sum w.
+// above u sum w.  u counts as 2^-60 at least, so that weights too small to add up, or
+// to be told from 0, decide nothing (32-bit generators give multiples of 2^-24 or so, and
+// with u = 0 the first weight would be taken, however far below the others).
 //   Trees of given tokens: every row's token is taken with its own u, and a drafted
 // token is accepted if it is what its parent's row took and the parent is accepted.
 // The answer is then what taking token after token from the target alone would have
@@ -65,6 +67,13 @@ __host__ __device__ inline Parts parts_of(void* ws, int64_t T, int64_t rows, int
 }
 
 constexpr double kLog2e = 1.4426950408889634;
+constexpr double kLeastU = 0x1p-60;
+// A chunk's blocks whose weights all lie below 2^kFar of its largest are left out of its sums:
+// 2048 of them are below 2^-49 of kLeastU.
+constexpr double kFar = -120.0;
+// The least factor between weights relative to a chunk's maximum and to the row's with which
+// the chunk is taken from: the largest of each block that its sums hold is then no subnormal.
+constexpr double kLeastFactor = 0x1p-900;
 
 // Weights at one temperature, k = log2(e) / temperature: of a logit l relative to a
 // finite maximum m, 2^y with y = (l - m) k.  Adding 1.5 * 2^52 leaves the integer n
@@ -258,8 +267,7 @@ __global__ __launch_bounds__(256) void verify_chunks_kernel(VerifyArgs a, int C,
     double s4[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
     for (int i = 0; i < L::K; ++i) {
-      // all below 2^-72 of the largest (masked, say): nothing beside it
-      if (!__ballot(((double)mb[i] - md) * weight.k > -72.0)) continue;
+      if (!__ballot(((double)mb[i] - md) * weight.k > kFar)) continue;  // nothing beside the largest (masked, say)
 #pragma unroll
       for (int e = 0; e < L::E; ++e) s4[i / L::KQ] += weight(l[i][e], md);
     }
@@ -308,7 +316,7 @@ __device__ __forceinline__ int pick_token(int C, double u, int lane, ChunkSum ch
                                           Weights weights) {
   double total = 0.0;
   for (int c0 = 0; c0 < C; c0 += 64) total += wave_sum(c0 + lane < C ? chunk_sum(c0 + lane) : 0.0);
-  const double limit = u * total;
+  const double limit = fmax(u, kLeastU) * total;
   double carry = 0.0, rest = 0.0, before, all;
   bool hit;
   int chunk = -1;
@@ -372,9 +380,13 @@ template <int DT>
 __device__ __forceinline__ int pick_of_row(const VerifyArgs& a, const Partial* ch, const Quarters* qs, int C, int64_t t,
                                            const Partial& row, const Weights& weight, double u, int lane) {
   using L = Logits<DT>;
+  auto factor = [&](int c) {
+    const double f = weight(ch[c].max, row.max);
+    return f < kLeastFactor ? 0.0 : f;
+  };
   return pick_token<L::KQ, L::E>(
-      C, u, lane, [&](int c) { return ch[c].sum == 0.0 ? 0.0 : ch[c].sum * weight(ch[c].max, row.max); },
-      [&](int c, int q) { return qs[c].sum[q] * weight(ch[c].max, row.max); },
+      C, u, lane, [&](int c) { return ch[c].sum == 0.0 ? 0.0 : ch[c].sum * factor(c); },
+      [&](int c, int q) { return qs[c].sum[q] * factor(c); },
       [&](int c, int q, double(&w)[L::KQ][L::E]) {
         float l[L::KQ][L::E];
         L::load_quarter(a.logits, t * a.stride, c, q, a.V, lane, l);
