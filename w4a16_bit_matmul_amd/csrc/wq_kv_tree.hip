@@ -195,8 +195,9 @@ __global__ __launch_bounds__(256, 2) void kv_tree_kernel(KvAttnArgs a, int rtile
       }
       if (j0 == 0) {
         float* mt = meta + buf * kTreeMeta + t0;
-        const float v = f16_bits_to_f32(x.vs);
-        mt[0] = x.ok ? f16_bits_to_f32(x.ks) : 0.0f;
+        const float k = f16_bits_to_f32(x.ks), v = f16_bits_to_f32(x.vs);
+        // (an infinite one as NaN: the score would be -inf where the product's sign is the other)
+        mt[0] = !x.ok ? 0.0f : fabsf(k) <= 65504.0f ? k : __builtin_nanf("");
         const bool finite = fabsf(v) <= 65504.0f;
         mt[kTreeTok] = x.ok && finite ? v : 0.0f;
         mt[2 * kTreeTok] = !x.ok ? kGone : finite ? scale_power(v) : kBad;

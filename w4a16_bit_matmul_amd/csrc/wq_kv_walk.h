@@ -474,7 +474,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attn_kernel(KvAttnArgs a, i
         const uint32_t sb = off ? 0u : (tile.s >> (16 * n)) & 0xffffu;
         const float sv = f16_bits_to_f32((uint16_t)sb);
         float* mn = meta + kMeta * n;
-        mn[lane] = sv;  // K's, then V's
+        // K's, then V's.  TREE: an infinite K scale as NaN, a score that every row that sees the token takes over
+        // (infinite, the score may be -inf and the token gone)
+        mn[lane] = TREE && lane < 32 && !(fabsf(sv) <= 65504.0f) ? __builtin_nanf("") : sv;
         const uint32_t z10 = z | 0x6400u, z6 = (z << 4) | 0x5400u;  // 1024 + z, 64 + z
         if (lane < 32) {
           *reinterpret_cast<u2*>(mn + 64 + 2 * ml) = u2{z10 * 0x00010001u, z6 * 0x00010001u};
