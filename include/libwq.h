@@ -707,7 +707,7 @@ int wq_kv_tree_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int 
  *              but the root and then the one taken last; -1 behind.  A sequence
  *              without nodes: 0
  * Of each sequence the first max_queries (1..1024) nodes count.  Weights and sums are
- * 64-bit, in a fixed order.  Limits: V up to 2^24, 2^26 chunks of 2048 logits of a row.
+ * 64-bit, in a fixed order.  Limits: V up to 2^24, 2^26 - 4 chunks of 2048 logits of a row.
  *   workspace  wq_verify_drafts_workspace_bytes bytes, 256-byte aligned; as for
  *              wq_kv_attention.
  * WQ_EINVAL, WQ_EALIGN, WQ_EWORKSPACE as elsewhere; WQ_EUNSUPPORTED for draft_logits with

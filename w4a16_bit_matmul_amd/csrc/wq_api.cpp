@@ -726,7 +726,7 @@ int check_verify(int64_t T, int64_t V, int64_t B, bool drafts) {
   if (V > (1 << 24)) return WQ_EUNSUPPORTED;
   const int64_t C = wq::verify_chunks(V);
   // workgroups of four chunks
-  return (drafts ? 2 : 1) * T >= 4 * kMaxGrid / C || B >= kMaxGrid / ((C + 3) / 4) ? WQ_EUNSUPPORTED : WQ_OK;
+  return (drafts ? 2 : 1) * T > 4 * (kMaxGrid - 1) / C || B >= kMaxGrid / ((C + 3) / 4) ? WQ_EUNSUPPORTED : WQ_OK;
 }
 
 }  // namespace
@@ -755,7 +755,7 @@ int wq_kv_append(const void* q, const void* k, const void* v, int dtype, int64_t
   if (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(positions, 4) || !aligned(q_weight, 16) ||
       !aligned(k_weight, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(q_starts, 4))
     return WQ_EALIGN;
-  if (wq::kv_append_waves(T, q ? Hq : 0, Hkv, D) >= 4 * kMaxGrid) return WQ_EUNSUPPORTED;
+  if (wq::kv_append_waves(T, q ? Hq : 0, Hkv, D) > 4 * (kMaxGrid - 1)) return WQ_EUNSUPPORTED;
   const wq::KvAppendArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
                            static_cast<const uint16_t*>(v), T, q_stride, k_stride, v_stride, dtype, Hq, Hkv, D, norm,
                            static_cast<const uint16_t*>(q_weight), static_cast<const uint16_t*>(k_weight), eps, positions,

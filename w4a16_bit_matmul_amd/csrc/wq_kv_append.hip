@@ -245,7 +245,7 @@ template <int DT, int U>
 hipError_t launch_u(const KvAppendArgs& a, hipStream_t stream) {
   const uint32_t qu = a.q ? (uint32_t)(((int64_t)a.Hq * a.D + 512 * U - 1) / (512 * U)) : 0;
   const uint32_t ku = (uint32_t)(((int64_t)a.Hkv * a.D + 512 * U - 1) / (512 * U));
-  const uint32_t waves = (uint32_t)a.T * (qu + 2 * ku);  // below 2^26 (checked by the caller)
+  const uint32_t waves = (uint32_t)a.T * (qu + 2 * ku);  // up to 2^26 - 4 (checked by the caller)
   const unsigned grid = (waves + 3) / 4;
   if (a.interleaved) kv_append_kernel<DT, true, U><<<grid, 256, 0, stream>>>(a, qu, ku, waves);
   else kv_append_kernel<DT, false, U><<<grid, 256, 0, stream>>>(a, qu, ku, waves);

@@ -641,6 +641,7 @@ hipError_t launch_dt(const VerifyArgs& a, hipStream_t stream) {
   const int C = verify_chunks(a.V);
   const int64_t rows = a.draft ? 2 * a.T : a.T;
   const size_t lds = 3 * a.max_queries * sizeof(int);
+  const unsigned tree_threads = 64 * (unsigned)(a.max_queries < 16 ? a.max_queries : 16);
   if (rows == 0) {  // sequences without nodes
     verify_walk_kernel<<<(unsigned)a.B, 64, lds, stream>>>(a, C);
     return hipGetLastError();
@@ -656,8 +657,8 @@ hipError_t launch_dt(const VerifyArgs& a, hipStream_t stream) {
       verify_left_kernel<DT, false><<<grid, 256, 0, stream>>>(a, C);
     }
     verify_end_kernel<DT><<<(unsigned)a.B, 64, 0, stream>>>(a, C);
-  } else if (a.max_queries <= kFewNodes) {
-    verify_tree_kernel<DT><<<(unsigned)a.B, 64 * (unsigned)(a.max_queries < 16 ? a.max_queries : 16), 0, stream>>>(a, C);
+  } else if (a.max_queries <= kFewNodes && (uint64_t)a.B * tree_threads < (uint64_t)1 << 32) {  // (threads of a grid)
+    verify_tree_kernel<DT><<<(unsigned)a.B, tree_threads, 0, stream>>>(a, C);
   } else {
     verify_pick_kernel<DT><<<(unsigned)((a.T + 3) / 4), 256, 0, stream>>>(a, C);
     verify_walk_kernel<<<(unsigned)a.B, 64, lds, stream>>>(a, C);
