@@ -54,7 +54,8 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _compile_calls(verbose: bool) -> None:
+def build_calls(verbose: bool = False) -> str:
+    """The compiled part of the Python binding, from torch's headers."""
     import sysconfig
 
     import torch
@@ -71,15 +72,15 @@ def _compile_calls(verbose: bool) -> None:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("g++ failed for wq_calls.cpp")
     os.replace(CALLS + ".tmp", CALLS)
+    return CALLS
 
 
 def build(verbose: bool = False) -> str:
+    """libwq.so.  hipcc is all that it takes: the C ABI is there without torch."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = [os.path.join(CSRC, f) for f in PER_FILE]
     with ThreadPoolExecutor(max_workers=min(4, len(srcs))) as ex:
-        calls = ex.submit(_compile_calls, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        calls.result()
     tmp = OUT + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:
@@ -91,3 +92,8 @@ def build(verbose: bool = False) -> str:
 
 if __name__ == "__main__":
     print(build(verbose=True))
+    import importlib.util
+    if importlib.util.find_spec("torch"):
+        print(build_calls(verbose=True))
+    else:
+        print("torch is not installed: the Python binding is left out", file=sys.stderr)
