@@ -82,7 +82,7 @@ struct KvPlan {
 
 // A unit is HP heads of one sequence and one tile of query rows; its steps are
 // the runs of 32 kWaves tokens that a workgroup's waves take together.
-// tree: of a draft tree's nodes.
+// tree: of a draft tree's nodes, which the walk of this file always takes.
 KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_queries, bool tree) {
   KvPlan p;
   const int64_t G = Hq / Hkv, rows = max_queries * G;
@@ -97,7 +97,7 @@ KvPlan plan_kv(int B, int Hq, int Hkv, int D, int64_t max_context, int64_t max_q
   // 789) and nearly all of their rows are used (64 sequences, 128 rows a head: 97 us
   // and 133; 72 rows: 91 and 75).  With heads of 256 (two sequences over 7-8K, 32 / 4
   // heads) 660 us and 588: decoded tiles of 128 KB leave it one workgroup a CU.
-  p.chunk = D != 256 && p.grid >= kShares && 5 * ((rows + 31) / 32) >= 16 * p.rtiles;
+  p.chunk = !tree && D != 256 && p.grid >= kShares && 5 * ((rows + 31) / 32) >= 16 * p.rtiles;
   if (p.chunk) return p;
   // more than 16 rows: two tiles share the decoded codes (4 contexts of up to 4K
   // with 32 rows: 29 us, 32 with one; with heads of 256 two spill 432 bytes or more)
