@@ -631,7 +631,8 @@ int wq_kv_attention_plan(int64_t T, int Hq, int Hkv, int D, int64_t B, int page_
  *   rounded to dtype: q_out, k_out.
  * Keys so rounded and the values v are quantized as wq_kv_quantize would, into the
  * token's cache row.  Every step is one correctly rounded fp32 operation (the mean of
- * squares the fp32 rounding of a 64-bit sum), so the cache's bytes follow from the
+ * squares the fp32 rounding of a 64-bit sum over D, which adds eight neighbouring squares in
+ * order, then neighbours' sums, pair by pair), so the cache's bytes follow from the
  * inputs; squares whose mean passes fp32's range (bf16 values from 2^64 on) give zeros.
  *   q, q_out   may both be NULL: keys and values alone (Hq still a multiple of Hkv)
  *   positions  device int32 [T], or NULL: the token's place in its sequence.  Outside

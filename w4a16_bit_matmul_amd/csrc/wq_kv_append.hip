@@ -10,9 +10,10 @@
 // The codes are whole numbers: whether a value lands on one side of a half or the
 // other hangs on its last bit, and on every operation before it.  So every step is
 // one correctly rounded fp32 operation (this file is compiled with
-// -ffp-contract=off), and the sum of squares, whose order would matter, is taken in
-// 64 bits: products of 16-bit values are exact there and 256 of them add up to
-// within 2^-45, so that its fp32 rounding does not depend on the order.  Keys are
+// -ffp-contract=off).  The sum of squares is taken in 64 bits, where products of 16-bit
+// values are exact and 256 of them add up to within 2^-45, and in one order, eight neighbouring
+// values and then neighbours' sums, pair by pair: near an fp32 midpoint 2^-45 too decides
+// how the mean rounds.  Keys are
 // rounded to 16 bits first so that the cache holds what wq_kv_quantize makes of the
 // rotated keys that a prompt's own attention reads (2^-9 of a value beside a step
 // of a fifteenth of the block's range).
