@@ -16,8 +16,8 @@
 // the last token one from p.
 //
 // Which token that is changes where a cumulated weight passes u sum w, so weights and
-// sums are 64-bit: with 100,000 tokens, 2^-24 of error in the sums would move one
-// pick in a few hundred, 2^-45 none in 10^8.  The 64-bit exponential is 2^f by a
+// sums are 64-bit: with 100,000 tokens, 2^-24 of error in the weights would move one
+// pick in a few hundred, their 2^-44.6 less than one in 10^8.  The 64-bit exponential is 2^f by a
 // polynomial on [-1/2, 1/2] (Chebyshev interpolation) times 2^n; 64-bit operations
 // have the rate of 32-bit ones here.
 //
@@ -77,10 +77,10 @@ constexpr double kLeastFactor = 0x1p-900;
 
 // Weights at one temperature, k = log2(e) / temperature: of a logit l relative to a
 // finite maximum m, 2^y with y = (l - m) k.  Adding 1.5 * 2^52 leaves the integer n
-// nearest to y in the low word; 2^(y - n) is the polynomial, 1.9e-14 off at most
-// (degree 10 3e-16, degree 8 1.1e-12) and 1 at 0, so that equal logits have whole
-// weights.  y stops at -1100, whose power is 0: masked logits weigh nothing (NaN
-// neither: they are looked for apart).
+// nearest to y in the low word; 2^(y - n) is the polynomial, 3.8e-14 of it off at most
+// (degree 10 3e-16, degree 8 1.1e-12): half of that is the interpolation's, as much comes of its
+// value at 0, set to 1 so that equal logits have whole weights.  y stops at -1100, whose power
+// is 0: masked logits weigh nothing (NaN neither: they are looked for apart).
 struct Weights {
   double k, low;
   // in vector registers: an instruction takes one constant from scalar ones, and copying
