@@ -27,7 +27,8 @@
 //
 // 48 trees of 5-16 nodes over 3-6K tokens, 64 / 8 heads of 128: 170 us and 14 for the
 // join (75 GFLOP, 440 TFLOP/s), matrix instructions 24 % and others 41 % of the
-// cycles; tiles decoded by each wave for itself, in the walk, took 260.  Four of
+// cycles (a wave issues 38 % of its time, waits for operands or at a tile's barrier 43 %, and
+// for the other wave of its SIMD 19 %); tiles decoded by each wave for itself, in the walk, took 260.  Four of
 // 100-120 nodes over 7-12K, 32 / 8 heads of 64: 97 us and 7.5, 18 % and 48 % (126 in the
 // walk).  One of 8 nodes over 308 tokens, in the walk: 9 us, all latency.
 #include "wq_kv_walk.h"
@@ -46,9 +47,11 @@ constexpr int kTreeTile = 2 * kTreeTok * D / 8;  // 16-byte chunks of a decoded 
 constexpr int kTreeMeta = 3 * kTreeTok;
 constexpr float kGone = 128.0f, kBad = 129.0f;
 
-// 16-byte chunk j of token t in a tile's row: the lanes that write or read
-// together (16 tokens of a chunk of K; 4 tokens of four chunks of V; four tokens,
-// four apart, as decoded) fall in different banks.
+// 16-byte chunk j of token t in a tile's row: the lanes that read together (16 tokens of
+// a chunk of K; 4 tokens of four chunks of V) fall in different banks.  Those that write
+// decoded chunks (two tokens, every fourth or second chunk of each) meet in pairs: 16 cycles an
+// instruction in place of 8, all of the kernel's bank conflicts, 8 % of its cycles with heads of 128 and
+// 5 % with heads of 64, beside other waves' work.
 template <int D>
 __device__ __forceinline__ int place(int t, int j) {
   return D == 64 ? j ^ ((t >> 1) & 7) : j ^ ((t & 3) << 2 | (t >> 2 & 3));
