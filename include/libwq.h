@@ -660,9 +660,9 @@ int wq_kv_append(const void* q, const void* k, const void* v, int dtype, int64_t
  *              own bit and those of its ancestors, as a rule; any mask is allowed
  * Where context_lens[b] is smaller than n, nodes whose token would lie before the
  * first do not exist.  A token whose cached scales are infinite or NaN, K's or V's, makes the
- * rows that see it infinite or NaN (a V scale, the values of its block), and no others.  max_context, max_queries, lse, workspace (of
- * wq_kv_tree_attention_workspace_bytes) and errors as there; WQ_EINVAL also for a NULL
- * mask, mask_words outside 1..65536 and max_queries above 64 * mask_words. */
+ * rows that see it infinite or NaN (a V scale, the values of its block), and no others.
+ * max_context, max_queries, lse, workspace (of wq_kv_tree_attention_workspace_bytes) and
+ * errors as there; WQ_EINVAL also for a NULL mask, mask_words outside 1..65536 and max_queries above 64 * mask_words. */
 int wq_kv_tree_attention(const void* q, int dtype, int64_t T, int Hq, int Hkv, int D, int64_t q_stride,
                          const uint8_t* k_codes, const uint16_t* k_s_f16, const uint8_t* k_zpacked,
                          const uint8_t* v_codes, const uint16_t* v_s_f16, const uint8_t* v_zpacked, int64_t S, int64_t B,

@@ -845,8 +845,8 @@ def wq_verify_drafts(logits: torch.Tensor, tokens: torch.Tensor, uniform: torch.
                      workspace: torch.Tensor | None = None, stream=None):
     """Drafted tokens against the target's distributions, logits [T][V] (float32, bf16
     or fp16; row i of a sequence after its node i), with random numbers uniform [T] in
-    [0, 1) (a token is taken as by 2^-60 at least).  tokens int32 [T]: the nodes' (a root's is not read).  Without draft_logits
-    the nodes form a tree of given tokens, parents int32 [T] (a node's parent among its
+    [0, 1) (a token is taken as by 2^-60 at least).  tokens int32 [T]: the nodes' (a root's
+    is not read).  Without draft_logits the nodes form a tree of given tokens, parents int32 [T] (a node's parent among its
     sequence's nodes; None: the one before): each row's token is taken with its own
     uniform, and a node is accepted if its token is what its accepted parent's row gave.  With
     draft_logits [T][V] they are a chain, each token drawn from the row before it at the
